@@ -49,13 +49,18 @@ enum {
   QUAROT_ERR_CUDA = 6         /* another CUDA runtime/driver error            */
 };
 
+/* 16-bit element types of the 8-bit entry points (their `dtype` argument). */
+enum { QUAROT_FP16 = 0, QUAROT_BF16 = 1 };
+
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* quarot_status_string(int status);
 
 /* ABI version: (major << 16) | minor.  1.1 adds, with every 1.0 entry point
  * unchanged: quarot_w4a4_gemm_plan, quarot_legacy_imma_probe,
  * quarot_rotate_quant_a8, quarot_w4a4_gemm_a8, quarot_rotate_quant_rowsum,
- * quarot_int4_rowsum and quarot_w4a4_gemm_rowsums. */
+ * quarot_int4_rowsum and quarot_w4a4_gemm_rowsums; and the 8-bit layer
+ * quarot_quant_fp8, quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8,
+ * quarot_fp8_gemm and quarot_fp8_gated_gemm. */
 int quarot_version(void);
 
 /* Synchronizes `stream`, then returns and clears the device error word of the
@@ -397,6 +402,96 @@ int quarot_decode_attn_asym(const void* q, const uint8_t* k_q, const void* k_s, 
                             const uint8_t* v_q, const void* v_s, const int16_t* v_z, int64_t B, int64_t Hq,
                             int64_t Hkv, int64_t d, int64_t T, int64_t T_max, float sm_scale, int unrotate_out,
                             void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The 8-bit layer.  W4A4 models keep some layers above four bits (the first
+ * and last blocks, the output head, the feed-forward's down projection); these
+ * entry points run such layers in e4m3 with a scale for each block of 128, and
+ * add and norm the residual stream between them.  The pages have no
+ * counterpart; the quantizer is that of [S] Stage 2b (symmetric, abs-max) on
+ * the e4m3 grid.
+ *
+ * The block quantizer: with m = max(max |v| over the block, 1e-12),
+ *   scale = m / 448,   code = e4m3(v * 448 / m)
+ * (fp32; code rounded to nearest, ties to even, an exact tie of the quotient
+ * included), so code * scale stands for v.  A block that holds an infinity or
+ * a NaN gets the scale NaN and NaN codes.  Blocks at the end of a row (and, for weights, of a
+ * column) hold what is left.
+ *
+ * Layouts:
+ *   token codes    uint8 [M, d] (e4m3), token scales fp32 [ceil(d / 128), M]:
+ *                  block-major, so the scales of one block lie side by side
+ *   weight codes   uint8 [N, K] (e4m3), weight scales fp32
+ *                  [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block
+ * d and K are multiples of 16, at most 2^20 (QUAROT_ERR_UNSUPPORTED otherwise);
+ * codes, 16-bit tensors and outputs are 16-byte aligned, scales 4-byte
+ * aligned, leading dimensions multiples of 8 (QUAROT_ERR_ALIGNMENT).  dtype is
+ * QUAROT_FP16 or QUAROT_BF16 (QUAROT_ERR_INVALID_ARG otherwise).  M == 0 or
+ * N == 0 is a no-op.  Outputs do not overlap inputs unless stated.  None of
+ * them needs a workspace; results do not depend on what else runs.
+ */
+
+/*
+ * quarot_quant_fp8 -- the block quantizer on tokens x [M, ld_x] (first d
+ * columns): q_out uint8 [M, d], scale_out fp32 [ceil(d / 128), M].
+ */
+int quarot_quant_fp8(const void* x, int dtype, int64_t M, int64_t d, int64_t ld_x, uint8_t* q_out, float* scale_out,
+                     void* stream);
+
+/*
+ * quarot_quant_fp8_block -- the block quantizer on a weight matrix w [N, ld_w]
+ * ([out, in], first K columns), 128 x 128 blocks: q_out uint8 [N, K],
+ * scale_out fp32 [ceil(N / 128), ceil(K / 128)].
+ */
+int quarot_quant_fp8_block(const void* w, int dtype, int64_t N, int64_t K, int64_t ld_w, uint8_t* q_out,
+                           float* scale_out, void* stream);
+
+/*
+ * quarot_add_rmsnorm_quant_fp8 -- residual addition, RMSNorm and the token
+ * quantizer in one pass.  For each row, in fp32:
+ *   h = rnd16(x + residual)          (h = x when residual is NULL)
+ *   r = sqrt(mean h^2 + eps)
+ *   codes and scales of h * weight by the block quantizer, the scales divided
+ *   by r: code * scale stands for h / r * weight.  (A common factor of the row
+ *   changes no code; the 1e-12 floor applies to h * weight.)
+ *   x, residual   [M, ld_x], [M, ld_r], first d columns; residual may be NULL
+ *   weight        [d], or NULL (its scale absorbed, [S] Stage 1a)
+ *   eps           > 0 and finite
+ *   residual_out  [M, ld_out], receives h, or NULL; may be x or residual
+ *                 itself (same pointer and leading dimension)
+ *   q_out, scale_out  as quarot_quant_fp8
+ * A mean square above the fp32 range gives r = inf and scales of 0.
+ */
+int quarot_add_rmsnorm_quant_fp8(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
+                                 int dtype, int64_t M, int64_t d, float eps, void* residual_out, int64_t ld_out,
+                                 uint8_t* q_out, float* scale_out, void* stream);
+
+/*
+ * quarot_fp8_gemm -- y = A W^T of block-scaled e4m3 operands:
+ *   y[i, j] = rnd16(sum_b a_scale[b, i] w_scale[j / 128, b]
+ *                         sum_{k in block b} a[i, k] w[j, k])
+ * Products of codes accumulate in fp32 on the tensor cores within a block of
+ * 128, blocks are scaled and summed in fp32, one rounding to dtype at the end.
+ *   a_q, a_scale  token codes [M, K] and scales; w_q, w_scale weight codes
+ *                 [N, K] and scales
+ *   y             [M, N] of dtype
+ *   M, N          any (odd ones included), below 2^31 - 256
+ */
+int quarot_fp8_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q, const float* w_scale, int64_t M,
+                    int64_t N, int64_t K, void* y, int dtype, void* stream);
+
+/*
+ * quarot_fp8_gated_gemm -- the gated half of a feed-forward block in one
+ * kernel: with g = A Wg^T and u = A Wu^T as in quarot_fp8_gemm, kept in fp32,
+ *   z = g / (1 + exp(-g)) * u,
+ * quantized to q_out uint8 [M, I] and scale_out fp32 [ceil(I / 128), M] by the
+ * block quantizer: the operand of the down projection's quarot_fp8_gemm.
+ *   wg_q, wu_q    weight codes [I, K]; wg_scale, wu_scale their scales
+ *   I             a multiple of 16 (QUAROT_ERR_UNSUPPORTED otherwise)
+ */
+int quarot_fp8_gated_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* wg_q, const float* wg_scale,
+                          const uint8_t* wu_q, const float* wu_scale, int64_t M, int64_t I, int64_t K, uint8_t* q_out,
+                          float* scale_out, void* stream);
 
 /* quarot_legacy_imma_probe -- a measurement utility: one launch that issues
  * nothing but one legacy warp-level tensor-core instruction, mma.sync s8

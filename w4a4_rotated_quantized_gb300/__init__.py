@@ -10,15 +10,20 @@ Functions (same names as the C entry points):
     quarot_rotate_quant, quarot_w4a4_gemm, quarot_kv_write,
     quarot_decode_attn, quarot_decode_workspace_bytes, quarot_check_error,
     and the tensor-core operand form of the layer: quarot_rotate_quant_a8,
-    quarot_w4a4_gemm_a8
+    quarot_w4a4_gemm_a8; the 8-bit layer: quarot_quant_fp8,
+    quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8, quarot_fp8_gemm,
+    quarot_fp8_gated_gemm
 
 ``QuarotLinear`` composes them into the W4A4 linear layer: weight rows
 rotated and quantized once, then per call the tokens rotated and quantized
 and the INT4 GEMM with its dequant epilogue.  ``QuarotKVCache`` holds the
 rotated INT4 KV cache with its append, decode and prompt-attention calls.
+``QuarotFp8Linear`` and ``QuarotFp8GatedMLP`` are the layers kept at 8 bits:
+e4m3 codes with a scale for each block of 128.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -63,6 +68,12 @@ _SIGS = {
     "quarot_legacy_imma_probe": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, ctypes.POINTER(ctypes.c_int64), _P]),
     "quarot_prefill_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                            ctypes.c_float, ctypes.c_int, _P, _P]),
+    "quarot_quant_fp8": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P]),
+    "quarot_quant_fp8_block": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P]),
+    "quarot_add_rmsnorm_quant_fp8": (ctypes.c_int, [_P, _I64, _P, _I64, _P, ctypes.c_int, _I64, _I64, ctypes.c_float,
+                                                    _P, _I64, _P, _P, _P]),
+    "quarot_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int, _P]),
+    "quarot_fp8_gated_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "quarot_kv_write_asym": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P,
                                             _P, _P, _P, _P]),
     "quarot_decode_attn_asym": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
@@ -530,6 +541,213 @@ class QuarotLinear:
             a_q, a_scale, _ = quarot_rotate_quant(x2, self.signs, clip_ratio=self.clip_ratio, stream=stream)
             y, _ = quarot_w4a4_gemm(a_q, a_scale, self.w_q, self.w_scale, y=y, stream=stream)
         return y.view(*lead, self.out_features)
+
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # QUAROT_FP16, QUAROT_BF16
+_E4M3 = torch.float8_e4m3fn
+
+
+def _on(dev):
+    """The tensors' device as the current one, where it is another."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _need_16bit(t, name, dev=None, dtype=None) -> int:
+    """A 2-D fp16 or bf16 input read row by row; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+        raise QuarotError(1, f"{name} must be an fp16 or bf16 CUDA tensor")
+    return _need_rows(t, t.dtype if dtype is None else dtype, name, dev)
+
+
+def _need_shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _fp8_outputs(M, d, scale_shape, q_out, scale_out, dev):
+    if q_out is None:
+        q_out = torch.empty((M, d), dtype=_E4M3, device=dev)
+    else:
+        _need(q_out, _E4M3, "q_out", dev)
+        _need_shape(q_out, (M, d), "q_out")
+    if scale_out is None:
+        scale_out = torch.empty(scale_shape, dtype=torch.float32, device=dev)
+    else:
+        _need(scale_out, torch.float32, "scale_out", dev)
+        _need_shape(scale_out, scale_shape, "scale_out")
+    return q_out, scale_out
+
+
+def quarot_quant_fp8(x, q_out=None, scale_out=None, stream=None):
+    """x: fp16 or bf16 [M, d], rows contiguous (any row stride) -> (e4m3 codes
+    [M, d], fp32 scales [ceil(d / 128), M], one for each token and 128 columns)."""
+    ld = _need_16bit(x, "x")
+    dev = x.device
+    M, d = x.shape
+    q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
+    with _on(dev):
+        st = load().quarot_quant_fp8(_ptr(x), _DTYPES[x.dtype], M, d, ld, _ptr(q_out), _ptr(scale_out),
+                                     _stream(stream, dev))
+    _check(st, "quarot_quant_fp8")
+    return q_out, scale_out
+
+
+def quarot_quant_fp8_block(w, q_out=None, scale_out=None, stream=None):
+    """w: fp16 or bf16 [N, K], rows contiguous (any row stride) -> (e4m3 codes
+    [N, K], fp32 scales [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block)."""
+    ld = _need_16bit(w, "w")
+    dev = w.device
+    N, K = w.shape
+    q_out, scale_out = _fp8_outputs(N, K, (_blocks(N), _blocks(K)), q_out, scale_out, dev)
+    with _on(dev):
+        st = load().quarot_quant_fp8_block(_ptr(w), _DTYPES[w.dtype], N, K, ld, _ptr(q_out), _ptr(scale_out),
+                                           _stream(stream, dev))
+    _check(st, "quarot_quant_fp8_block")
+    return q_out, scale_out
+
+
+def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-6, residual_out=None, q_out=None,
+                                 scale_out=None, stream=None):
+    """h = x + residual (rounded to their type), RMSNorm of h (times weight)
+    and quantization in one pass: (e4m3 codes [M, d], fp32 scales
+    [ceil(d / 128), M], h [M, d]).  x, residual, residual_out: fp16 or bf16
+    [M, d], rows contiguous (any row stride); weight [d] or None.
+    residual_out may be x or residual itself; without a residual h is x,
+    and is copied only if residual_out is given."""
+    ld = _need_16bit(x, "x")
+    dev, dt = x.device, x.dtype
+    M, d = x.shape
+    ld_r = ld_h = d
+    if residual is not None:
+        ld_r = _need_rows(residual, dt, "residual", dev)
+        _need_shape(residual, (M, d), "residual")
+        if residual_out is None:
+            residual_out = torch.empty((M, d), dtype=dt, device=dev)
+    if residual_out is not None:
+        ld_h = _need_rows(residual_out, dt, "residual_out", dev)
+        _need_shape(residual_out, (M, d), "residual_out")
+    if weight is not None:
+        _need(weight, dt, "weight", dev)
+        _need_shape(weight, (d,), "weight")
+    q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
+    with _on(dev):
+        st = load().quarot_add_rmsnorm_quant_fp8(_ptr(x), ld, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], M, d,
+                                                 float(eps), _ptr(residual_out), ld_h, _ptr(q_out), _ptr(scale_out),
+                                                 _stream(stream, dev))
+    _check(st, "quarot_add_rmsnorm_quant_fp8")
+    return q_out, scale_out, x if residual_out is None else residual_out
+
+
+def _need_fp8_operand(codes, scale, name, weights, dev=None):
+    _need(codes, _E4M3, name, dev)
+    _need(scale, torch.float32, name + " scale", codes.device)
+    if codes.dim() != 2:
+        raise QuarotError(1, f"{name} must be 2-D")
+    rows, K = codes.shape
+    _need_shape(scale, (_blocks(rows), _blocks(K)) if weights else (_blocks(K), rows), name + " scale")
+
+
+def quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y=None, out_dtype=torch.float16, stream=None):
+    """Token codes [M, K] and scales x weight codes [N, K] and scales ->
+    y fp16 or bf16 [M, N] (``out_dtype``, or the type of ``y``)."""
+    _need_fp8_operand(a_q, a_scale, "a_q", False)
+    dev = a_q.device
+    _need_fp8_operand(w_q, w_scale, "w_q", True, dev)
+    M, K = a_q.shape
+    N = w_q.shape[0]
+    if w_q.shape[1] != K:
+        raise QuarotError(1, "a_q and w_q disagree on K")
+    if y is None:
+        if out_dtype not in _DTYPES:
+            raise QuarotError(1, "out_dtype must be float16 or bfloat16")
+        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        if y.dtype not in _DTYPES:
+            raise QuarotError(1, "y must be fp16 or bf16")
+        _need(y, y.dtype, "y", dev)
+        _need_shape(y, (M, N), "y")
+    with _on(dev):
+        st = load().quarot_fp8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(y),
+                                    _DTYPES[y.dtype], _stream(stream, dev))
+    _check(st, "quarot_fp8_gemm")
+    return y
+
+
+def quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out=None, scale_out=None, stream=None):
+    """silu(A Wg^T) * (A Wu^T) of block-scaled codes (weights [I, K]) ->
+    (e4m3 codes [M, I], fp32 scales [ceil(I / 128), M])."""
+    _need_fp8_operand(a_q, a_scale, "a_q", False)
+    dev = a_q.device
+    _need_fp8_operand(wg_q, wg_scale, "wg_q", True, dev)
+    _need_fp8_operand(wu_q, wu_scale, "wu_q", True, dev)
+    M, K = a_q.shape
+    I = wg_q.shape[0]
+    if wg_q.shape[1] != K or wu_q.shape != wg_q.shape:
+        raise QuarotError(1, "a_q, wg_q and wu_q disagree on their shapes")
+    q_out, scale_out = _fp8_outputs(M, I, (_blocks(I), M), q_out, scale_out, dev)
+    with _on(dev):
+        st = load().quarot_fp8_gated_gemm(_ptr(a_q), _ptr(a_scale), _ptr(wg_q), _ptr(wg_scale), _ptr(wu_q),
+                                          _ptr(wu_scale), M, I, K, _ptr(q_out), _ptr(scale_out), _stream(stream, dev))
+    _check(st, "quarot_fp8_gated_gemm")
+    return q_out, scale_out
+
+
+class QuarotFp8Linear:
+    """A linear layer kept at 8 bits, y = x W^T in e4m3 with a scale for each
+    block of 128: the weight [N, K] (fp16 or bf16) is quantized at
+    construction (quarot_quant_fp8_block); each call quantizes the tokens
+    (quarot_quant_fp8) and runs quarot_fp8_gemm.  x: [..., K], fp16 or bf16
+    -> [..., N] of the same type.  ``from_codes`` takes tokens that are
+    quantized already (by quarot_add_rmsnorm_quant_fp8 or a gated product)."""
+
+    def __init__(self, weight, stream=None):
+        self.w_q, self.w_scale = quarot_quant_fp8_block(weight, stream=stream)
+        self.out_features, self.in_features = weight.shape
+
+    def __call__(self, x, y=None, stream=None):
+        if x.shape[-1] != self.in_features:
+            raise QuarotError(1, f"x has {x.shape[-1]} features, the layer {self.in_features}")
+        lead = x.shape[:-1]
+        a_q, a_scale = quarot_quant_fp8(x.reshape(-1, self.in_features), stream=stream)
+        if y is not None:
+            y = y.view(-1, self.out_features)
+        return self.from_codes(a_q, a_scale, y=y, out_dtype=x.dtype, stream=stream).view(*lead, self.out_features)
+
+    def from_codes(self, a_q, a_scale, y=None, out_dtype=torch.float16, stream=None):
+        return quarot_fp8_gemm(a_q, a_scale, self.w_q, self.w_scale, y=y, out_dtype=out_dtype, stream=stream)
+
+
+class QuarotFp8GatedMLP:
+    """A pre-norm gated feed-forward block at 8 bits: per call
+    h = x + residual and its RMSNorm (quarot_add_rmsnorm_quant_fp8), the gated
+    product (quarot_fp8_gated_gemm) and the down projection
+    (quarot_fp8_gemm), three launches.  w_gate, w_up: [I, K], w_down: [K, I],
+    fp16 or bf16; norm_weight [K] or None.  x, residual: [..., K] ->
+    (block output [..., K], h [..., K]), the next block's x and residual."""
+
+    def __init__(self, w_gate, w_up, w_down, norm_weight=None, eps: float = 1e-6, stream=None):
+        if w_up.shape != w_gate.shape or tuple(w_down.shape) != tuple(reversed(w_gate.shape)):
+            raise QuarotError(1, "w_gate and w_up are [I, K], w_down [K, I]")
+        self.gate_q, self.gate_scale = quarot_quant_fp8_block(w_gate, stream=stream)
+        self.up_q, self.up_scale = quarot_quant_fp8_block(w_up, stream=stream)
+        self.down = QuarotFp8Linear(w_down, stream=stream)
+        self.norm_weight, self.eps = norm_weight, float(eps)
+        self.features = w_gate.shape[1]
+
+    def __call__(self, x, residual=None, stream=None):
+        if x.shape[-1] != self.features:
+            raise QuarotError(1, f"x has {x.shape[-1]} features, the block {self.features}")
+        x2 = x.reshape(-1, self.features)
+        r2 = None if residual is None else residual.reshape(-1, self.features)
+        a_q, a_scale, h = quarot_add_rmsnorm_quant_fp8(x2, r2, self.norm_weight, eps=self.eps, stream=stream)
+        z_q, z_scale = quarot_fp8_gated_gemm(a_q, a_scale, self.gate_q, self.gate_scale, self.up_q, self.up_scale,
+                                             stream=stream)
+        y = self.down.from_codes(z_q, z_scale, out_dtype=x.dtype, stream=stream)
+        return y.view(x.shape), h.view(x.shape)
 
 
 class QuarotKVCache:
