@@ -1,7 +1,7 @@
 """Builds libquarot.so in-tree for sm_103a with nvcc (no CMake, no torch).
 
-Each translation unit under csrc/ is compiled as relocatable device code in
-parallel, then linked into a shared library next to this file.  A rebuild is
+Each translation unit under csrc/ is compiled in parallel, as relocatable
+device code or (WHOLE_PROGRAM) by itself, then linked into a shared library next to this file.  A rebuild is
 skipped when the library is newer than every source and header.
 """
 from __future__ import annotations
@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libquarot.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-std=c++17", "-rdc=true", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
+WHOLE_PROGRAM = {"fp8_gemm.cu"}  # ptxas honours setmaxnreg only there
+FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
 
 def _nvcc() -> str:
@@ -55,7 +56,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src_obj):
         src, obj = src_obj
-        cmd = [nvcc, *ARCH, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
+        rdc = "-rdc=false" if os.path.basename(src) in WHOLE_PROGRAM else "-rdc=true"
+        cmd = [nvcc, *ARCH, *FLAGS, rdc, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")

@@ -69,6 +69,9 @@ extern "C" int quarot_check_error(void* stream) {
   if (cudaMemcpyFromSymbol(&word, quarot::g_error_word, sizeof(word)) != cudaSuccess) return QUAROT_ERR_CUDA;
   if (word != 0 && cudaMemcpyToSymbol(quarot::g_error_word, &zero, sizeof(zero)) != cudaSuccess)
     return QUAROT_ERR_CUDA;
+  unsigned int fp8_word = 0;
+  if (!quarot::take_fp8_error_word(&fp8_word)) return QUAROT_ERR_CUDA;
+  word |= fp8_word;
   if (word & (1u << QUAROT_ERR_TIMEOUT)) return QUAROT_ERR_TIMEOUT;
   return word ? QUAROT_ERR_CUDA : QUAROT_OK;
 }

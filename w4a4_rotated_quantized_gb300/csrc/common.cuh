@@ -15,7 +15,17 @@ namespace quarot {
 // Device error word: one bit per status code, bit (1 << code).  A kernel
 // sets the bit of QUAROT_ERR_TIMEOUT when a bounded wait expires;
 // quarot_check_error() reads the word, clears it and maps the bits back.
-extern __device__ unsigned int g_error_word;  // defined in abi.cu (relocatable device code)
+// Defined in abi.cu (relocatable device code); a file that is compiled as a
+// whole program (QUAROT_OWN_ERROR_WORD) has its own, which
+// quarot_check_error() reads through that file's take function.
+#ifdef QUAROT_OWN_ERROR_WORD
+static __device__ unsigned int g_error_word = 0;
+#else
+extern __device__ unsigned int g_error_word;
+#endif
+
+// Reads and clears the error word of fp8_gemm.cu; false on a CUDA error.
+bool take_fp8_error_word(unsigned int* word);
 
 // ~1 s: far above any legitimate wait, short enough to keep a shared GPU
 // usable if a barrier is never satisfied.
