@@ -206,7 +206,8 @@ def test_norm_edge_rows(q, dtype):
 # ---------------------------------------------------------------- products
 GEMM = [(1, 1, 16), (1, 4096, 4096), (2, 127, 144), (5, 129, 128), (8, 1000, 12288), (17, 64, 272), (33, 4100, 1008),
         (64, 256, 256), (65, 300, 528), (100, 129, 4096), (128, 128, 384), (129, 1025, 640), (200, 777, 2064),
-        (256, 512, 512), (257, 2048, 1040), (513, 1031, 272), (1000, 257, 4096), (1500, 2500, 400)]
+        (256, 512, 512), (257, 2048, 1040), (513, 1031, 272), (1000, 257, 4096), (1500, 2500, 400),
+        (2600, 2100, 144), (2601, 2101, 1168), (20000, 300, 128), (150, 40000, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -256,7 +257,8 @@ def test_gemm_nan_stays_in_its_row_and_column(q, M):
 
 
 GATED = [(1, 16, 16), (1, 4096, 4096), (3, 144, 272), (7, 272, 128), (16, 1040, 4096), (33, 400, 1008), (64, 256, 512),
-         (65, 656, 528), (130, 1024, 640), (257, 272, 1040), (333, 1040, 2064), (600, 784, 400)]
+         (65, 656, 528), (130, 1024, 640), (257, 272, 1040), (333, 1040, 2064), (600, 784, 400),
+         (2600, 1040, 144), (2601, 1168, 1296), (20000, 144, 128), (150, 20000, 272)]
 
 
 @pytest.mark.parametrize("M,I,K", GATED)

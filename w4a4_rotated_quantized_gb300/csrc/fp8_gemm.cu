@@ -69,6 +69,14 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         "h"(uint16_t(3))
         : "memory");
 }
+// The same on the barrier of each CTA in `mask`.
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
   if constexpr (CG == 1) {
@@ -91,7 +99,7 @@ __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // 32 (16) columns of this warp's 32 tensor-memory lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
       "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -101,7 +109,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
@@ -130,6 +138,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
         : "memory");
 }
 
+// The same box into the same place of each CTA in `mask`, completing on each one's own barrier.
+__device__ __forceinline__ void tma_load_to(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar,
+                                            uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
+      "%3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -148,10 +166,33 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival on CTA `rank`'s barrier.  What it hands over are finished
-// tensor-memory reads (tcgen05.wait::ld before it), no generic-proxy data.
-__device__ __forceinline__ void arrive_remote(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa(smem_u32(bar), rank)) : "memory");
+// Arrival on a barrier of either CTA (a shared::cluster address).  What it
+// hands over are finished tensor-memory reads (tcgen05.wait::ld before it), no
+// generic-proxy data.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_s(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int n = 0; n < 100000; ++n)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+// One lane of a converged warp, in the form in which the compiler sees that it is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Whether the phase is over, without waiting (try_wait may sleep).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
@@ -161,6 +202,15 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* o) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
                : "memory");
+}
+
+// Four bytes from global to this CTA's shared memory, asynchronously; the
+// arrival on the barrier follows this thread's copies so far.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdiv_rn(g, 1.0f + expf(-g)); }
@@ -189,21 +239,27 @@ __device__ __forceinline__ float silu(float g) { return __fdiv_rn(g, 1.0f + expf
 // i0 + 64 h + [0, 64), so a thread holds gate and up of the same columns.
 namespace wide {
 
-constexpr int S = 6;                        // stages
+constexpr int S = 6;  // stages
 constexpr int A_BYTES = 128 * BK, B_BYTES = 128 * BK;
 constexpr int OFF_B = S * A_BYTES;
 constexpr int OFF_BAR = OFF_B + S * B_BYTES;
-constexpr int NBAR = 2 * S + 4 + 4 + 1 + 1;  // full empty acc_full[2][2] acc_empty[2][2] exchange drain
+constexpr int CH = 8;  // k-blocks whose scales are handed over together
+constexpr int NBAR = 2 * S + 4 + 4 + 2 + 2 + 1 + 1;  // full empty acc_full[2][2] acc_empty[2][2] sc_full[2] sc_empty[2] exchange drain
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int OFF_AMAX = (OFF_MISC + 16 + 127) / 128 * 128;  // float [2][2][128]
-constexpr int OFF_STG = OFF_AMAX + 2 * 2 * 128 * 4;           // 16-bit [8 warps][32 rows][34]
+constexpr int SLOT = 132;                                      // 128 token scales and the weight blocks' two
+constexpr int OFF_SCALE = OFF_AMAX + 2 * 2 * 128 * 4;          // float [2][CH][SLOT]
+constexpr int OFF_STG = OFF_SCALE + 2 * CH * SLOT * 4;         // 16-bit [8 warps][32 rows][STG_LD]
 constexpr int STG_LD = 34;
 constexpr int SMEM = OFF_STG + 8 * 32 * STG_LD * 2 + 1024;
 constexpr int EPI0 = 4, NT = 32 * (EPI0 + 8);
-constexpr int REG_LO = 56, REG_HI = 224;  // of the 168 a thread that the block is launched with
+constexpr int REG_LO = 104, REG_HI = 200;  // of the 168 a thread that the block is launched with
 static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t IDESC = idesc(256, 128);
+constexpr bool HALVES = true;
+constexpr int CW = 16;                                    // columns of a tensor-memory read
+constexpr int W_BOX = 64;                                 // weight rows of a copy: a half's from one CTA
+constexpr int MN = HALVES ? 128 : 256;                    // columns of an MMA
 static_assert(SMEM <= 227 * 1024, "shared memory");
 
 template <bool GATED, typename T>
@@ -216,9 +272,11 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;     // [buffer * 2 + half]
-  uint64_t* acc_empty = acc_full + 4;
-  uint64_t* exch = acc_empty + 4;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 4;  // [buffer][half]
+  uint64_t* sc_full = acc_empty + 4;
+  uint64_t* sc_empty = sc_full + 2;
+  uint64_t* exch = sc_empty + 2;
   uint64_t* drain = exch + 1;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_MISC + 4);
@@ -227,7 +285,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   const uint32_t rank = cluster_rank();
   const int pair_id = int(blockIdx.x) >> 1, n_pairs = int(gridDim.x) >> 1;
   constexpr int TN = GATED ? 128 : 256;  // output columns of a tile
-  const int tiles_n = (N + TN - 1) / TN;
+  const int tiles_n = (N + TN - 1) / TN, nblk = (N + BLK - 1) / BLK;
   const int n_tiles = ((M + 255) / 256) * tiles_n;
 
   if (threadIdx.x == 0) {
@@ -240,7 +298,11 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);  // the half's four warps of both CTAs (used in the leader)
+      mbar_init(&acc_empty[i], HALVES ? 8 : 16);  // the epilogue warps of both CTAs (used in the leader)
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sc_full[i], 32);
+      mbar_init(&sc_empty[i], 8);
     }
     mbar_init(exch, 8);
     mbar_init(drain, 1);
@@ -258,72 +320,119 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      // The leader's barrier expects both CTAs' bytes; a stage is loaded again
-      // once the MMAs that read it are done, which they are only after that
-      // barrier's phase completed, so no byte lands in an earlier phase.
+      // Both CTAs' bytes complete on the leader's barrier.  A stage is loaded
+      // again once the MMAs that read it are done, which they are only after
+      // that barrier's phase, so no byte lands in an earlier one.
       const CUtensorMap* tw = GATED && rank == 1 ? &tmW1 : &tmW0;
-      int s = 0;
-      uint32_t par = 0;  // of the stage's current phase
-      long issued = 0;
-      for (int tile = pair_id; tile < n_tiles && !warp_flag(abort_flag); tile += n_pairs) {
-        const int m0 = tile / tiles_n * 256 + int(rank) * 128;
-        const int nt = tile % tiles_n;
-        const int w0 = GATED ? nt * 128 : nt * 256 + int(rank) * 64;
-        constexpr int WH = GATED ? 64 : 128;  // weight rows between the halves
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!warp_wait(&empty[s], par ^ 1u, abort_flag)) break;
-          if (lane == 0) {
+      if (lane == 0) {
+        int s = 0;
+        uint32_t par = 0;  // of the stage's current phase
+        long issued = 0;
+        bool ok = true;
+        for (int tile = pair_id; ok && tile < n_tiles; tile += n_pairs) {
+          const int m0 = tile / tiles_n * 256 + int(rank) * 128;
+          const int nt = tile % tiles_n;
+          const int w0 = GATED ? nt * 128 : nt * 256 + int(rank) * (HALVES ? 64 : 128);
+          constexpr int WH = GATED || !HALVES ? 64 : 128;  // weight rows between the halves
+          for (int kb = 0; kb < nkb; ++kb) {
+            ok = wait_s(&empty[s], par ^ 1u, abort_flag);
+            if (!ok) break;
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (A_BYTES + B_BYTES));
             const uint32_t bar = mapa(smem_u32(&full[s]), 0);
             tma_load<2>(smem_u32(sm + s * A_BYTES), &tmA, kb * BK, m0, bar);
-            const uint32_t b = smem_u32(sm + OFF_B + s * B_BYTES);
-            tma_load<2>(b, tw, kb * BK, w0, bar);
-            tma_load<2>(b + 64 * BK, tw, kb * BK, w0 + WH, bar);
+            const uint32_t bs = smem_u32(sm + OFF_B + s * B_BYTES);
+            tma_load<2>(bs, tw, kb * BK, w0, bar);
+            tma_load<2>(bs + W_BOX * BK, tw, kb * BK, w0 + WH, bar);
+            ++issued;
+            if (++s == S) { s = 0; par ^= 1u; }
           }
-          __syncwarp();
-          ++issued;
+        }
+        // the last stages' MMAs: no arrival is under way when the CTAs part
+        for (int i = 0; ok && i < S; ++i) {
+          ok = wait_s(&empty[s], par ^ 1u, abort_flag);
           if (++s == S) { s = 0; par ^= 1u; }
         }
+        // after an expired wait: the copies in flight (the peer's complete here
+        // too, and it stays until the final cluster barrier)
+        if (!ok && rank == 0)
+          for (long j = issued > S ? issued - S : 0; j < issued; ++j)
+            wait_s(&full[j % S], uint32_t((j / S) & 1), nullptr);
       }
-      // after an expired wait: both CTAs' copies in flight complete on the
-      // leader's barriers, and the peer stays until the final cluster barrier
-      if (rank == 0 && warp_flag(abort_flag) && lane == 0)
-        for (long j = issued > S ? issued - S : 0; j < issued; ++j)
-          mbar_wait_bounded(&full[j % S], uint32_t((j / S) & 1), nullptr);
+      __syncwarp();
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer
-      int s = 0;
+      const uint64_t a_desc = sw128_desc(smem_u32(sm)), b_desc = sw128_desc(smem_u32(sm + OFF_B));
+      // One thread.  An MMA is accepted when the one before it is almost done,
+      // so between two k-blocks there is one MMA's time for everything else:
+      // whether the next k-block may start is asked before this one's last
+      // MMA, and the stage is released after the next one's first.
+      if (elect_one()) {
+      int s = 0, last = -1;
       uint32_t par = 0, it = 0;
       bool ok = true;
-      for (int tile = pair_id; ok && tile < n_tiles && !warp_flag(abort_flag); tile += n_pairs) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
+      constexpr int H = HALVES ? 2 : 1;
+      for (int tile = pair_id; ok && tile < n_tiles; tile += n_pairs) {
+        for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
           const int b = int(it & 1);
           const uint32_t acc_par = ((it >> 1) & 1) ^ 1u;
-          ok = warp_wait(&full[s], par, abort_flag);
-          const uint64_t ad = sw128_desc(smem_u32(sm + s * A_BYTES));
-          const uint64_t bd = sw128_desc(smem_u32(sm + OFF_B + s * B_BYTES));
+          const uint64_t ad = a_desc + uint64_t(s * (A_BYTES >> 4));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && warp_wait(&acc_empty[2 * b + h], acc_par, abort_flag);
+          for (int h = 0; h < H; ++h) {
+            if (h == 0) ok = wait_s(&full[s], par, abort_flag);
+            ok = ok && wait_s(&acc_empty[2 * b + h], acc_par, abort_flag);
             if (!ok) break;
             fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-              for (int kk = 0; kk < BK / 32; ++kk)
-                mma<2>(tmem + uint32_t(256 * b + 128 * h), ad + uint64_t(2 * kk),
-                       bd + uint64_t(h * (64 * BK >> 4) + 2 * kk), IDESC, kk != 0);
-              commit<2>(&acc_full[2 * b + h]);
-              if (h == 1) commit<2>(&empty[s]);
-            }
-            __syncwarp();
+            const uint64_t bd = b_desc + uint64_t(s * (B_BYTES >> 4) + h * (64 * BK >> 4));
+            const uint32_t d = tmem + uint32_t(256 * b + 128 * h);
+            mma<2>(d, ad, bd, idesc(256, MN), 0);
+            mma<2>(d, ad + 2, bd + 2, idesc(256, MN), 1);
+            mma<2>(d, ad + 4, bd + 4, idesc(256, MN), 1);
+            mma<2>(d, ad + 6, bd + 6, idesc(256, MN), 1);
+            commit<2>(&acc_full[2 * b + h]);
+            if (h == H - 1) commit<2>(&empty[s]);
           }
-          if (!ok) break;
           if (++s == S) { s = 0; par ^= 1u; }
         }
       }
-      if (lane == 0) {
-        commit<2>(drain);
-        mbar_wait_bounded(drain, 0, nullptr);
+      commit<2>(drain);
+      }
+      __syncwarp();
+      warp_wait(drain, 0, nullptr);
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- scales
+      // Word by word with cp.async (rows of any alignment): each lane four
+      // tokens' scales of a k-block, lanes 0 and 1 the weight blocks' (gated:
+      // of gate and up), CH k-blocks to a barrier.
+      const uint32_t sc = smem_u32(sm + OFF_SCALE) + 4 * lane;
+      int tile = pair_id, kb = nkb;
+      const float *pa = nullptr, *pw = nullptr;
+      int m = 0;
+      tile -= n_pairs;
+      for (uint32_t it = 0;; ++it) {
+        if (kb == nkb) {
+          tile += n_pairs;
+          if (tile >= n_tiles) {
+            if (it % CH != 0) cp_async_arrive(&sc_full[it / CH & 1]);
+            break;
+          }
+          const int nt = tile % tiles_n;
+          m = tile / tiles_n * 256 + int(rank) * 128 + lane;
+          pa = as + m;
+          pw = lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
+                         : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb);
+          kb = 0;
+        }
+        if (it % CH == 0 && !__all_sync(0xffffffffu, wait_s(&sc_empty[it / CH & 1], (it / (2 * CH) & 1) ^ 1u, abort_flag)))
+          break;
+        const uint32_t d = sc + it % (2 * CH) * (SLOT * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m + 32 * i < M) cp_async4(d + 128 * i, pa + 32 * i);
+        if (lane < 2) cp_async4(d + 512, pw);
+        pa += M;
+        ++pw;
+        ++kb;
+        if (it % CH == CH - 1) cp_async_arrive(&sc_full[it / CH & 1]);
       }
     }
   } else {
@@ -331,72 +440,52 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HI));
     const int quad = warp & 3, h = (warp - EPI0) >> 2;
     const int r = 32 * quad + lane;
-    const uint32_t tm_row = tmem + uint32_t(128 * h) + (uint32_t(32 * quad) << 16);
+    const uint32_t tm_row = tmem + uint32_t((GATED && !HALVES ? 64 : 128) * h) + (uint32_t(32 * quad) << 16);
+    auto col = [](int c) { return uint32_t(c + (GATED && !HALVES && c >= 64 ? 64 : 0)); };
     uint32_t it = 0;
     int ti = 0;
     bool ok = true;
+    const float* sc = reinterpret_cast<const float*>(sm + OFF_SCALE);
+    const uint32_t free0 = mapa(smem_u32(&acc_empty[HALVES ? h : 0]), 0);  // the leader's, of buffer 0
     for (int tile = pair_id; ok && tile < n_tiles && !*abort_flag; tile += n_pairs, ++ti) {
       const int gm = tile / tiles_n * 256 + int(rank) * 128 + r;
       const int nt = tile % tiles_n;
       const bool in = gm < M;
-      const float* asr = as + (in ? gm : 0);
-      // weight scale rows of this half (gated: of gate and up)
-      const int nblk = (N + BLK - 1) / BLK;
-      const float* w0 = ws0 + size_t(min(GATED ? nt : 2 * nt + h, nblk - 1)) * nkb;
-      const float* w1 = GATED ? ws1 + size_t(nt) * nkb : nullptr;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      // scales G k-blocks at a time, loaded a group ahead
-      constexpr int G = 4;
-      float sa[G], sw[G], su[G], na[G], nw[G], nu[G];
-      auto load_scales = [&](int kb0) {
-#pragma unroll
-        for (int u = 0; u < G; ++u) {
-          const bool k = kb0 + u < nkb;
-          na[u] = in && k ? __ldg(asr + size_t(kb0 + u) * M) : 0.f;
-          nw[u] = k ? __ldg(w0 + kb0 + u) : 0.f;
-          nu[u] = GATED && k ? __ldg(w1 + kb0 + u) : 0.f;
-        }
-      };
-      load_scales(0);
-      for (int kb0 = 0; ok && kb0 < nkb; kb0 += G) {
-#pragma unroll
-        for (int u = 0; u < G; ++u) {
-          sa[u] = na[u];
-          sw[u] = nw[u];
-          su[u] = nu[u];
-        }
-        load_scales(kb0 + G);
-#pragma unroll
-        for (int u = 0; u < G; ++u) {
-          if (kb0 + u >= nkb) break;
-          const int b = int(it & 1);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[2 * b + h], (it >> 1) & 1, abort_flag));
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int b = int(it & 1);
+        if (it % CH == 0) {
+          ok = __all_sync(0xffffffffu, wait_s(&sc_full[it / CH & 1], it / (2 * CH) & 1, abort_flag));
           if (!ok) break;
-          ++it;
-          fence_after_sync();
-          const uint32_t t = tm_row + uint32_t(256 * b);
-          const float s0 = sa[u] * sw[u], s1 = GATED ? sa[u] * su[u] : s0;
-          uint32_t v[2][32];
-          tmem_ld32(t, v[0]);
+        }
+        ok = __all_sync(0xffffffffu, wait_s(&acc_full[2 * b + (HALVES ? h : 0)], (it >> 1) & 1, abort_flag));
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t t = tm_row + uint32_t(256 * b);
+        uint32_t v[2][CW];
+        tmem_ld(t, v[0]);
+        const float* sl = sc + it % (2 * CH) * SLOT;
+        const float s0 = sl[r] * sl[GATED ? 128 : 128 + h], s1 = GATED ? sl[r] * sl[129] : s0;
+        if (it % CH == CH - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_empty[it / CH & 1]);
+        }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            wait_ld();
-            if (c < 3) {
-              tmem_ld32(t + 32u * (c + 1), v[(c + 1) & 1]);
-            } else {  // the last read is done: the buffer is free
-              fence_before_sync();
-              __syncwarp();
-              if (lane == 0) arrive_remote(&acc_empty[2 * b + h], 0);
-            }
-            const float sc = GATED && c >= 2 ? s1 : s0;
-            const float2 s2 = make_float2(sc, sc);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[16 * c + j] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])),
-                                           s2, acc[16 * c + j]);
+        for (int c = 0; c < 128 / CW; ++c) {
+          wait_ld();
+          if (c < 128 / CW - 1) {
+            tmem_ld(t + col(CW * (c + 1)), v[(c + 1) & 1]);
+          } else {  // the last read is done: the buffer is free
+            if (lane == 0) arrive_cluster(free0 + uint32_t(16 * b));
           }
+          const float sc2 = GATED && c >= 64 / CW ? s1 : s0;
+          const float2 s2 = make_float2(sc2, sc2);
+#pragma unroll
+          for (int j = 0; j < CW / 2; ++j)
+            acc[CW / 2 * c + j] = __ffma2_rn(
+                make_float2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), s2, acc[CW / 2 * c + j]);
         }
       }
       if (!ok) break;
@@ -442,7 +531,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         am[h * 128 + r] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(exch);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(exch, uint32_t(ti & 1), abort_flag));
+        ok = __all_sync(0xffffffffu, wait_s(exch, uint32_t(ti & 1), abort_flag));
         if (!ok) break;
         m = block_amax(max_nan(m, am[(h ^ 1) * 128 + r]));
         const Quotient quo(m);
@@ -649,10 +738,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         constexpr int CW = TN < 32 ? 16 : 32;
 #pragma unroll
         for (int c = 0; c < TN / CW; ++c) {
-          uint32_t v[32];
-          const uint32_t t = tm_row + uint32_t((b * NW + p) * TN + c * CW);
-          if constexpr (CW == 32) tmem_ld32(t, v);
-          else tmem_ld16(t, v);
+          uint32_t v[CW];
+          tmem_ld(tm_row + uint32_t((b * NW + p) * TN + c * CW), v);
           wait_ld();
           if (p == NW - 1 && c == TN / CW - 1) {
             fence_before_sync();
@@ -846,7 +933,7 @@ static int run(const Args& p) {
   constexpr int TN = GATED ? 128 : 256;
   const int64_t tiles = ((p.M + 255) / 256) * ((p.N + TN - 1) / TN);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch(p, wide::wide_kernel<GATED, T>, attr, dim3(unsigned(2 * pairs)), wide::NT, 2, wide::SMEM, 128, 64,
+  return launch(p, wide::wide_kernel<GATED, T>, attr, dim3(unsigned(2 * pairs)), wide::NT, 2, wide::SMEM, 128, wide::W_BOX,
                 static_cast<T*>(p.y));
 }
 
