@@ -11,8 +11,8 @@
 // epilogue warps read it, scale it and add it to fp32 sums in registers while
 // the MMAs of the next k-blocks fill other tensor-memory columns.
 //
-//   namespace wide    many tokens: CTA pairs (cta_group::2), 256 tokens x 256
-//                     weight rows (gated: 128 gate and 128 up rows)
+//   namespace wide    many tokens: persistent CTAs, 128 tokens x 256 weight rows
+//                     (gated: 128 gate and 128 up rows) at a time
 //   namespace narrow  few tokens: the weight rows are the MMA's M and the
 //                     tokens its N, the depth split over a thread-block cluster
 //
@@ -43,56 +43,22 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 // Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3, both K-major.
 __host__ __device__ constexpr uint32_t idesc(int m, int n) { return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24); }
 
-template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accumulate));
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accumulate));
-}
-// Arrives on the barrier (CG 2: on both CTAs') when all earlier MMAs of this thread are done.
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"(uint16_t(3))
-        : "memory");
-}
-// The same on the barrier of each CTA in `mask`.
-__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate));
 }
-template <int CG>
+// Arrives on the barrier when all earlier MMAs of this thread are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
-  if constexpr (CG == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -120,31 +86,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* tm) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
 }
-// One box at (x, y) into this CTA's shared memory; `bar` is a shared::cluster
-// address (CG 2: of either CTA of the pair).
-template <int CG>
+// One box at (x, y) into this CTA's shared memory.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// The same box into the same place of each CTA in `mask`, completing on each one's own barrier.
-__device__ __forceinline__ void tma_load_to(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar,
-                                            uint16_t mask) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-      "%3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
@@ -166,17 +112,21 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival on a barrier of either CTA (a shared::cluster address).  What it
-// hands over are finished tensor-memory reads (tcgen05.wait::ld before it), no
-// generic-proxy data.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
-__device__ __forceinline__ bool wait_s(uint64_t* bar, uint32_t parity, volatile int* abort) {
-#pragma unroll 1
-  for (int n = 0; n < 100000; ++n)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
+}
+// Arrival of the lanes that `pred` names, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t pred) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar), "r"(pred)
+               : "memory");
 }
 // One lane of a converged warp, in the form in which the compiler sees that it is one.
 __device__ __forceinline__ bool elect_one() {
@@ -184,20 +134,30 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-// Whether the phase is over, without waiting (try_wait may sleep).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+// Bounded waits: a try_wait sleeps for up to about 1.3 us, and kTries of them
+// are a little over the wait limit.  They are on every k-block's path, so they
+// are a handful of instructions: the caller records an expired one where its
+// loop ends.  wait_one is for one thread, wait_warp for a converged warp, whose
+// loop the vote keeps uniform.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int n = 0; n < kTries; ++n)
+    if (try_wait(bar, parity)) return true;
+  return false;
 }
-__device__ __forceinline__ bool warp_flag(volatile int* flag) { return __shfl_sync(0xffffffffu, *flag, 0) != 0; }
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity));
+}
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* o) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
@@ -209,58 +169,63 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* o) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Shared-memory words by address: through a pointer made from an integer (the
+// aligned base) the compiler falls back to generic loads, far slower here.
+__device__ __forceinline__ float lds(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdiv_rn(g, 1.0f + expf(-g)); }
 
 // ===================================================================== wide
-// Persistent CTA pairs; a pair computes 256 tokens x 256 weight rows.  Each
-// CTA loads its 128 token rows and half of the weight rows of a k-block (32
-// KB, S stages) and holds the sums of its 128 tokens x 256 columns: 256
-// epilogue threads x 128 fp32 registers.
+// Persistent CTAs, one on an SM; a tile is 128 tokens x 256 weight rows (gated:
+// 128 gate and 128 up rows).  A stage holds a k-block of both (48 KB).
 //
-//   warp 0      TMA producer; both CTAs' loads complete on the leader's barrier
-//   warp 1      TMEM allocator; MMA issuer in the leader
-//   warps 4-11  epilogue: warp w reads TMEM lane quadrant w % 4, column half (w - 4) / 4
+//   warp 0      TMA producer
+//   warp 1      TMEM allocator, MMA issuer
+//   warp 2      scales, CH k-blocks to a hand-over
+//   warps 4-11  epilogue: warp w reads TMEM lane quadrant w % 4, column half (w - 4) / 4,
+//               and holds the sums of 32 tokens x 128 columns (128 registers a thread)
 //
-// The first warpgroup hands registers to the other two (setmaxnreg), whose
-// sums, tensor-memory reads in flight and scales need about 200 a thread.
+// Two accumulators of 256 tensor-memory columns: one k-block is read, scaled
+// and summed while the MMAs of the next fill the other.
 //
-// The MMAs of a k-block run as two of N = 128 (column halves), each with its
-// own accumulator and barriers, two buffers each: 4 x 128 tensor-memory
-// columns.  A half's buffer is free for 3/4 of two k-blocks' MMA time before
-// its next MMA needs it.
-//
-// Column half h of a tile holds, from CTA 0's weight rows, columns [0, 64) and
-// from CTA 1's [64, 128): weight rows n0 + 128 h + 64 rank + [0, 64) for the
-// plain product; for the gated one CTA 0 loads gate rows and CTA 1 up rows
-// i0 + 64 h + [0, 64), so a thread holds gate and up of the same columns.
+// What bounds it: a k-block's MMAs take 512 clocks, reading and summing its
+// accumulator 375 (256 of them the fp32 sums), but the two are tied by a chain
+// of hand-overs (MMAs done -> read -> buffer free -> next MMAs) that is long on
+// latency.  So everything on that chain is short: one elected thread runs the
+// MMA loop, barriers are this CTA's own (CTA pairs, whose MMAs need less shared
+// memory traffic, lose more to their remote barriers than they gain), and a
+// k-block's scale is read from shared memory while the one before is summed.
 namespace wide {
 
-constexpr int S = 6;  // stages
-constexpr int A_BYTES = 128 * BK, B_BYTES = 128 * BK;
-constexpr int OFF_B = S * A_BYTES;
-constexpr int OFF_BAR = OFF_B + S * B_BYTES;
-constexpr int CH = 8;  // k-blocks whose scales are handed over together
-constexpr int NBAR = 2 * S + 4 + 4 + 2 + 2 + 1 + 1;  // full empty acc_full[2][2] acc_empty[2][2] sc_full[2] sc_empty[2] exchange drain
+constexpr int S = 4;  // stages
+constexpr int A_BYTES = 128 * BK, B_BYTES = 256 * BK, STAGE = A_BYTES + B_BYTES;
+constexpr int CH = 8;      // k-blocks whose scales are handed over together
+constexpr int SLOT = 132;  // 128 token scales and the two weight blocks'
+constexpr int OFF_BAR = S * STAGE;
+constexpr int NBAR = 2 * S + 2 + 2 + 2 + 2 + 1 + 1;  // full empty acc_full[2] acc_empty[2] sc_full[2] sc_empty[2] exchange drain
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int OFF_AMAX = (OFF_MISC + 16 + 127) / 128 * 128;  // float [2][2][128]
-constexpr int SLOT = 132;                                      // 128 token scales and the weight blocks' two
-constexpr int OFF_SCALE = OFF_AMAX + 2 * 2 * 128 * 4;          // float [2][CH][SLOT]
-constexpr int OFF_STG = OFF_SCALE + 2 * CH * SLOT * 4;         // 16-bit [8 warps][32 rows][STG_LD]
+constexpr int OFF_SCALE = OFF_AMAX + 2 * 2 * 128 * 4;         // float [2][CH][SLOT]
+constexpr int OFF_STG = OFF_SCALE + 2 * CH * SLOT * 4;        // 16-bit [8 warps][32 rows][STG_LD]
 constexpr int STG_LD = 34;
 constexpr int SMEM = OFF_STG + 8 * 32 * STG_LD * 2 + 1024;
 constexpr int EPI0 = 4, NT = 32 * (EPI0 + 8);
-constexpr int REG_LO = 104, REG_HI = 200;  // of the 168 a thread that the block is launched with
-static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
+constexpr int REG_LO = 88, REG_HI = 208;  // of the 168 a thread that the block is launched with
+constexpr int CW = 16;                    // columns of a tensor-memory read
 constexpr uint32_t TMEM_COLS = 512;
-constexpr bool HALVES = true;
-constexpr int CW = 16;                                    // columns of a tensor-memory read
-constexpr int W_BOX = 64;                                 // weight rows of a copy: a half's from one CTA
-constexpr int MN = HALVES ? 128 : 256;                    // columns of an MMA
 static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 
 template <bool GATED, typename T>
 __global__ void __launch_bounds__(NT, 1)
@@ -270,218 +235,174 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             float* __restrict__ qs) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
-  uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
-  uint64_t* acc_empty = acc_full + 4;  // [buffer][half]
-  uint64_t* sc_full = acc_empty + 4;
-  uint64_t* sc_empty = sc_full + 2;
-  uint64_t* exch = sc_empty + 2;
-  uint64_t* drain = exch + 1;
+  const uint32_t full = smem_u32(sm + OFF_BAR);
+  const uint32_t empty = full + 8 * S;
+  const uint32_t acc_full = empty + 8 * S;
+  const uint32_t acc_empty = acc_full + 8 * 2;
+  const uint32_t sc_full = acc_empty + 8 * 2;
+  const uint32_t sc_empty = sc_full + 8 * 2;
+  const uint32_t exch = sc_empty + 8 * 2;
+  const uint32_t drain = exch + 8;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair_id = int(blockIdx.x) >> 1, n_pairs = int(gridDim.x) >> 1;
+  // the shuffles tell the compiler what is the same in all lanes: the roles'
+  // branches, the barriers' and the tensor memory's addresses (20 % of the time)
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr int TN = GATED ? 128 : 256;  // output columns of a tile
   const int tiles_n = (N + TN - 1) / TN, nblk = (N + BLK - 1) / BLK;
-  const int n_tiles = ((M + 255) / 256) * tiles_n;
+  const int n_tiles = ((M + 127) / 128) * tiles_n;
 
   if (threadIdx.x == 0) {
     prefetch_map(&tmA);
     prefetch_map(&tmW0);
     if (GATED) prefetch_map(&tmW1);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], HALVES ? 8 : 16);  // the epilogue warps of both CTAs (used in the leader)
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sc_full[i], 32);
-      mbar_init(&sc_empty[i], 8);
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 8);
+      mbar_init(sc_full + 8 * i, 32);
+      mbar_init(sc_empty + 8 * i, 8);
     }
     mbar_init(exch, 8);
     mbar_init(drain, 1);
-    *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc<2>(smem_u32(const_cast<uint32_t*>(slot)), TMEM_COLS);
+  if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), TMEM_COLS);
   fence_before_sync();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before any remote arrival
   fence_after_sync();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
 
+  bool ok = true;
   if (warp < EPI0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      // Both CTAs' bytes complete on the leader's barrier.  A stage is loaded
-      // again once the MMAs that read it are done, which they are only after
-      // that barrier's phase, so no byte lands in an earlier one.
-      const CUtensorMap* tw = GATED && rank == 1 ? &tmW1 : &tmW0;
-      if (lane == 0) {
+      if (elect_one()) {
         int s = 0;
-        uint32_t par = 0;  // of the stage's current phase
-        long issued = 0;
-        bool ok = true;
-        for (int tile = pair_id; ok && tile < n_tiles; tile += n_pairs) {
-          const int m0 = tile / tiles_n * 256 + int(rank) * 128;
-          const int nt = tile % tiles_n;
-          const int w0 = GATED ? nt * 128 : nt * 256 + int(rank) * (HALVES ? 64 : 128);
-          constexpr int WH = GATED || !HALVES ? 64 : 128;  // weight rows between the halves
-          for (int kb = 0; kb < nkb; ++kb) {
-            ok = wait_s(&empty[s], par ^ 1u, abort_flag);
+        uint32_t par = 0, it = 0;
+        for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x)) {
+          const int m0 = tile / tiles_n * 128, w0 = tile % tiles_n * TN;
+          for (int kb = 0; kb < nkb; ++kb, ++it) {
+            ok = wait_one(empty + 8 * s, par ^ 1u);
             if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (A_BYTES + B_BYTES));
-            const uint32_t bar = mapa(smem_u32(&full[s]), 0);
-            tma_load<2>(smem_u32(sm + s * A_BYTES), &tmA, kb * BK, m0, bar);
-            const uint32_t bs = smem_u32(sm + OFF_B + s * B_BYTES);
-            tma_load<2>(bs, tw, kb * BK, w0, bar);
-            tma_load<2>(bs + W_BOX * BK, tw, kb * BK, w0 + WH, bar);
-            ++issued;
+            const uint32_t bar = full + 8 * s, st = smem_u32(sm + s * STAGE);
+            mbar_arrive_expect_tx(bar, STAGE);
+            tma_load(st, &tmA, kb * BK, m0, bar);
+            tma_load(st + A_BYTES, &tmW0, kb * BK, w0, bar);
+            tma_load(st + A_BYTES + B_BYTES / 2, GATED ? &tmW1 : &tmW0, kb * BK, GATED ? w0 : w0 + 128, bar);
             if (++s == S) { s = 0; par ^= 1u; }
           }
         }
-        // the last stages' MMAs: no arrival is under way when the CTAs part
-        for (int i = 0; ok && i < S; ++i) {
-          ok = wait_s(&empty[s], par ^ 1u, abort_flag);
-          if (++s == S) { s = 0; par ^= 1u; }
-        }
-        // after an expired wait: the copies in flight (the peer's complete here
-        // too, and it stays until the final cluster barrier)
-        if (!ok && rank == 0)
-          for (long j = issued > S ? issued - S : 0; j < issued; ++j)
-            wait_s(&full[j % S], uint32_t((j / S) & 1), nullptr);
+        if (!ok)  // after an expired wait: the copies in flight
+          for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_one(full + 8 * (j % S), (j / S) & 1);
       }
       __syncwarp();
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      const uint64_t a_desc = sw128_desc(smem_u32(sm)), b_desc = sw128_desc(smem_u32(sm + OFF_B));
-      // One thread.  An MMA is accepted when the one before it is almost done,
-      // so between two k-blocks there is one MMA's time for everything else:
-      // whether the next k-block may start is asked before this one's last
-      // MMA, and the stage is released after the next one's first.
       if (elect_one()) {
-      int s = 0, last = -1;
-      uint32_t par = 0, it = 0;
-      bool ok = true;
-      constexpr int H = HALVES ? 2 : 1;
-      for (int tile = pair_id; ok && tile < n_tiles; tile += n_pairs) {
-        for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
-          const int b = int(it & 1);
-          const uint32_t acc_par = ((it >> 1) & 1) ^ 1u;
-          const uint64_t ad = a_desc + uint64_t(s * (A_BYTES >> 4));
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            if (h == 0) ok = wait_s(&full[s], par, abort_flag);
-            ok = ok && wait_s(&acc_empty[2 * b + h], acc_par, abort_flag);
+        const uint64_t desc = sw128_desc(smem_u32(sm));
+        int s = 0;
+        uint32_t par = 0, it = 0;
+        for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x))
+          for (int kb = 0; kb < nkb; ++kb, ++it) {
+            const uint32_t b = it & 1;
+            ok = wait_one(full + 8 * s, par) && wait_one(acc_empty + 8 * b, ((it >> 1) & 1) ^ 1u);
             if (!ok) break;
             fence_after_sync();
-            const uint64_t bd = b_desc + uint64_t(s * (B_BYTES >> 4) + h * (64 * BK >> 4));
-            const uint32_t d = tmem + uint32_t(256 * b + 128 * h);
-            mma<2>(d, ad, bd, idesc(256, MN), 0);
-            mma<2>(d, ad + 2, bd + 2, idesc(256, MN), 1);
-            mma<2>(d, ad + 4, bd + 4, idesc(256, MN), 1);
-            mma<2>(d, ad + 6, bd + 6, idesc(256, MN), 1);
-            commit<2>(&acc_full[2 * b + h]);
-            if (h == H - 1) commit<2>(&empty[s]);
+            const uint64_t ad = desc + uint64_t(s * (STAGE >> 4)), bd = ad + (A_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk) mma(tmem + 256u * b, ad + 2 * kk, bd + 2 * kk, idesc(128, 256), kk != 0);
+            commit(acc_full + 8 * b);
+            commit(empty + 8 * s);
+            if (++s == S) { s = 0; par ^= 1u; }
           }
-          if (++s == S) { s = 0; par ^= 1u; }
-        }
-      }
-      commit<2>(drain);
+        commit(drain);
       }
       __syncwarp();
-      warp_wait(drain, 0, nullptr);
+      ok = wait_warp(drain, 0) && ok;
     } else if (warp == 2) {
       // ---------------------------------------------------------- scales
       // Word by word with cp.async (rows of any alignment): each lane four
       // tokens' scales of a k-block, lanes 0 and 1 the weight blocks' (gated:
-      // of gate and up), CH k-blocks to a barrier.
+      // of gate and up).
       const uint32_t sc = smem_u32(sm + OFF_SCALE) + 4 * lane;
-      int tile = pair_id, kb = nkb;
-      const float *pa = nullptr, *pw = nullptr;
-      int m = 0;
-      tile -= n_pairs;
-      for (uint32_t it = 0;; ++it) {
-        if (kb == nkb) {
-          tile += n_pairs;
-          if (tile >= n_tiles) {
-            if (it % CH != 0) cp_async_arrive(&sc_full[it / CH & 1]);
-            break;
-          }
-          const int nt = tile % tiles_n;
-          m = tile / tiles_n * 256 + int(rank) * 128 + lane;
-          pa = as + m;
-          pw = lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
-                         : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb);
-          kb = 0;
-        }
-        if (it % CH == 0 && !__all_sync(0xffffffffu, wait_s(&sc_empty[it / CH & 1], (it / (2 * CH) & 1) ^ 1u, abort_flag)))
-          break;
-        const uint32_t d = sc + it % (2 * CH) * (SLOT * 4);
+      uint32_t it = 0;
+      for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x)) {
+        const int nt = tile % tiles_n, m = tile / tiles_n * 128 + lane;
+        const float* pa = as + m;
+        const float* pw = lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
+                                    : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb);
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          if (it % CH == 0) ok = wait_warp(sc_empty + 8 * (it / CH & 1), (it / (2 * CH) & 1) ^ 1u);
+          if (!ok) break;
+          const uint32_t d = sc + it % (2 * CH) * (SLOT * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (m + 32 * i < M) cp_async4(d + 128 * i, pa + 32 * i);
-        if (lane < 2) cp_async4(d + 512, pw);
-        pa += M;
-        ++pw;
-        ++kb;
-        if (it % CH == CH - 1) cp_async_arrive(&sc_full[it / CH & 1]);
+          for (int i = 0; i < 4; ++i)
+            if (m + 32 * i < M) cp_async4(d + 128 * i, pa + 32 * i);
+          if (lane < 2) cp_async4(d + 512, pw);
+          pa += M;
+          ++pw;
+          if (it % CH == CH - 1) cp_async_arrive(sc_full + 8 * (it / CH & 1));
+        }
       }
+      if (it % CH != 0) cp_async_arrive(sc_full + 8 * (it / CH & 1));
     }
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HI));
     const int quad = warp & 3, h = (warp - EPI0) >> 2;
     const int r = 32 * quad + lane;
-    const uint32_t tm_row = tmem + uint32_t((GATED && !HALVES ? 64 : 128) * h) + (uint32_t(32 * quad) << 16);
-    auto col = [](int c) { return uint32_t(c + (GATED && !HALVES && c >= 64 ? 64 : 0)); };
+    // columns: plain 128 h + [0, 128); gated 64 h + [0, 64) of gate and of up, 128 apart
+    const uint32_t tm_row = tmem + uint32_t((GATED ? 64 : 128) * h) + (uint32_t(32 * quad) << 16);
+    auto col = [](int c) { return uint32_t(c + (GATED && c >= 64 ? 64 : 0)); };
+    const uint32_t sc = smem_u32(sm + OFF_SCALE);
     uint32_t it = 0;
     int ti = 0;
-    bool ok = true;
-    const float* sc = reinterpret_cast<const float*>(sm + OFF_SCALE);
-    const uint32_t free0 = mapa(smem_u32(&acc_empty[HALVES ? h : 0]), 0);  // the leader's, of buffer 0
-    for (int tile = pair_id; ok && tile < n_tiles && !*abort_flag; tile += n_pairs, ++ti) {
-      const int gm = tile / tiles_n * 256 + int(rank) * 128 + r;
+    float sn0 = 0.f, sn1 = 0.f;  // of k-block `it`, read while the one before is summed
+    auto next_scales = [&]() {
+      if (it % CH == 0 && ok) ok = wait_warp(sc_full + 8 * (it / CH & 1), it / (2 * CH) & 1);
+      const uint32_t sl = sc + it % (2 * CH) * (4 * SLOT);
+      const float a = lds(sl + 4 * r);
+      sn0 = a * lds(sl + 4 * (GATED ? 128 : 128 + h));
+      if (GATED) sn1 = a * lds(sl + 4 * 129);
+      if (it % CH == CH - 1) {
+        __syncwarp();
+        mbar_arrive_if(sc_empty + 8 * (it / CH & 1), lane == 0);
+      }
+    };
+    const uint32_t last = uint32_t((n_tiles - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x)) * uint32_t(nkb);
+    next_scales();
+    for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x), ++ti) {
+      const int gm = tile / tiles_n * 128 + r;
       const int nt = tile % tiles_n;
       const bool in = gm < M;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int b = int(it & 1);
-        if (it % CH == 0) {
-          ok = __all_sync(0xffffffffu, wait_s(&sc_full[it / CH & 1], it / (2 * CH) & 1, abort_flag));
-          if (!ok) break;
-        }
-        ok = __all_sync(0xffffffffu, wait_s(&acc_full[2 * b + (HALVES ? h : 0)], (it >> 1) & 1, abort_flag));
+      for (int kb = 0; kb < nkb; ++kb) {
+        const uint32_t b = it & 1;
+        ok = ok && wait_warp(acc_full + 8 * b, (it >> 1) & 1);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t t = tm_row + uint32_t(256 * b);
+        const uint32_t t = tm_row + 256u * b;
         uint32_t v[2][CW];
         tmem_ld(t, v[0]);
-        const float* sl = sc + it % (2 * CH) * SLOT;
-        const float s0 = sl[r] * sl[GATED ? 128 : 128 + h], s1 = GATED ? sl[r] * sl[129] : s0;
-        if (it % CH == CH - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_empty[it / CH & 1]);
-        }
+        const float s0 = sn0, s1 = GATED ? sn1 : sn0;
 #pragma unroll
         for (int c = 0; c < 128 / CW; ++c) {
           wait_ld();
           if (c < 128 / CW - 1) {
             tmem_ld(t + col(CW * (c + 1)), v[(c + 1) & 1]);
           } else {  // the last read is done: the buffer is free
-            if (lane == 0) arrive_cluster(free0 + uint32_t(16 * b));
+            mbar_arrive_if(acc_empty + 8 * b, lane == 0);
+            if (++it < last) next_scales();
           }
-          const float sc2 = GATED && c >= 64 / CW ? s1 : s0;
-          const float2 s2 = make_float2(sc2, sc2);
+          const float s = GATED && c >= 64 / CW ? s1 : s0;
+          const float2 s2 = make_float2(s, s);
 #pragma unroll
           for (int j = 0; j < CW / 2; ++j)
             acc[CW / 2 * c + j] = __ffma2_rn(
@@ -531,7 +452,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         am[h * 128 + r] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(exch);
-        ok = __all_sync(0xffffffffu, wait_s(exch, uint32_t(ti & 1), abort_flag));
+        ok = wait_warp(exch, uint32_t(ti & 1));
         if (!ok) break;
         m = block_amax(max_nan(m, am[(h ^ 1) * 128 + r]));
         const Quotient quo(m);
@@ -554,12 +475,12 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
   }
 
+  if (!ok) record_error(QUAROT_ERR_TIMEOUT);
   fence_before_sync();
   __syncthreads();
-  cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
   if (warp == 1) {
     fence_after_sync();
-    tmem_free<2>(tmem, TMEM_COLS);
+    tmem_free(tmem, TMEM_COLS);
   }
 }
 
@@ -610,15 +531,14 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   constexpr int S = C::S, NW = C::NW, KC = C::KC;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-  uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  const uint32_t full = smem_u32(sm + C::OFF_BAR);
+  const uint32_t empty = full + 8 * S;
+  const uint32_t acc_full = empty + 8 * S;
+  const uint32_t acc_empty = acc_full + 8 * 2;
+  const uint32_t drain = acc_empty + 8 * 2;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = int(cluster_rank()), ranks = int(cluster_size());
   const int wb = int(blockIdx.x) / ranks;  // block of 128 weight rows (and of output columns)
   const int m0 = int(blockIdx.y) * TN;
@@ -629,51 +549,51 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     prefetch_map(&tmW0);
     if (GATED) prefetch_map(&tmW1);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 4);
     }
     mbar_init(drain, 1);
-    *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc<1>(smem_u32(const_cast<uint32_t*>(slot)), C::COLS);
+  if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), C::COLS);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
-    int issued = 0;
-    for (int kb = kb_lo; kb < kb_hi; ++kb) {
-      const int i = kb - kb_lo, s = i % S;
-      if (!warp_wait(&empty[s], uint32_t((i / S) & 1) ^ 1u, abort_flag)) break;
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&full[s]), st = smem_u32(sm + s * C::STAGE);
-        mbar_arrive_expect_tx(&full[s], C::STAGE);
-        tma_load<1>(st, &tmW0, kb * BK, wb * 128, bar);
-        if (GATED) tma_load<1>(st + C::W_BYTES, &tmW1, kb * BK, wb * 128, bar);
-        tma_load<1>(st + NW * C::W_BYTES, &tmA, kb * BK, m0, bar);
+    bool ok = true;
+    if (elect_one()) {
+      int i = 0;
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++i) {
+        const int s = i % S;
+        ok = wait_one(empty + 8 * s, uint32_t((i / S) & 1) ^ 1u);
+        if (!ok) break;
+        const uint32_t bar = full + 8 * s, st = smem_u32(sm + s * C::STAGE);
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load(st, &tmW0, kb * BK, wb * 128, bar);
+        if (GATED) tma_load(st + C::W_BYTES, &tmW1, kb * BK, wb * 128, bar);
+        tma_load(st + NW * C::W_BYTES, &tmA, kb * BK, m0, bar);
       }
-      __syncwarp();
-      issued = i + 1;
+      if (!ok)  // after an expired wait: the copies in flight
+        for (int j = i > S ? i - S : 0; j < i; ++j) wait_one(full + 8 * (j % S), uint32_t((j / S) & 1));
     }
-    if (warp_flag(abort_flag) && lane == 0)
-      for (int j = issued > S ? issued - S : 0; j < issued; ++j)
-        mbar_wait_bounded(&full[j % S], uint32_t((j / S) & 1), nullptr);
+    __syncwarp();
+    if (!ok) record_error(QUAROT_ERR_TIMEOUT);
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    for (int kb = kb_lo; kb < kb_hi; ++kb) {
-      const int i = kb - kb_lo, s = i % S, b = i & 1;
-      if (!warp_wait(&full[s], uint32_t((i / S) & 1), abort_flag) ||
-          !warp_wait(&acc_empty[b], uint32_t((i >> 1) & 1) ^ 1u, abort_flag))
-        break;
-      fence_after_sync();
-      if (lane == 0) {
+    bool ok = true;
+    if (elect_one()) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const int i = kb - kb_lo, s = i % S, b = i & 1;
+        ok = wait_one(full + 8 * s, uint32_t((i / S) & 1)) && wait_one(acc_empty + 8 * b, uint32_t((i >> 1) & 1) ^ 1u);
+        if (!ok) break;
+        fence_after_sync();
         const uint32_t st = smem_u32(sm + s * C::STAGE);
         const uint64_t ad = sw128_desc(st + NW * C::W_BYTES);
 #pragma unroll
@@ -681,17 +601,15 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           const uint64_t wd = sw128_desc(st + p * C::W_BYTES);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            mma<1>(tmem + uint32_t((b * NW + p) * TN), wd + uint64_t(2 * kk), ad + uint64_t(2 * kk), idesc(128, TN), kk != 0);
+            mma(tmem + uint32_t((b * NW + p) * TN), wd + uint64_t(2 * kk), ad + uint64_t(2 * kk), idesc(128, TN), kk != 0);
         }
-        commit<1>(&acc_full[b]);
-        commit<1>(&empty[s]);
+        commit(acc_full + 8 * b);
+        commit(empty + 8 * s);
       }
-      __syncwarp();
+      commit(drain);
     }
-    if (lane == 0) {
-      commit<1>(drain);
-      mbar_wait_bounded(drain, 0, nullptr);
-    }
+    __syncwarp();
+    if (!wait_warp(drain, 0) || !ok) record_error(QUAROT_ERR_TIMEOUT);
   } else {
     // ------------------------------------------------------------ epilogue
     float2 acc[NW][TN / 2];
@@ -717,6 +635,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     };
     fetch(kb_lo);
     const uint32_t tm_row = tmem + (uint32_t(32 * warp) << 16);
+    bool ok = true;
     for (int kb = kb_lo; kb < kb_hi; ++kb) {
       const int i = kb - kb_lo, b = i & 1, kc = i % KC;
       if (kc == 0) {
@@ -730,7 +649,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         __syncwarp();
         fetch(kb + KC);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], uint32_t((i >> 1) & 1), abort_flag))) break;
+      ok = wait_warp(acc_full + 8 * b, uint32_t((i >> 1) & 1));
+      if (!ok) break;
       fence_after_sync();
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
@@ -742,9 +662,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           tmem_ld(tm_row + uint32_t((b * NW + p) * TN + c * CW), v);
           wait_ld();
           if (p == NW - 1 && c == TN / CW - 1) {
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
+            mbar_arrive_if(acc_empty + 8 * b, lane == 0);
           }
 #pragma unroll
           for (int j = 0; j < CW / 4; ++j) {
@@ -759,7 +677,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     // every k-block's accumulator was waited for, so the stages' loads and
     // reads are over: the sums [NW][TN][128 weight rows] take their place
     // (after an expired wait the values are void, the producer drains below)
-    if (!warp_flag(abort_flag)) {
+    if (ok) {
       float* part = reinterpret_cast<float*>(sm);
 #pragma unroll
       for (int p = 0; p < NW; ++p)
@@ -768,6 +686,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           part[(p * TN + 2 * j) * 128 + 32 * warp + lane] = acc[p][j].x;
           part[(p * TN + 2 * j + 1) * 128 + 32 * warp + lane] = acc[p][j].y;
         }
+    } else {
+      record_error(QUAROT_ERR_TIMEOUT);
     }
   }
 
@@ -776,7 +696,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   cluster_sync();
   if (warp == 5) {
     fence_after_sync();
-    tmem_free<1>(tmem, C::COLS);
+    tmem_free(tmem, C::COLS);
   }
   // ---- a warp per token: lane l holds weight rows 4 l .. 4 l + 3
   const uint32_t part = smem_u32(sm);
@@ -866,7 +786,7 @@ static int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K <= 0) return QUAROT_ERR_INVALID_ARG;
   const int64_t lim = (int64_t(1) << 31) - 256;
   if (K % 16 != 0 || K > (int64_t(1) << 20) || M > lim || N > lim) return QUAROT_ERR_UNSUPPORTED;
-  if (((M + 255) / 256) * ((N + 127) / 128) >= (int64_t(1) << 31) - 512) return QUAROT_ERR_UNSUPPORTED;
+  if (((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 31) - 512) return QUAROT_ERR_UNSUPPORTED;
   return QUAROT_OK;
 }
 
@@ -928,13 +848,11 @@ static int run(const Args& p) {
     if (p.M <= 64) return launch_narrow<GATED, 64, T>(p, cl);
     if constexpr (!GATED) return launch_narrow<GATED, 128, T>(p, cl);
   }
-  if (sms < 2) return QUAROT_ERR_UNSUPPORTED;
   static AttrCache attr;
   constexpr int TN = GATED ? 128 : 256;
-  const int64_t tiles = ((p.M + 255) / 256) * ((p.N + TN - 1) / TN);
-  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch(p, wide::wide_kernel<GATED, T>, attr, dim3(unsigned(2 * pairs)), wide::NT, 2, wide::SMEM, 128, wide::W_BOX,
-                static_cast<T*>(p.y));
+  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + TN - 1) / TN);
+  return launch(p, wide::wide_kernel<GATED, T>, attr, dim3(unsigned(tiles < sms ? tiles : sms)), wide::NT, 1, wide::SMEM,
+                128, 128, static_cast<T*>(p.y));
 }
 
 }  // namespace gemm
