@@ -94,6 +94,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
       : "memory");
 }
 
+// One box from this CTA's shared memory to (x, y), parts past the tensor's end left out.
+__device__ __forceinline__ void tma_store(const CUtensorMap* tm, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -184,7 +200,22 @@ __device__ __forceinline__ void sts(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float silu(float g) { return __fdiv_rn(g, 1.0f + expf(-g)); }
+// g / (1 + exp(-g)) to a few 2^-23: exp(-g) = 2^h 2^l with h = rn(-g log2 e) and
+// 2^l = 1 + l ln 2 for the rounding error l of h (exact by fma), 2^h and 1 / x by the
+// hardware approximations, 1 / x improved by a Newton step.  Far below zero h stops at
+// 126, where the result times anything stays below the quantizer's floor.  The
+// library's expf and division cost 25 % of the gated kernel.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kL2E = 1.44269502f, kL2ELow = 1.92596299e-8f;  // log2 e in two parts
+  const float h = fminf(-g * kL2E, 126.f);
+  const float l = h < 126.f ? fmaf(-g, kL2ELow, fmaf(-g, kL2E, -h)) : 0.f;
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
+  const float d = 1.0f + fmaf(e, l * 0.693147181f, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = fmaf(r, fmaf(-d, r, 1.0f), r);
+  return g * r;
+}
 
 // ===================================================================== wide
 // Persistent CTAs, one on an SM; a tile is 128 tokens x 256 weight rows (gated:
@@ -217,8 +248,9 @@ constexpr int NBAR = 2 * S + 2 + 2 + 2 + 2 + 1 + 1;  // full empty acc_full[2] a
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int OFF_AMAX = (OFF_MISC + 16 + 127) / 128 * 128;  // float [2][2][128]
 constexpr int OFF_SCALE = OFF_AMAX + 2 * 2 * 128 * 4;         // float [2][CH][SLOT]
-constexpr int OFF_STG = OFF_SCALE + 2 * CH * SLOT * 4;        // 16-bit [8 warps][32 rows][STG_LD]
+// staging of the output, 16-bit: [8 warps][2][32 rows][16] for TMA, [8 warps][32 rows][STG_LD] without it
 constexpr int STG_LD = 34;
+constexpr int OFF_STG = (OFF_SCALE + 2 * CH * SLOT * 4 + 127) / 128 * 128;
 constexpr int SMEM = OFF_STG + 8 * 32 * STG_LD * 2 + 1024;
 constexpr int EPI0 = 4, NT = 32 * (EPI0 + 8);
 constexpr int REG_LO = 88, REG_HI = 208;  // of the 168 a thread that the block is launched with
@@ -230,7 +262,7 @@ static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 template <bool GATED, typename T>
 __global__ void __launch_bounds__(NT, 1)
 wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW0,
-            const __grid_constant__ CUtensorMap tmW1, const float* __restrict__ as, const float* __restrict__ ws0,
+            const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmY, const float* __restrict__ as, const float* __restrict__ ws0,
             const float* __restrict__ ws1, int M, int N, int nkb, T* __restrict__ y, uint8_t* __restrict__ q,
             float* __restrict__ qs) {
   extern __shared__ unsigned char smem_raw[];
@@ -412,29 +444,41 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       if (!ok) break;
       if constexpr (!GATED) {
         const int n0 = nt * 256 + 128 * h;
-        const bool vec = (N % 16) == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
+        if ((N & 7) == 0) {
+          // 16 columns at a time through one of the warp's two buffers to a TMA
+          // store: the writes go out under the next tile's MMAs.  (Stores from
+          // registers, 32 bytes to each of 32 rows, held the warps for 2.8 us a tile.)
+          const int row0 = gm - lane;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int gn = n0 + 32 * c;
-          if (gn >= N) break;
-          uint32_t o[16];
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t buf = smem_u32(sm + OFF_STG) + uint32_t(((warp - EPI0) * 2 + (c & 1)) * 1024);
+            uint32_t o[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = from_f2<T>(acc[16 * c + j]);
-          if (vec) {
-            if (in) {
-              T* yr = y + size_t(gm) * N + gn;
-              st_global_v8(yr, o);
-              if (gn + 16 < N) st_global_v8(yr + 16, o + 8);
+            for (int j = 0; j < 8; ++j) o[j] = from_f2<T>(acc[8 * c + j]);
+            bulk_wait_read<1>();  // of the lane that stores; the others have none
+            __syncwarp();
+            sts128(buf + 32u * lane, o);
+            sts128(buf + 32u * lane + 16, o + 4);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              if (row0 < M && n0 + 16 * c < N) tma_store(&tmY, n0 + 16 * c, row0, buf);
+              bulk_commit();
             }
-          } else {
-            // rows of any alignment: through shared memory, a row's 32 columns by the 32 lanes
-            uint16_t* stg = reinterpret_cast<uint16_t*>(sm + OFF_STG) + (warp - EPI0) * 32 * STG_LD;
+          }
+        } else {
+          // rows of any alignment: through shared memory, a row's 32 columns by the 32 lanes
+          uint16_t* stg = reinterpret_cast<uint16_t*>(sm + OFF_STG) + (warp - EPI0) * 32 * STG_LD;
+          uint16_t* y16 = reinterpret_cast<uint16_t*>(y);
+          const int row0 = gm - lane, rows = min(32, M - row0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int gn = n0 + 32 * c;
+            if (gn >= N) break;
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(stg + lane * STG_LD + 2 * j) = o[j];
+            for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(stg + lane * STG_LD + 2 * j) = from_f2<T>(acc[16 * c + j]);
             __syncwarp();
-            uint16_t* y16 = reinterpret_cast<uint16_t*>(y);
-            const int row0 = gm - lane, rows = min(32, M - row0);
             if (gn + lane < N)
               for (int i = 0; i < rows; ++i) y16[size_t(row0 + i) * N + gn + lane] = stg[i * STG_LD + lane];
           }
@@ -448,13 +492,13 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           m = max_nan(m, max_nan(fabsf(acc[j].x), fabsf(acc[j].y)));
         }
         // the block's other 64 columns are the other half's: exchange the abs-max
-        float* am = reinterpret_cast<float*>(sm + OFF_AMAX) + (ti & 1) * 256;
-        am[h * 128 + r] = m;
+        const uint32_t am = smem_u32(sm + OFF_AMAX) + (ti & 1) * 1024 + 4 * r;
+        sts(am + 512 * h, m);
         __syncwarp();
         if (lane == 0) mbar_arrive(exch);
         ok = wait_warp(exch, uint32_t(ti & 1));
         if (!ok) break;
-        m = block_amax(max_nan(m, am[(h ^ 1) * 128 + r]));
+        m = block_amax(max_nan(m, lds(am + 512 * (h ^ 1))));
         const Quotient quo(m);
         const int n0 = nt * 128 + 64 * h;
         if (in) {
@@ -475,6 +519,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
   }
 
+  bulk_wait_read<0>();  // shared memory is read out
   if (!ok) record_error(QUAROT_ERR_TIMEOUT);
   fence_before_sync();
   __syncthreads();
@@ -524,7 +569,7 @@ struct Cfg {
 template <bool GATED, int TN, typename T>
 __global__ void __launch_bounds__(NT, 2)
 narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW0,
-              const __grid_constant__ CUtensorMap tmW1, const float* __restrict__ as, const float* __restrict__ ws0,
+              const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmY, const float* __restrict__ as, const float* __restrict__ ws0,
               const float* __restrict__ ws1, int M, int N, int nkb, T* __restrict__ y, uint8_t* __restrict__ q,
               float* __restrict__ qs) {
   using C = Cfg<GATED, TN>;
@@ -773,6 +818,17 @@ static bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t K,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The 16-bit output [rows, N], N % 8 == 0, in the boxes of 16 columns x 32 rows that an epilogue warp stores.
+static bool make_out_map(CUtensorMap* tm, void* base, int64_t rows, int64_t N) {
+  cuuint64_t gdim[2] = {cuuint64_t(N), cuuint64_t(rows)};
+  cuuint64_t gstride[1] = {cuuint64_t(2 * N)};
+  cuuint32_t box[2] = {16, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -803,10 +859,12 @@ struct Args {
 template <typename Kern, typename T>
 static int launch(const Args& p, Kern* kern, AttrCache& attr, dim3 grid, int threads, int cluster, int smem, int a_box,
                   int w_box, T* y) {
-  CUtensorMap ta, t0, t1;
+  CUtensorMap ta, t0, t1, ty;
   if (!make_map(&ta, p.a, p.M, p.K, a_box) || !make_map(&t0, p.w0, p.N, p.K, w_box)) return QUAROT_ERR_CUDA;
   if (p.w1 == nullptr) t1 = t0;
   else if (!make_map(&t1, p.w1, p.N, p.K, w_box)) return QUAROT_ERR_CUDA;
+  if (y == nullptr || p.N % 8 != 0) ty = t0;
+  else if (!make_out_map(&ty, y, p.M, p.N)) return QUAROT_ERR_CUDA;
   if (!smem_attr_once(kern, smem, attr)) return QUAROT_ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -820,7 +878,7 @@ static int launch(const Args& p, Kern* kern, AttrCache& attr, dim3 grid, int thr
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, t0, t1, p.as, p.ws0, p.ws1, int(p.M), int(p.N),
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, t0, t1, ty, p.as, p.ws0, p.ws1, int(p.M), int(p.N),
                                            int((p.K + BK - 1) / BK), y, p.q, p.qs);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }
