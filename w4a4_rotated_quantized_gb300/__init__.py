@@ -23,7 +23,6 @@ e4m3 codes with a scale for each block of 128.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -547,21 +546,41 @@ _DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # QUAROT_FP16, QUAROT_BF16
 _E4M3 = torch.float8_e4m3fn
 
 
-def _on(dev):
-    """The tensors' device as the current one, where it is another."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+# A decode step makes a handful of these calls with microseconds of GPU work
+# each: the checks read each attribute once, and only a tensor that fails is
+# looked at again, by the checks that say what is wrong with it.
+def _fp8_call(name, dev, stream, *args):
+    """Calls the entry point on `stream` (default: the current one) with the
+    tensors' device current, and checks its status."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    fn = getattr(_lib if _lib is not None else load(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != QUAROT_OK:
+        raise QuarotError(st, name)
 
 
-def _need_16bit(t, name, dev=None, dtype=None) -> int:
+def _rows(t, name, dev=None, dtype=None) -> int:
     """A 2-D fp16 or bf16 input read row by row; returns its row stride."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous()
+            and (t.dtype in _DTYPES if dtype is None else t.dtype is dtype) and (dev is None or t.get_device() == dev)):
+        return t.shape[1]
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise QuarotError(1, f"{name} must be an fp16 or bf16 CUDA tensor")
-    return _need_rows(t, t.dtype if dtype is None else dtype, name, dev)
+    return _need_rows(t, t.dtype if dtype is None else dtype, name, None if dev is None else torch.device("cuda", dev))
 
 
-def _need_shape(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+def _dense(t, dtype, shape, name, dev):
+    """A contiguous tensor of this type and shape on CUDA device `dev`; its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, dtype, name, torch.device("cuda", dev))
+    if t.shape != shape:
+        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
 
 
 def _blocks(n: int) -> int:
@@ -572,41 +591,35 @@ def _fp8_outputs(M, d, scale_shape, q_out, scale_out, dev):
     if q_out is None:
         q_out = torch.empty((M, d), dtype=_E4M3, device=dev)
     else:
-        _need(q_out, _E4M3, "q_out", dev)
-        _need_shape(q_out, (M, d), "q_out")
+        _dense(q_out, _E4M3, (M, d), "q_out", dev.index)
     if scale_out is None:
         scale_out = torch.empty(scale_shape, dtype=torch.float32, device=dev)
     else:
-        _need(scale_out, torch.float32, "scale_out", dev)
-        _need_shape(scale_out, scale_shape, "scale_out")
+        _dense(scale_out, torch.float32, scale_shape, "scale_out", dev.index)
     return q_out, scale_out
 
 
 def quarot_quant_fp8(x, q_out=None, scale_out=None, stream=None):
     """x: fp16 or bf16 [M, d], rows contiguous (any row stride) -> (e4m3 codes
     [M, d], fp32 scales [ceil(d / 128), M], one for each token and 128 columns)."""
-    ld = _need_16bit(x, "x")
-    dev = x.device
+    ld = _rows(x, "x")
     M, d = x.shape
+    dev = x.device
     q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
-    with _on(dev):
-        st = load().quarot_quant_fp8(_ptr(x), _DTYPES[x.dtype], M, d, ld, _ptr(q_out), _ptr(scale_out),
-                                     _stream(stream, dev))
-    _check(st, "quarot_quant_fp8")
+    _fp8_call("quarot_quant_fp8", dev.index, stream, x.data_ptr(), _DTYPES[x.dtype], M, d, ld, q_out.data_ptr(),
+              scale_out.data_ptr())
     return q_out, scale_out
 
 
 def quarot_quant_fp8_block(w, q_out=None, scale_out=None, stream=None):
     """w: fp16 or bf16 [N, K], rows contiguous (any row stride) -> (e4m3 codes
     [N, K], fp32 scales [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block)."""
-    ld = _need_16bit(w, "w")
-    dev = w.device
+    ld = _rows(w, "w")
     N, K = w.shape
+    dev = w.device
     q_out, scale_out = _fp8_outputs(N, K, (_blocks(N), _blocks(K)), q_out, scale_out, dev)
-    with _on(dev):
-        st = load().quarot_quant_fp8_block(_ptr(w), _DTYPES[w.dtype], N, K, ld, _ptr(q_out), _ptr(scale_out),
-                                           _stream(stream, dev))
-    _check(st, "quarot_quant_fp8_block")
+    _fp8_call("quarot_quant_fp8_block", dev.index, stream, w.data_ptr(), _DTYPES[w.dtype], N, K, ld, q_out.data_ptr(),
+              scale_out.data_ptr())
     return q_out, scale_out
 
 
@@ -618,81 +631,81 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
     [M, d], rows contiguous (any row stride); weight [d] or None.
     residual_out may be x or residual itself; without a residual h is x,
     and is copied only if residual_out is given."""
-    ld = _need_16bit(x, "x")
-    dev, dt = x.device, x.dtype
+    ld = _rows(x, "x")
     M, d = x.shape
+    dev, dt = x.device, x.dtype
+    di = dev.index
     ld_r = ld_h = d
+    res = h = w = None
     if residual is not None:
-        ld_r = _need_rows(residual, dt, "residual", dev)
-        _need_shape(residual, (M, d), "residual")
+        ld_r = _rows(residual, "residual", di, dt)
+        if residual.shape != x.shape:
+            raise QuarotError(1, f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+        res = residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty((M, d), dtype=dt, device=dev)
     if residual_out is not None:
-        ld_h = _need_rows(residual_out, dt, "residual_out", dev)
-        _need_shape(residual_out, (M, d), "residual_out")
+        ld_h = _rows(residual_out, "residual_out", di, dt)
+        if residual_out.shape != x.shape:
+            raise QuarotError(1, f"residual_out has shape {tuple(residual_out.shape)}, expected {tuple(x.shape)}")
+        h = residual_out.data_ptr()
     if weight is not None:
-        _need(weight, dt, "weight", dev)
-        _need_shape(weight, (d,), "weight")
+        w = _dense(weight, dt, (d,), "weight", di)
     q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
-    with _on(dev):
-        st = load().quarot_add_rmsnorm_quant_fp8(_ptr(x), ld, _ptr(residual), ld_r, _ptr(weight), _DTYPES[dt], M, d,
-                                                 float(eps), _ptr(residual_out), ld_h, _ptr(q_out), _ptr(scale_out),
-                                                 _stream(stream, dev))
-    _check(st, "quarot_add_rmsnorm_quant_fp8")
+    _fp8_call("quarot_add_rmsnorm_quant_fp8", di, stream, x.data_ptr(), ld, res, ld_r, w, _DTYPES[dt], M, d,
+              float(eps), h, ld_h, q_out.data_ptr(), scale_out.data_ptr())
     return q_out, scale_out, x if residual_out is None else residual_out
 
 
-def _need_fp8_operand(codes, scale, name, weights, dev=None):
-    _need(codes, _E4M3, name, dev)
-    _need(scale, torch.float32, name + " scale", codes.device)
-    if codes.dim() != 2:
-        raise QuarotError(1, f"{name} must be 2-D")
-    rows, K = codes.shape
-    _need_shape(scale, (_blocks(rows), _blocks(K)) if weights else (_blocks(K), rows), name + " scale")
+def _fp8_weight(w_q, w_scale, name, K, dev):
+    """Addresses of weight codes [N, K] and their scales."""
+    if not isinstance(w_q, torch.Tensor) or w_q.dim() != 2 or w_q.shape[1] != K:
+        raise QuarotError(1, f"{name} must be 2-D with {K} columns")
+    N = w_q.shape[0]
+    return (_dense(w_q, _E4M3, (N, K), name, dev),
+            _dense(w_scale, torch.float32, (_blocks(N), _blocks(K)), name + " scale", dev))
+
+
+def _fp8_tokens(a_q, a_scale):
+    """(addresses of token codes [M, K] and their scales, M, K, device)."""
+    if not isinstance(a_q, torch.Tensor) or not a_q.is_cuda or a_q.dim() != 2:
+        raise QuarotError(1, "a_q must be a 2-D CUDA tensor")
+    M, K = a_q.shape
+    dev = a_q.get_device()
+    return (_dense(a_q, _E4M3, (M, K), "a_q", dev), _dense(a_scale, torch.float32, (_blocks(K), M), "a_q scale", dev),
+            M, K, dev)
 
 
 def quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y=None, out_dtype=torch.float16, stream=None):
     """Token codes [M, K] and scales x weight codes [N, K] and scales ->
     y fp16 or bf16 [M, N] (``out_dtype``, or the type of ``y``)."""
-    _need_fp8_operand(a_q, a_scale, "a_q", False)
-    dev = a_q.device
-    _need_fp8_operand(w_q, w_scale, "w_q", True, dev)
-    M, K = a_q.shape
+    a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
+    w, sw = _fp8_weight(w_q, w_scale, "w_q", K, dev)
     N = w_q.shape[0]
-    if w_q.shape[1] != K:
-        raise QuarotError(1, "a_q and w_q disagree on K")
     if y is None:
         if out_dtype not in _DTYPES:
             raise QuarotError(1, "out_dtype must be float16 or bfloat16")
-        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+        y = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
     else:
-        if y.dtype not in _DTYPES:
+        if not isinstance(y, torch.Tensor) or y.dtype not in _DTYPES:
             raise QuarotError(1, "y must be fp16 or bf16")
-        _need(y, y.dtype, "y", dev)
-        _need_shape(y, (M, N), "y")
-    with _on(dev):
-        st = load().quarot_fp8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(y),
-                                    _DTYPES[y.dtype], _stream(stream, dev))
-    _check(st, "quarot_fp8_gemm")
+        _dense(y, y.dtype, (M, N), "y", dev)
+    _fp8_call("quarot_fp8_gemm", dev, stream, a, sa, w, sw, M, N, K, y.data_ptr(), _DTYPES[y.dtype])
     return y
 
 
 def quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out=None, scale_out=None, stream=None):
     """silu(A Wg^T) * (A Wu^T) of block-scaled codes (weights [I, K]) ->
     (e4m3 codes [M, I], fp32 scales [ceil(I / 128), M])."""
-    _need_fp8_operand(a_q, a_scale, "a_q", False)
-    dev = a_q.device
-    _need_fp8_operand(wg_q, wg_scale, "wg_q", True, dev)
-    _need_fp8_operand(wu_q, wu_scale, "wu_q", True, dev)
-    M, K = a_q.shape
+    a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
+    g, sg = _fp8_weight(wg_q, wg_scale, "wg_q", K, dev)
+    u, su = _fp8_weight(wu_q, wu_scale, "wu_q", K, dev)
     I = wg_q.shape[0]
-    if wg_q.shape[1] != K or wu_q.shape != wg_q.shape:
-        raise QuarotError(1, "a_q, wg_q and wu_q disagree on their shapes")
-    q_out, scale_out = _fp8_outputs(M, I, (_blocks(I), M), q_out, scale_out, dev)
-    with _on(dev):
-        st = load().quarot_fp8_gated_gemm(_ptr(a_q), _ptr(a_scale), _ptr(wg_q), _ptr(wg_scale), _ptr(wu_q),
-                                          _ptr(wu_scale), M, I, K, _ptr(q_out), _ptr(scale_out), _stream(stream, dev))
-    _check(st, "quarot_fp8_gated_gemm")
+    if wu_q.shape[0] != I:
+        raise QuarotError(1, "wg_q and wu_q disagree on their shapes")
+    q_out, scale_out = _fp8_outputs(M, I, (_blocks(I), M), q_out, scale_out, a_q.device)
+    _fp8_call("quarot_fp8_gated_gemm", dev, stream, a, sa, g, sg, u, su, M, I, K, q_out.data_ptr(),
+              scale_out.data_ptr())
     return q_out, scale_out
 
 
