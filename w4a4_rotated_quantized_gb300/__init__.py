@@ -565,9 +565,13 @@ def _fp8_call(name, dev, stream, *args):
 
 def _rows(t, name, dev=None, dtype=None) -> int:
     """A 2-D fp16 or bf16 input read row by row; returns its row stride."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous()
-            and (t.dtype in _DTYPES if dtype is None else t.dtype is dtype) and (dev is None or t.get_device() == dev)):
-        return t.shape[1]
+    try:
+        d = t.get_device()  # -1 off the GPU
+        if (d >= 0 if dev is None else d == dev) and t.is_contiguous() and t.dim() == 2 and (
+                t.dtype in _DTYPES if dtype is None else t.dtype is dtype):
+            return t.shape[1]
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise QuarotError(1, f"{name} must be an fp16 or bf16 CUDA tensor")
     return _need_rows(t, t.dtype if dtype is None else dtype, name, None if dev is None else torch.device("cuda", dev))
@@ -575,12 +579,13 @@ def _rows(t, name, dev=None, dtype=None) -> int:
 
 def _dense(t, dtype, shape, name, dev):
     """A contiguous tensor of this type and shape on CUDA device `dev`; its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
-            and t.is_contiguous()):
-        _need(t, dtype, name, torch.device("cuda", dev))
-    if t.shape != shape:
-        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name, torch.device("cuda", dev))
+    raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _blocks(n: int) -> int:

@@ -196,6 +196,11 @@ __device__ __forceinline__ float lds(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float lds_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void sts(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -237,6 +242,10 @@ __device__ __forceinline__ float silu(float g) {
 // MMA loop, barriers are this CTA's own (CTA pairs, whose MMAs need less shared
 // memory traffic, lose more to their remote barriers than they gain), and a
 // k-block's scale is read from shared memory while the one before is summed.
+//
+// SPLIT: fewer tiles than SMs.  A cluster takes one tile, each CTA a share of
+// the depth; the sums are joined through distributed shared memory in rank
+// order (no workspace, no atomics, the same bits every time).
 namespace wide {
 
 constexpr int S = 4;  // stages
@@ -259,7 +268,22 @@ constexpr uint32_t TMEM_COLS = 512;
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 
-template <bool GATED, typename T>
+// A warp's 32 rows x 16 columns through one of its two buffers to a TMA store.
+__device__ __forceinline__ void store16(const CUtensorMap* tm, int x, int y, uint32_t buf, int lane, const uint32_t* o,
+                                        bool in) {
+  bulk_wait_read<1>();  // of the lane that stores; the others have none
+  __syncwarp();
+  sts128(buf + 32u * lane, o);
+  sts128(buf + 32u * lane + 16, o + 4);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    if (in) tma_store(tm, x, y, buf);
+    bulk_commit();
+  }
+}
+
+template <bool GATED, bool SPLIT, typename T>
 __global__ void __launch_bounds__(NT, 1)
 wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW0,
             const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmY, const float* __restrict__ as, const float* __restrict__ ws0,
@@ -283,6 +307,10 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   constexpr int TN = GATED ? 128 : 256;  // output columns of a tile
   const int tiles_n = (N + TN - 1) / TN, nblk = (N + BLK - 1) / BLK;
   const int n_tiles = ((M + 127) / 128) * tiles_n;
+  // tiles of this CTA, and its k-blocks of each
+  const int ranks = SPLIT ? int(cluster_size()) : 1, rank = SPLIT ? int(cluster_rank()) : 0;
+  const int tile0 = SPLIT ? int(blockIdx.x) / ranks : int(blockIdx.x), tstep = SPLIT ? n_tiles : int(gridDim.x);
+  const int kb0 = SPLIT ? nkb * rank / ranks : 0, kb1 = SPLIT ? nkb * (rank + 1) / ranks : nkb;
 
   if (threadIdx.x == 0) {
     prefetch_map(&tmA);
@@ -316,9 +344,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       if (elect_one()) {
         int s = 0;
         uint32_t par = 0, it = 0;
-        for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x)) {
+        for (int tile = tile0; ok && tile < n_tiles; tile += tstep) {
           const int m0 = tile / tiles_n * 128, w0 = tile % tiles_n * TN;
-          for (int kb = 0; kb < nkb; ++kb, ++it) {
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
             ok = wait_one(empty + 8 * s, par ^ 1u);
             if (!ok) break;
             const uint32_t bar = full + 8 * s, st = smem_u32(sm + s * STAGE);
@@ -339,8 +367,8 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         const uint64_t desc = sw128_desc(smem_u32(sm));
         int s = 0;
         uint32_t par = 0, it = 0;
-        for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x))
-          for (int kb = 0; kb < nkb; ++kb, ++it) {
+        for (int tile = tile0; ok && tile < n_tiles; tile += tstep)
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const uint32_t b = it & 1;
             ok = wait_one(full + 8 * s, par) && wait_one(acc_empty + 8 * b, ((it >> 1) & 1) ^ 1u);
             if (!ok) break;
@@ -363,12 +391,12 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       // of gate and up).
       const uint32_t sc = smem_u32(sm + OFF_SCALE) + 4 * lane;
       uint32_t it = 0;
-      for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x)) {
+      for (int tile = tile0; ok && tile < n_tiles; tile += tstep) {
         const int nt = tile % tiles_n, m = tile / tiles_n * 128 + lane;
-        const float* pa = as + m;
-        const float* pw = lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
-                                    : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const float* pa = as + size_t(kb0) * M + m;
+        const float* pw = kb0 + (lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
+                                    : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb));
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           if (it % CH == 0) ok = wait_warp(sc_empty + 8 * (it / CH & 1), (it / (2 * CH) & 1) ^ 1u);
           if (!ok) break;
           const uint32_t d = sc + it % (2 * CH) * (SLOT * 4);
@@ -406,16 +434,16 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         mbar_arrive_if(sc_empty + 8 * (it / CH & 1), lane == 0);
       }
     };
-    const uint32_t last = uint32_t((n_tiles - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x)) * uint32_t(nkb);
-    next_scales();
-    for (int tile = int(blockIdx.x); ok && tile < n_tiles; tile += int(gridDim.x), ++ti) {
+    const uint32_t last = uint32_t((n_tiles - tile0 + tstep - 1) / tstep) * uint32_t(kb1 - kb0);
+    if (last > 0) next_scales();
+    for (int tile = tile0; ok && tile < n_tiles; tile += tstep, ++ti) {
       const int gm = tile / tiles_n * 128 + r;
       const int nt = tile % tiles_n;
       const bool in = gm < M;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t b = it & 1;
         ok = ok && wait_warp(acc_full + 8 * b, (it >> 1) & 1);
         if (!ok) break;
@@ -441,6 +469,19 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 make_float2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), s2, acc[CW / 2 * c + j]);
         }
       }
+      if constexpr (SPLIT) {
+        // partial sums to where the stages were (all read by now): [column][token]
+        if (ok) {
+          const uint32_t part = smem_u32(sm) + 4 * r + 512 * ((GATED ? 64 : 128) * h);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const uint32_t d = part + 512 * (2 * i + (GATED && i >= 32 ? 64 : 0));
+            sts(d, acc[i].x);
+            sts(d + 512, acc[i].y);
+          }
+        }
+        break;
+      }
       if (!ok) break;
       if constexpr (!GATED) {
         const int n0 = nt * 256 + 128 * h;
@@ -455,16 +496,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = from_f2<T>(acc[8 * c + j]);
-            bulk_wait_read<1>();  // of the lane that stores; the others have none
-            __syncwarp();
-            sts128(buf + 32u * lane, o);
-            sts128(buf + 32u * lane + 16, o + 4);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              if (row0 < M && n0 + 16 * c < N) tma_store(&tmY, n0 + 16 * c, row0, buf);
-              bulk_commit();
-            }
+            store16(&tmY, n0 + 16 * c, row0, buf, lane, o, row0 < M && n0 + 16 * c < N);
           }
         } else {
           // rows of any alignment: through shared memory, a row's 32 columns by the 32 lanes
@@ -517,6 +549,96 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
       }
     }
+    if constexpr (SPLIT) {
+      // ---- the ranks' sums, in rank order, through distributed shared memory:
+      // 16 columns at a time, dealt out over the cluster's 2 * ranks warp sets
+      cluster_sync();
+      const int gm = tile0 / tiles_n * 128 + r, row0 = gm - lane, nt = tile0 % tiles_n;
+      const uint32_t part = smem_u32(sm) + 4 * r;
+      auto sum16 = [&](int col, float2 (&o)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = make_float2(0.f, 0.f);
+        for (int k = 0; k < ranks; ++k) {
+          const uint32_t src = mapa(part + 512 * col, uint32_t(k));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = __fadd2_rn(o[i], make_float2(lds_cluster(src + 1024 * i), lds_cluster(src + 1024 * i + 512)));
+        }
+      };
+      const int w0 = 2 * rank + h;
+      if constexpr (!GATED) {
+        int n = 0;
+        for (int c = w0; c < 16 && row0 < M; c += 2 * ranks, ++n) {
+          const int gn = nt * 256 + 16 * c;
+          if (gn >= N) break;
+          float2 f[8];
+          sum16(16 * c, f);
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = from_f2<T>(f[i]);
+          if ((N & 7) == 0) {
+            const uint32_t buf = smem_u32(sm + OFF_STG) + uint32_t(((warp - EPI0) * 2 + (n & 1)) * 1024);
+            store16(&tmY, gn, row0, buf, lane, o, true);
+          } else {
+            uint16_t* stg = reinterpret_cast<uint16_t*>(sm + OFF_STG) + (warp - EPI0) * 32 * STG_LD;
+            uint16_t* y16 = reinterpret_cast<uint16_t*>(y);
+            const int cc = gn + (lane & 15), rows = min(32, M - row0);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(stg + lane * STG_LD + 2 * i) = o[i];
+            __syncwarp();
+            if (cc < N)
+              for (int i = lane >> 4; i < rows; i += 2) y16[size_t(row0 + i) * N + cc] = stg[i * STG_LD + (lane & 15)];
+          }
+        }
+      } else {
+        float2 z[2][8];  // at most two of the eight chunks
+        float m = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int c = w0 + 2 * ranks * n;
+          if (c >= 8 || row0 >= M) break;
+          float2 u[8];
+          sum16(16 * c, z[n]);
+          sum16(128 + 16 * c, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            z[n][i] = make_float2(silu(z[n][i].x) * u[i].x, silu(z[n][i].y) * u[i].y);
+            m = max_nan(m, max_nan(fabsf(z[n][i].x), fabsf(z[n][i].y)));
+          }
+        }
+        const uint32_t am = smem_u32(sm + OFF_AMAX) + 4 * r;
+        sts(am + 512 * h, m);
+        cluster_sync();
+        if (row0 < M) {
+          for (int k = 0; k < ranks; ++k) {
+            const uint32_t src = mapa(am, uint32_t(k));
+            m = max_nan(m, max_nan(lds_cluster(src), lds_cluster(src + 512)));
+          }
+          m = block_amax(m);
+          const Quotient quo(m);
+          if (gm < M && w0 == 0) qs[size_t(nt) * M + gm] = block_scale(m);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int c = w0 + 2 * ranks * n, gn = nt * 128 + 16 * c;
+            if (c < 8 && gn < N && gm < M) {
+              uint4 o;
+              o.x = cvt_e4m3x4(quo(z[n][0]), quo(z[n][1]));
+              o.y = cvt_e4m3x4(quo(z[n][2]), quo(z[n][3]));
+              o.z = cvt_e4m3x4(quo(z[n][4]), quo(z[n][5]));
+              o.w = cvt_e4m3x4(quo(z[n][6]), quo(z[n][7]));
+              *reinterpret_cast<uint4*>(q + size_t(gm) * N + gn) = o;
+            }
+          }
+        }
+      }
+      cluster_sync();  // this CTA's sums have been read
+    }
+  }
+  if (SPLIT && warp < EPI0) {  // the barriers that the epilogue warps pass
+    cluster_sync();
+    if (GATED) cluster_sync();
+    cluster_sync();
   }
 
   bulk_wait_read<0>();  // shared memory is read out
@@ -553,7 +675,7 @@ struct Cfg {
   static constexpr int KC = GATED ? 2 : 4;  // k-blocks whose scales a warp stages at a time
   static constexpr int W_BYTES = 128 * BK, A_BYTES = TN * BK;
   static constexpr int STAGE = NW * W_BYTES + A_BYTES;
-  static constexpr int S = TN == 128 ? 3 : GATED ? (TN == 64 ? 2 : 3) : (TN == 64 ? 4 : TN == 32 ? 5 : 6);
+  static constexpr int S = GATED ? 3 : TN == 64 ? 4 : TN == 32 ? 5 : 6;
   static constexpr uint32_t COLS = 2 * NW * TN < 32 ? 32 : 2 * NW * TN;  // two accumulator buffers
   static constexpr int OFF_BAR = S * STAGE;
   static constexpr int NBAR = 2 * S + 5;  // full empty acc_full[2] acc_empty[2] drain
@@ -863,7 +985,7 @@ static int launch(const Args& p, Kern* kern, AttrCache& attr, dim3 grid, int thr
   if (!make_map(&ta, p.a, p.M, p.K, a_box) || !make_map(&t0, p.w0, p.N, p.K, w_box)) return QUAROT_ERR_CUDA;
   if (p.w1 == nullptr) t1 = t0;
   else if (!make_map(&t1, p.w1, p.N, p.K, w_box)) return QUAROT_ERR_CUDA;
-  if (y == nullptr || p.N % 8 != 0) ty = t0;
+  if (threads != wide::NT || y == nullptr || p.N % 8 != 0) ty = t0;
   else if (!make_out_map(&ty, y, p.M, p.N)) return QUAROT_ERR_CUDA;
   if (!smem_attr_once(kern, smem, attr)) return QUAROT_ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
@@ -891,26 +1013,44 @@ static int launch_narrow(const Args& p, int cluster) {
                 narrow::Cfg<GATED, TN>::SMEM, TN, 128, static_cast<T*>(p.y));
 }
 
+// Over how many CTAs a tile's depth is split: as many as find an SM at once,
+// with two k-blocks each at least.  A cluster of 8 finds room on 4/5 of the SMs
+// only (the SMs of a GPC are not a multiple of 8), one of 4 on 18/19.
+static int split_ranks(int64_t tiles, int64_t nkb, int sms) {
+  if (tiles * 8 <= sms * 15 / 19 && nkb >= 16) return 8;
+  if (tiles * 4 <= sms * 18 / 19 && nkb >= 8) return 4;
+  if (tiles * 2 <= sms && nkb >= 4) return 2;
+  return 1;
+}
+
 template <bool GATED, typename T>
 static int run(const Args& p) {
   if (!get_encoder()) return QUAROT_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return QUAROT_ERR_CUDA;
-  constexpr int kNarrow = GATED ? 64 : 128;
+  // Narrow up to here: at 64 tokens (gated: 32) it and the split wide form take
+  // the same time; beyond, a token tile's sums crowd out its stages (50 MB of
+  // weights: 15.8 us at 64 tokens, 35 at 100, the wide form 16 to 19 and 17).
+  constexpr int kNarrow = GATED ? 32 : 64;
   const int64_t wbs = (p.N + 127) / 128, nkb = (p.K + BK - 1) / BK;
   if (p.M <= kNarrow && wbs <= (int64_t(1) << 27)) {
     int cl = 1;
     while (cl < 8 && wbs * cl * 2 <= 2 * sms && nkb / (2 * cl) >= 4) cl *= 2;
     if (p.M <= 16) return launch_narrow<GATED, 16, T>(p, cl);
     if (p.M <= 32) return launch_narrow<GATED, 32, T>(p, cl);
-    if (p.M <= 64) return launch_narrow<GATED, 64, T>(p, cl);
-    if constexpr (!GATED) return launch_narrow<GATED, 128, T>(p, cl);
+    if constexpr (!GATED) return launch_narrow<GATED, 64, T>(p, cl);
   }
-  static AttrCache attr;
   constexpr int TN = GATED ? 128 : 256;
   const int64_t tiles = ((p.M + 127) / 128) * ((p.N + TN - 1) / TN);
-  return launch(p, wide::wide_kernel<GATED, T>, attr, dim3(unsigned(tiles < sms ? tiles : sms)), wide::NT, 1, wide::SMEM,
-                128, 128, static_cast<T*>(p.y));
+  const int ranks = split_ranks(tiles, nkb, sms);
+  if (ranks > 1) {
+    static AttrCache attr;
+    return launch(p, wide::wide_kernel<GATED, true, T>, attr, dim3(unsigned(tiles * ranks)), wide::NT, ranks, wide::SMEM,
+                  128, 128, static_cast<T*>(p.y));
+  }
+  static AttrCache attr;
+  return launch(p, wide::wide_kernel<GATED, false, T>, attr, dim3(unsigned(tiles < sms ? tiles : sms)), wide::NT, 1,
+                wide::SMEM, 128, 128, static_cast<T*>(p.y));
 }
 
 }  // namespace gemm
