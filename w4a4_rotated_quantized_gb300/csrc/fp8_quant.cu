@@ -33,6 +33,36 @@ struct Chunk {
   }
 };
 
+// Abs-max of 16-bit pairs, as they are (a NaN wins); exact, so the same as in fp32.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+  using V = __half2;
+  static __device__ __forceinline__ V abs_max(V a, V b) { return __hmax2_nan(__habs2(a), __habs2(b)); }
+  static __device__ __forceinline__ float2 value(V a) { return __half22float2(a); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static __device__ __forceinline__ V abs_max(V a, V b) { return __hmax2_nan(__habs2(a), __habs2(b)); }
+  static __device__ __forceinline__ float2 value(V a) { return __bfloat1622float2(a); }
+};
+template <typename T, int N>
+__device__ __forceinline__ float raw_amax(const uint4 (&r)[N]) {
+  using P = Pair<T>;
+  typename P::V m[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const typename P::V* v = reinterpret_cast<const typename P::V*>(&r[i]);
+    m[i] = P::abs_max(P::abs_max(v[0], v[1]), P::abs_max(v[2], v[3]));
+  }
+#pragma unroll
+  for (int i = 1; i < N; ++i) m[0] = P::abs_max(m[0], m[i]);
+  const float2 f = P::value(m[0]);
+  return max_nan(f.x, f.y);
+}
+
 // Maximum over the 16 lanes (one block of 128 columns) of a half warp.
 __device__ __forceinline__ float half_warp_max(float m) {
 #pragma unroll
@@ -41,36 +71,44 @@ __device__ __forceinline__ float half_warp_max(float m) {
 }
 
 // ------------------------------------------------------------------ tokens
-// A half warp owns a block: 16 lanes x 8 columns, one 16-byte load each.  U
-// blocks per half warp, all loaded before the first is quantized.  Blocks are
-// numbered along the rows, so a warp reads 512 contiguous bytes.
-constexpr int QT = 256, QU = 4;
+// Eight lanes own a block, 16 columns each (two 16-byte loads, one 16-byte
+// store); a lane group takes U blocks, all loaded before the first is
+// quantized.  Blocks are numbered along the rows, so a warp reads 1 KB without
+// a gap.
+constexpr int QT = 256, QU = 2, QG = QT / 8;
 
 template <typename T>
 __global__ void __launch_bounds__(QT) quant_tokens_kernel(const T* __restrict__ x, uint32_t M, uint32_t d, int64_t ld,
                                                           uint32_t nb, uint32_t total, uint8_t* __restrict__ q,
                                                           float* __restrict__ scale) {
-  const uint32_t l = threadIdx.x & 15u, hw = threadIdx.x >> 4;
-  uint4 raw[QU];
-  uint32_t row[QU], blk[QU];
+  const uint32_t l = threadIdx.x & 7u, g = threadIdx.x >> 3;
+  uint4 raw[QU][2];
+  uint32_t row[QU], col[QU];
   bool in[QU];
 #pragma unroll
   for (int u = 0; u < QU; ++u) {
-    const uint32_t i = (blockIdx.x * QU + u) * (QT / 16) + hw;
+    const uint32_t i = (blockIdx.x * QU + u) * QG + g;
     row[u] = i / nb;
-    blk[u] = i - row[u] * nb;
-    in[u] = i < total && blk[u] * BLK + l * 8 < d;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (in[u]) raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + int64_t(row[u]) * ld + blk[u] * BLK + l * 8));
+    col[u] = (i - row[u] * nb) * BLK + l * 16;
+    in[u] = i < total && col[u] < d;
+    raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+    if (in[u]) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + int64_t(row[u]) * ld + col[u]);
+      raw[u][0] = __ldg(src);
+      raw[u][1] = __ldg(src + 1);
+    }
   }
 #pragma unroll
   for (int u = 0; u < QU; ++u) {
-    const Chunk<T> c(raw[u]);
-    const float m = block_amax(half_warp_max(c.amax()));
-    const uint2 o = c.codes(Quotient(m));
+    float m = raw_amax<T>(raw[u]);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = block_amax(m);
+    const Quotient quo(m);
+    const uint2 a = Chunk<T>(raw[u][0]).codes(quo), b = Chunk<T>(raw[u][1]).codes(quo);
     if (in[u]) {
-      *reinterpret_cast<uint2*>(q + size_t(row[u]) * d + blk[u] * BLK + l * 8) = o;
-      if (l == 0) scale[size_t(blk[u]) * M + row[u]] = block_scale(m);
+      *reinterpret_cast<uint4*>(q + size_t(row[u]) * d + col[u]) = make_uint4(a.x, a.y, b.x, b.y);
+      if (l == 0) scale[size_t(col[u] / BLK) * M + row[u]] = block_scale(m);
     }
   }
 }
@@ -88,11 +126,9 @@ __global__ void __launch_bounds__(256) quant_block_kernel(const T* __restrict__ 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (c0 < d && r0 + 16 * i < N) raw[i] = __ldcs(reinterpret_cast<const uint4*>(x + int64_t(r0 + 16 * i) * ld + c0));
+    if (c0 < d && r0 + 16 * i < N) raw[i] = __ldg(reinterpret_cast<const uint4*>(x + int64_t(r0 + 16 * i) * ld + c0));
   }
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, Chunk<T>(raw[i]).amax());
+  float m = raw_amax<T>(raw);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
@@ -136,7 +172,7 @@ __global__ void norm_quant_kernel(const T* x, int64_t ld_x, const T* res, int64_
       const uint32_t c = base + u * step + threadIdx.x * 8u;
       a[u] = b[u] = g[u] = make_uint4(0, 0, 0, 0);
       if (c < d) {
-        a[u] = __ldcs(reinterpret_cast<const uint4*>(xr + c));
+        a[u] = *reinterpret_cast<const uint4*>(xr + c);
         if constexpr (RES) b[u] = *reinterpret_cast<const uint4*>(rr + c);
         if constexpr (WGT) g[u] = __ldg(reinterpret_cast<const uint4*>(w + c));
       }
@@ -225,7 +261,7 @@ extern "C" int quarot_quant_fp8(const void* x, int dtype, int64_t M, int64_t d, 
   const int e = check_matrix(x, dtype, M, d, ld_x, q_out, scale_out);
   if (e != QUAROT_OK || M == 0) return e;
   const uint32_t nb = uint32_t((d + BLK - 1) / BLK), total = uint32_t(M) * nb;
-  const unsigned grid = (total + QU * (QT / 16) - 1) / (QU * (QT / 16));
+  const unsigned grid = (total + QU * QG - 1) / (QU * QG);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == QUAROT_FP16)
     quant_tokens_kernel<__half><<<grid, QT, 0, st>>>(static_cast<const __half*>(x), uint32_t(M), uint32_t(d), ld_x, nb,
