@@ -196,6 +196,11 @@ __device__ __forceinline__ float lds(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ float lds_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -786,7 +791,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       for (int j = 0; j < TN / 2; ++j) acc[p][j] = make_float2(0.f, 0.f);
     // scales a_scale w_scale of KC k-blocks, in the warp's own rows of shared
     // memory; the token scales of the next KC are already in registers
-    float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + warp * KC * NW * TN;
+    const uint32_t sc = smem_u32(sm + C::OFF_SC) + uint32_t(warp * KC * NW * TN * 4);
     constexpr int PL = KC * TN / 32;
     float pre[PL], pw[NW];
     const float* w0 = ws0 + size_t(wb) * nkb;
@@ -811,7 +816,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int e = 0; e < PL; ++e) {
           const int k = (e * 32 + lane) / TN, n = (e * 32 + lane) % TN;
 #pragma unroll
-          for (int p = 0; p < NW; ++p) sc[(k * NW + p) * TN + n] = pre[e] * __shfl_sync(0xffffffffu, pw[p], k);
+          for (int p = 0; p < NW; ++p)
+            sts(sc + 4 * uint32_t((k * NW + p) * TN + n), pre[e] * __shfl_sync(0xffffffffu, pw[p], k));
         }
         __syncwarp();
         fetch(kb + KC);
@@ -821,7 +827,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       fence_after_sync();
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
-        const float* scp = sc + (kc * NW + p) * TN;
+        const uint32_t scp = sc + 4 * uint32_t((kc * NW + p) * TN);
         constexpr int CW = TN < 32 ? 16 : 32;
 #pragma unroll
         for (int c = 0; c < TN / CW; ++c) {
@@ -833,7 +839,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           }
 #pragma unroll
           for (int j = 0; j < CW / 4; ++j) {
-            const float4 s4 = *reinterpret_cast<const float4*>(scp + c * CW + 4 * j);
+            const float4 s4 = lds128(scp + 4 * (c * CW + 4 * j));
             float2* a2 = &acc[p][(c * CW + 4 * j) / 2];
             a2[0] = __ffma2_rn(make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), make_float2(s4.x, s4.y), a2[0]);
             a2[1] = __ffma2_rn(make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), make_float2(s4.z, s4.w), a2[1]);
@@ -845,13 +851,13 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     // reads are over: the sums [NW][TN][128 weight rows] take their place
     // (after an expired wait the values are void, the producer drains below)
     if (ok) {
-      float* part = reinterpret_cast<float*>(sm);
+      const uint32_t part = smem_u32(sm) + 4 * (32 * warp + lane);
 #pragma unroll
       for (int p = 0; p < NW; ++p)
 #pragma unroll
         for (int j = 0; j < TN / 2; ++j) {
-          part[(p * TN + 2 * j) * 128 + 32 * warp + lane] = acc[p][j].x;
-          part[(p * TN + 2 * j + 1) * 128 + 32 * warp + lane] = acc[p][j].y;
+          sts(part + 512 * (p * TN + 2 * j), acc[p][j].x);
+          sts(part + 512 * (p * TN + 2 * j + 1), acc[p][j].y);
         }
     } else {
       record_error(QUAROT_ERR_TIMEOUT);
