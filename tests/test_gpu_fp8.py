@@ -207,7 +207,8 @@ def test_norm_edge_rows(q, dtype):
 GEMM = [(1, 1, 16), (1, 4096, 4096), (2, 127, 144), (5, 129, 128), (8, 1000, 12288), (17, 64, 272), (33, 4100, 1008),
         (64, 256, 256), (65, 300, 528), (100, 129, 4096), (128, 128, 384), (129, 1025, 640), (200, 777, 2064),
         (256, 512, 512), (257, 2048, 1040), (513, 1031, 272), (1000, 257, 4096), (1500, 2500, 400),
-        (2600, 2100, 144), (2601, 2101, 1168), (20000, 300, 128), (150, 40000, 272)]
+        (2600, 2100, 144), (2601, 2101, 1168), (20000, 300, 128), (150, 40000, 272),
+        (300, 8, 256), (4000, 1, 16), (3000, 24, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)

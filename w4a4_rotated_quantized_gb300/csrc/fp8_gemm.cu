@@ -201,6 +201,14 @@ __device__ __forceinline__ float4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float4 lds128_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, float2 a, float2 b) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
+}
 __device__ __forceinline__ float lds_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -273,6 +281,16 @@ constexpr uint32_t TMEM_COLS = 512;
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 
+// A k-block at depth x of 128 tokens from m0 and of the tile's weight rows.
+template <bool GATED>
+__device__ __forceinline__ void load_stage(const CUtensorMap* tmA, const CUtensorMap* tmW0, const CUtensorMap* tmW1,
+                                           uint32_t bar, uint32_t st, int m0, int w0, int x) {
+  mbar_arrive_expect_tx(bar, STAGE);
+  tma_load(st, tmA, x, m0, bar);
+  tma_load(st + A_BYTES, tmW0, x, w0, bar);
+  tma_load(st + A_BYTES + B_BYTES / 2, GATED ? tmW1 : tmW0, x, GATED ? w0 : w0 + 128, bar);
+}
+
 // A warp's 32 rows x 16 columns through one of its two buffers to a TMA store.
 __device__ __forceinline__ void store16(const CUtensorMap* tm, int x, int y, uint32_t buf, int lane, const uint32_t* o,
                                         bool in) {
@@ -334,6 +352,12 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     mbar_init(exch, 8);
     mbar_init(drain, 1);
     fence_barrier_init();
+    if constexpr (SPLIT) {  // a CTA is short-lived: its first loads do not wait for the set-up
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int s = 0; s < min(S, kb1 - kb0); ++s)
+        load_stage<GATED>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE), tile0 / tiles_n * 128,
+                          tile0 % tiles_n * TN, (kb0 + s) * BK);
+    }
   }
   if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), TMEM_COLS);
   fence_before_sync();
@@ -352,13 +376,11 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int tile = tile0; ok && tile < n_tiles; tile += tstep) {
           const int m0 = tile / tiles_n * 128, w0 = tile % tiles_n * TN;
           for (int kb = kb0; kb < kb1; ++kb, ++it) {
-            ok = wait_one(empty + 8 * s, par ^ 1u);
-            if (!ok) break;
-            const uint32_t bar = full + 8 * s, st = smem_u32(sm + s * STAGE);
-            mbar_arrive_expect_tx(bar, STAGE);
-            tma_load(st, &tmA, kb * BK, m0, bar);
-            tma_load(st + A_BYTES, &tmW0, kb * BK, w0, bar);
-            tma_load(st + A_BYTES + B_BYTES / 2, GATED ? &tmW1 : &tmW0, kb * BK, GATED ? w0 : w0 + 128, bar);
+            if (!SPLIT || it >= S) {
+              ok = wait_one(empty + 8 * s, par ^ 1u);
+              if (!ok) break;
+              load_stage<GATED>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE), m0, w0, kb * BK);
+            }
             if (++s == S) { s = 0; par ^= 1u; }
           }
         }
@@ -475,15 +497,13 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
       }
       if constexpr (SPLIT) {
-        // partial sums to where the stages were (all read by now): [column][token]
+        // partial sums to where the stages were (all read by now):
+        // [column / 4][token][4], so that four columns are one 16-byte access
         if (ok) {
-          const uint32_t part = smem_u32(sm) + 4 * r + 512 * ((GATED ? 64 : 128) * h);
+          const uint32_t part = smem_u32(sm) + 16 * r + 512 * ((GATED ? 64 : 128) * h);
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const uint32_t d = part + 512 * (2 * i + (GATED && i >= 32 ? 64 : 0));
-            sts(d, acc[i].x);
-            sts(d + 512, acc[i].y);
-          }
+          for (int i = 0; i < 32; ++i)
+            sts128(part + 2048 * (i + (GATED && i >= 16 ? 16 : 0)), acc[2 * i], acc[2 * i + 1]);
         }
         break;
       }
@@ -559,15 +579,21 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       // 16 columns at a time, dealt out over the cluster's 2 * ranks warp sets
       cluster_sync();
       const int gm = tile0 / tiles_n * 128 + r, row0 = gm - lane, nt = tile0 % tiles_n;
-      const uint32_t part = smem_u32(sm) + 4 * r;
+      const uint32_t part = smem_u32(sm) + 16 * r;
       auto sum16 = [&](int col, float2 (&o)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = make_float2(0.f, 0.f);
+#pragma unroll 4
         for (int k = 0; k < ranks; ++k) {
           const uint32_t src = mapa(part + 512 * col, uint32_t(k));
+          float4 f[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            o[i] = __fadd2_rn(o[i], make_float2(lds_cluster(src + 1024 * i), lds_cluster(src + 1024 * i + 512)));
+          for (int i = 0; i < 4; ++i) f[i] = lds128_cluster(src + 2048 * i);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __fadd2_rn(o[2 * i], make_float2(f[i].x, f[i].y));
+            o[2 * i + 1] = __fadd2_rn(o[2 * i + 1], make_float2(f[i].z, f[i].w));
+          }
         }
       };
       const int w0 = 2 * rank + h;
@@ -716,6 +742,15 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const int m0 = int(blockIdx.y) * TN;
   const int kb_lo = int(int64_t(nkb) * rank / ranks), kb_hi = int(int64_t(nkb) * (rank + 1) / ranks);
 
+  auto load_stage = [&](int s, int kb) {
+    const uint32_t bar = full + 8 * s, st = smem_u32(sm) + uint32_t(s * C::STAGE);
+    mbar_arrive_expect_tx(bar, C::STAGE);
+    tma_load(st, &tmW0, kb * BK, wb * 128, bar);
+    if (GATED) tma_load(st + C::W_BYTES, &tmW1, kb * BK, wb * 128, bar);
+    tma_load(st + NW * C::W_BYTES, &tmA, kb * BK, m0, bar);
+  };
+  const int early = min(S, kb_hi - kb_lo);  // stages loaded before the set-up is over
+
   if (threadIdx.x == 0) {
     prefetch_map(&tmA);
     prefetch_map(&tmW0);
@@ -730,6 +765,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     mbar_init(drain, 1);
     fence_barrier_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    for (int s = 0; s < early; ++s) load_stage(s, kb_lo + s);
   }
   if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), C::COLS);
   fence_before_sync();
@@ -741,16 +778,12 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     // ------------------------------------------------------------ producer
     bool ok = true;
     if (elect_one()) {
-      int i = 0;
-      for (int kb = kb_lo; kb < kb_hi; ++kb, ++i) {
+      int i = early;
+      for (int kb = kb_lo + early; kb < kb_hi; ++kb, ++i) {
         const int s = i % S;
         ok = wait_one(empty + 8 * s, uint32_t((i / S) & 1) ^ 1u);
         if (!ok) break;
-        const uint32_t bar = full + 8 * s, st = smem_u32(sm + s * C::STAGE);
-        mbar_arrive_expect_tx(bar, C::STAGE);
-        tma_load(st, &tmW0, kb * BK, wb * 128, bar);
-        if (GATED) tma_load(st + C::W_BYTES, &tmW1, kb * BK, wb * 128, bar);
-        tma_load(st + NW * C::W_BYTES, &tmA, kb * BK, m0, bar);
+        load_stage(s, kb);
       }
       if (!ok)  // after an expired wait: the copies in flight
         for (int j = i > S ? i - S : 0; j < i; ++j) wait_one(full + 8 * (j % S), uint32_t((j / S) & 1));
@@ -866,11 +899,11 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
   fence_before_sync();
   __syncthreads();
-  cluster_sync();
-  if (warp == 5) {
+  if (warp == 5) {  // before the cluster's barrier: no CTA holds tensor memory while it waits for another
     fence_after_sync();
     tmem_free(tmem, C::COLS);
   }
+  cluster_sync();
   // ---- a warp per token: lane l holds weight rows 4 l .. 4 l + 3
   const uint32_t part = smem_u32(sm);
   const int n0 = wb * 128 + 4 * lane;
@@ -882,10 +915,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     for (int k = 0; k < ranks; ++k)
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
-        float4 f;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                     : "r"(mapa(part + uint32_t(((p * TN + n) * 128 + 4 * lane) * 4), uint32_t(k))));
+        const float4 f = lds128_cluster(mapa(part + uint32_t(((p * TN + n) * 128 + 4 * lane) * 4), uint32_t(k)));
         v[p][0] = __fadd2_rn(v[p][0], make_float2(f.x, f.y));
         v[p][1] = __fadd2_rn(v[p][1], make_float2(f.z, f.w));
       }
