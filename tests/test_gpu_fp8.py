@@ -385,6 +385,46 @@ def test_capture_streams_and_repeats(q, M):
         assert all(torch.equal(y, want[k + 1]) for y in got[k])
 
 
+@pytest.mark.parametrize("M", [1, 40, 129, 700])
+def test_calls_in_a_row_wait_for_one_another(q, M):
+    """Each call reads what the one before wrote, into buffers that the one before that still read."""
+    K, I = 1024, 1536
+    w = [_operand(n, k, 90 + i, True) for i, (n, k) in enumerate([(I, K), (I, K), (K, I)])]
+    w = [(c, s * 2.0 ** -12) for c, s in w]
+    weight = _rand((1, K), FP16, 93, loud=False)[0]
+    x0 = _rand((M, K), FP16, 94)
+    y, h = torch.empty_like(x0), torch.empty_like(x0)
+    a, sa = q.quarot_quant_fp8(x0)
+    z, sz = torch.empty((M, I), dtype=E4M3, device=DEV), torch.empty((I // 128, M), device=DEV)
+
+    def layers(n, pause):
+        y.copy_(x0)
+        h.copy_(x0)
+        for _ in range(n):
+            q.quarot_add_rmsnorm_quant_fp8(y, h, weight, residual_out=h, q_out=a, scale_out=sa)
+            pause()
+            q.quarot_fp8_gated_gemm(a, sa, *w[0], *w[1], q_out=z, scale_out=sz)
+            pause()
+            q.quarot_fp8_gemm(z, sz, *w[2], y=y)
+            pause()
+            q.quarot_quant_fp8(y, q_out=a, scale_out=sa)
+            pause()
+        return [t.clone() for t in (y, h, a.view(torch.uint8), sa, z.view(torch.uint8), sz)]
+
+    want = layers(12, torch.cuda.synchronize)
+    assert torch.isfinite(want[0].float()).all() and want[0].abs().max() > 0
+    for _ in range(3):
+        assert all(torch.equal(p, r) for p, r in zip(layers(12, lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layers(12, lambda: None)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, r) for p, r in zip(got, want))
+    q.quarot_check_error()
+
+
 def test_refusals(q):
     a, sa = _operand(4, 256, 1, False)
     w, sw = _operand(130, 256, 2, True)

@@ -90,5 +90,42 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float2 v) {
 }
 __device__ __forceinline__ uint32_t cvt_e4m3x4(float2 a, float2 b) { return cvt_e4m3x2(a) | (cvt_e4m3x2(b) << 16); }
 
+// The 8-bit calls follow one another in a layer, most of them hardly longer
+// than a launch and its set-up, so they are launched as programmatic
+// dependents: the next kernel of the stream may start when every CTA of this
+// one has called next_may_start() or ended, and it waits in
+// wait_for_previous() until this one is over and its writes are visible.
+// Every thread waits there before its first access to global memory, reads and
+// writes alike, so a kernel ends after all that came before it in the stream.
+// A CTA that needs tensor memory takes it before it lets the next kernel
+// start, which therefore never holds what an earlier one still waits for.  One
+// after another, without and with it: quantizer, 1 x 4096: 1.85 and 1.43 us;
+// weights, 12288 x 4096: 27.7 and 26.5 us; product, 1 x 4096 x 4096: 8.3 and
+// 6.9 us; gated, 4 x 12288 x 4096: 20.1 and 18.8 us (and 20.1 us where the
+// product lets the next one start before its main loop).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline int launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                            cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+}
+
 }  // namespace fp8
 }  // namespace quarot

@@ -174,12 +174,6 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_one(bar, parity));
 }
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* o) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-               "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-               : "memory");
-}
-
 // Four bytes from global to this CTA's shared memory, asynchronously; the
 // arrival on the barrier follows this thread's copies so far.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
@@ -221,7 +215,7 @@ __device__ __forceinline__ void sts(uint32_t addr, float v) {
 // g / (1 + exp(-g)) to a few 2^-23: exp(-g) = 2^h 2^l with h = rn(-g log2 e) and
 // 2^l = 1 + l ln 2 for the rounding error l of h (exact by fma), 2^h and 1 / x by the
 // hardware approximations, 1 / x improved by a Newton step.  Far below zero h stops at
-// 126, where the result times anything stays below the quantizer's floor.  The
+// 126, where the result times any |u| < 1e23 stays below the quantizer's floor.  The
 // library's expf and division cost 25 % of the gated kernel.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kL2E = 1.44269502f, kL2ELow = 1.92596299e-8f;  // log2 e in two parts
@@ -354,6 +348,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     fence_barrier_init();
     if constexpr (SPLIT) {  // a CTA is short-lived: its first loads do not wait for the set-up
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      wait_for_previous();
       for (int s = 0; s < min(S, kb1 - kb0); ++s)
         load_stage<GATED>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE), tile0 / tiles_n * 128,
                           tile0 % tiles_n * TN, (kb0 + s) * BK);
@@ -364,6 +359,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  wait_for_previous();
 
   bool ok = true;
   if (warp < EPI0) {
@@ -384,8 +380,8 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (++s == S) { s = 0; par ^= 1u; }
           }
         }
-        if (!ok)  // after an expired wait: the copies in flight
-          for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_one(full + 8 * (j % S), (j / S) & 1);
+        // whatever happens elsewhere, no copy is in flight when the CTA ends
+        for (uint32_t j = it > S ? it - S : 0; j < it; ++j) ok = wait_one(full + 8 * (j % S), (j / S) & 1) && ok;
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -408,6 +404,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (++s == S) { s = 0; par ^= 1u; }
           }
         commit(drain);
+        next_may_start();  // not earlier: its CTAs would hold the idle SMs for nothing
       }
       __syncwarp();
       ok = wait_warp(drain, 0) && ok;
@@ -686,9 +683,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 
 // ===================================================================== narrow
 // Few tokens: the time is that of reading the weights once.  A CTA takes 128
-// weight rows (gated: 128 gate and 128 up rows) as the MMA's M, TN tokens as
-// its N, and 1 / cluster_size of the depth.  Its thread (lane quadrant, lane)
-// holds one weight row's sums of the TN tokens.  At the end every CTA writes
+// weight rows (gated: 128 gate and 128 up rows) as the MMA's M, the tokens, up
+// to TN, as its N, and 1 / cluster_size of the depth.  Its thread (lane quadrant, lane)
+// holds one weight row's sums of the tokens.  At the end every CTA writes
 // its sums to its shared memory, and the warps of all the cluster's CTAs take
 // tokens in turn, adding the ranks' sums in rank order through distributed
 // shared memory: no workspace, no atomics, the same bits every time.
@@ -739,7 +736,6 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = int(cluster_rank()), ranks = int(cluster_size());
   const int wb = int(blockIdx.x) / ranks;  // block of 128 weight rows (and of output columns)
-  const int m0 = int(blockIdx.y) * TN;
   const int kb_lo = int(int64_t(nkb) * rank / ranks), kb_hi = int(int64_t(nkb) * (rank + 1) / ranks);
 
   auto load_stage = [&](int s, int kb) {
@@ -747,7 +743,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     mbar_arrive_expect_tx(bar, C::STAGE);
     tma_load(st, &tmW0, kb * BK, wb * 128, bar);
     if (GATED) tma_load(st + C::W_BYTES, &tmW1, kb * BK, wb * 128, bar);
-    tma_load(st + NW * C::W_BYTES, &tmA, kb * BK, m0, bar);
+    tma_load(st + NW * C::W_BYTES, &tmA, kb * BK, 0, bar);
   };
   const int early = min(S, kb_hi - kb_lo);  // stages loaded before the set-up is over
 
@@ -766,6 +762,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     mbar_init(drain, 1);
     fence_barrier_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    wait_for_previous();
     for (int s = 0; s < early; ++s) load_stage(s, kb_lo + s);
   }
   if (warp == 5) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), C::COLS);
@@ -773,6 +770,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  wait_for_previous();
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
@@ -785,8 +783,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         if (!ok) break;
         load_stage(s, kb);
       }
-      if (!ok)  // after an expired wait: the copies in flight
-        for (int j = i > S ? i - S : 0; j < i; ++j) wait_one(full + 8 * (j % S), uint32_t((j / S) & 1));
+      // whatever happens elsewhere, no copy is in flight when the CTA ends
+      for (int j = i > S ? i - S : 0; j < i; ++j) ok = wait_one(full + 8 * (j % S), uint32_t((j / S) & 1)) && ok;
     }
     __syncwarp();
     if (!ok) record_error(QUAROT_ERR_TIMEOUT);
@@ -812,6 +810,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         commit(empty + 8 * s);
       }
       commit(drain);
+      next_may_start();  // with the sums still to be joined
     }
     __syncwarp();
     if (!wait_warp(drain, 0) || !ok) record_error(QUAROT_ERR_TIMEOUT);
@@ -833,7 +832,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
         const int k = (e * 32 + lane) / TN, n = (e * 32 + lane) % TN;
-        pre[e] = kb + k < kb_hi && m0 + n < M ? __ldg(as + size_t(kb + k) * M + m0 + n) : 0.f;
+        pre[e] = kb + k < kb_hi && n < M ? __ldg(as + size_t(kb + k) * M + n) : 0.f;
       }
       pw[0] = lane < KC && kb + lane < kb_hi ? __ldg(w0 + kb + lane) : 0.f;
       if constexpr (GATED) pw[1] = lane < KC && kb + lane < kb_hi ? __ldg(w1 + kb + lane) : 0.f;
@@ -907,8 +906,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   // ---- a warp per token: lane l holds weight rows 4 l .. 4 l + 3
   const uint32_t part = smem_u32(sm);
   const int n0 = wb * 128 + 4 * lane;
-  const int tokens = min(TN, M - m0);
-  for (int n = rank * (NT / 32) + warp; n < tokens; n += ranks * (NT / 32)) {
+  for (int n = rank * (NT / 32) + warp; n < M; n += ranks * (NT / 32)) {
     float2 v[NW][2];
 #pragma unroll
     for (int p = 0; p < NW; ++p) v[p][0] = v[p][1] = make_float2(0.f, 0.f);
@@ -919,7 +917,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         v[p][0] = __fadd2_rn(v[p][0], make_float2(f.x, f.y));
         v[p][1] = __fadd2_rn(v[p][1], make_float2(f.z, f.w));
       }
-    const size_t row = size_t(m0 + n) * N;
+    const size_t row = size_t(n) * N;
     if constexpr (!GATED) {
       const uint32_t lo = from_f2<T>(v[0][0]), hi = from_f2<T>(v[0][1]);
       uint16_t* yr = reinterpret_cast<uint16_t*>(y) + row + n0;
@@ -942,7 +940,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       m = block_amax(m);
       const Quotient quo(m);
       if (n0 < N) *reinterpret_cast<uint32_t*>(q + row + n0) = cvt_e4m3x4(quo(z0), quo(z1));
-      if (lane == 0) qs[size_t(wb) * M + m0 + n] = block_scale(m);
+      if (lane == 0) qs[size_t(wb) * M + n] = block_scale(m);
     }
   }
   cluster_sync();  // the other ranks have read this CTA's sums
@@ -1024,28 +1022,15 @@ static int launch(const Args& p, Kern* kern, AttrCache& attr, dim3 grid, int thr
   if (threads != wide::NT || y == nullptr || p.N % 8 != 0) ty = t0;
   else if (!make_out_map(&ty, y, p.M, p.N)) return QUAROT_ERR_CUDA;
   if (!smem_attr_once(kern, smem, attr)) return QUAROT_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = p.st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(cluster);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, t0, t1, ty, p.as, p.ws0, p.ws1, int(p.M), int(p.N),
-                                           int((p.K + BK - 1) / BK), y, p.q, p.qs);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  return launch_dependent(kern, grid, unsigned(threads), size_t(smem), unsigned(cluster), p.st, ta, t0, t1, ty, p.as,
+                          p.ws0, p.ws1, p.M, p.N, (p.K + BK - 1) / BK, y, p.q, p.qs);
 }
 
 template <bool GATED, int TN, typename T>
 static int launch_narrow(const Args& p, int cluster) {
   static AttrCache attr;
-  const unsigned wbs = unsigned((p.N + 127) / 128), mts = unsigned((p.M + TN - 1) / TN);
-  return launch(p, narrow::narrow_kernel<GATED, TN, T>, attr, dim3(wbs * unsigned(cluster), mts), narrow::NT, cluster,
+  const unsigned wbs = unsigned((p.N + 127) / 128);
+  return launch(p, narrow::narrow_kernel<GATED, TN, T>, attr, dim3(wbs * unsigned(cluster)), narrow::NT, cluster,
                 narrow::Cfg<GATED, TN>::SMEM, TN, 128, static_cast<T*>(p.y));
 }
 
@@ -1069,7 +1054,7 @@ static int run(const Args& p) {
   // weights: 15.8 us at 64 tokens, 35 at 100, the wide form 16 to 19 and 17).
   constexpr int kNarrow = GATED ? 32 : 64;
   const int64_t wbs = (p.N + 127) / 128, nkb = (p.K + BK - 1) / BK;
-  if (p.M <= kNarrow && wbs <= (int64_t(1) << 27)) {
+  if (p.M <= kNarrow) {
     int cl = 1;
     while (cl < 8 && wbs * cl * 2 <= 2 * sms && nkb / (2 * cl) >= 4) cl *= 2;
     if (p.M <= 16) return launch_narrow<GATED, 16, T>(p, cl);

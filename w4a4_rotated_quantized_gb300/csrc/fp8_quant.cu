@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(QT) quant_tokens_kernel(const T* __restrict__ 
   uint4 raw[QU][2];
   uint32_t row[QU], col[QU];
   bool in[QU];
+  next_may_start();
+  wait_for_previous();
 #pragma unroll
   for (int u = 0; u < QU; ++u) {
     const uint32_t i = (blockIdx.x * QU + u) * QG + g;
@@ -123,6 +125,8 @@ __global__ void __launch_bounds__(256) quant_block_kernel(const T* __restrict__ 
   const uint32_t c0 = (blockIdx.x % nb) * BLK + (threadIdx.x & 15u) * 8u;
   const uint32_t r0 = (blockIdx.x / nb) * BLK + (threadIdx.x >> 4);
   uint4 raw[8];
+  next_may_start();
+  wait_for_previous();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
@@ -165,6 +169,8 @@ __global__ void norm_quant_kernel(const T* x, int64_t ld_x, const T* res, int64_
   uint8_t* qr = q + size_t(row) * d;
   const uint32_t step = blockDim.x * 8u;
   float2 ss = make_float2(0.f, 0.f);
+  next_may_start();
+  wait_for_previous();
   for (uint32_t base = 0; base < nb * BLK; base += NU * step) {
     uint4 a[NU], b[NU], g[NU];
 #pragma unroll
@@ -233,21 +239,21 @@ static int check_matrix(const void* x, int dtype, int64_t M, int64_t d, int64_t 
 }
 
 template <typename T>
-static void launch_norm(const void* x, int64_t ld_x, const void* res, int64_t ld_r, const void* w, int64_t M,
+static int launch_norm(const void* x, int64_t ld_x, const void* res, int64_t ld_r, const void* w, int64_t M,
                         int64_t d, float eps, void* h, int64_t ld_h, uint8_t* q, float* scale, cudaStream_t st) {
   const uint32_t nb = uint32_t((d + BLK - 1) / BLK);
   const int64_t chunks = int64_t(nb) * (BLK / 8);
   const unsigned threads = unsigned(chunks >= 512 ? 256 : (chunks + 31) / 32 * 32);
   const size_t smem = nb * sizeof(float);
   auto go = [&](auto kern) {
-    kern<<<unsigned(M), threads, smem, st>>>(static_cast<const T*>(x), ld_x, static_cast<const T*>(res), ld_r,
-                                             static_cast<const T*>(w), uint32_t(M), uint32_t(d), nb, eps,
-                                             static_cast<T*>(h), ld_h, q, scale);
+    return launch_dependent(kern, dim3(unsigned(M)), threads, smem, 1, st, static_cast<const T*>(x), ld_x,
+                            static_cast<const T*>(res), ld_r, static_cast<const T*>(w), M, d, nb, eps,
+                            static_cast<T*>(h), ld_h, q, scale);
   };
-  if (res && w) go(norm_quant_kernel<T, true, true>);
-  else if (res) go(norm_quant_kernel<T, true, false>);
-  else if (w) go(norm_quant_kernel<T, false, true>);
-  else go(norm_quant_kernel<T, false, false>);
+  if (res && w) return go(norm_quant_kernel<T, true, true>);
+  if (res) return go(norm_quant_kernel<T, true, false>);
+  if (w) return go(norm_quant_kernel<T, false, true>);
+  return go(norm_quant_kernel<T, false, false>);
 }
 
 }  // namespace fp8
@@ -264,12 +270,10 @@ extern "C" int quarot_quant_fp8(const void* x, int dtype, int64_t M, int64_t d, 
   const unsigned grid = (total + QU * QG - 1) / (QU * QG);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == QUAROT_FP16)
-    quant_tokens_kernel<__half><<<grid, QT, 0, st>>>(static_cast<const __half*>(x), uint32_t(M), uint32_t(d), ld_x, nb,
-                                                     total, q_out, scale_out);
-  else
-    quant_tokens_kernel<__nv_bfloat16><<<grid, QT, 0, st>>>(static_cast<const __nv_bfloat16*>(x), uint32_t(M),
-                                                            uint32_t(d), ld_x, nb, total, q_out, scale_out);
-  return cudaGetLastError() == cudaSuccess ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+    return launch_dependent(quant_tokens_kernel<__half>, dim3(grid), QT, 0, 1, st, static_cast<const __half*>(x), M, d,
+                            ld_x, nb, total, q_out, scale_out);
+  return launch_dependent(quant_tokens_kernel<__nv_bfloat16>, dim3(grid), QT, 0, 1, st,
+                          static_cast<const __nv_bfloat16*>(x), M, d, ld_x, nb, total, q_out, scale_out);
 }
 
 extern "C" int quarot_quant_fp8_block(const void* w, int dtype, int64_t N, int64_t K, int64_t ld_w, uint8_t* q_out,
@@ -281,12 +285,10 @@ extern "C" int quarot_quant_fp8_block(const void* w, int dtype, int64_t N, int64
   const unsigned grid = unsigned((N + BLK - 1) / BLK) * nb;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == QUAROT_FP16)
-    quant_block_kernel<__half><<<grid, 256, 0, st>>>(static_cast<const __half*>(w), uint32_t(N), uint32_t(K), ld_w, nb,
-                                                     q_out, scale_out);
-  else
-    quant_block_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(w), uint32_t(N),
-                                                            uint32_t(K), ld_w, nb, q_out, scale_out);
-  return cudaGetLastError() == cudaSuccess ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+    return launch_dependent(quant_block_kernel<__half>, dim3(grid), 256, 0, 1, st, static_cast<const __half*>(w), N, K,
+                            ld_w, nb, q_out, scale_out);
+  return launch_dependent(quant_block_kernel<__nv_bfloat16>, dim3(grid), 256, 0, 1, st,
+                          static_cast<const __nv_bfloat16*>(w), N, K, ld_w, nb, q_out, scale_out);
 }
 
 extern "C" int quarot_add_rmsnorm_quant_fp8(const void* x, int64_t ld_x, const void* residual, int64_t ld_r,
@@ -303,8 +305,6 @@ extern "C" int quarot_add_rmsnorm_quant_fp8(const void* x, int64_t ld_x, const v
   if (!aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16)) return QUAROT_ERR_ALIGNMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == QUAROT_FP16)
-    launch_norm<__half>(x, ld_x, residual, ld_r, weight, M, d, eps, residual_out, ld_out, q_out, scale_out, st);
-  else
-    launch_norm<__nv_bfloat16>(x, ld_x, residual, ld_r, weight, M, d, eps, residual_out, ld_out, q_out, scale_out, st);
-  return cudaGetLastError() == cudaSuccess ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+    return launch_norm<__half>(x, ld_x, residual, ld_r, weight, M, d, eps, residual_out, ld_out, q_out, scale_out, st);
+  return launch_norm<__nv_bfloat16>(x, ld_x, residual, ld_r, weight, M, d, eps, residual_out, ld_out, q_out, scale_out, st);
 }
