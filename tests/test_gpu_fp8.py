@@ -299,6 +299,24 @@ def test_gated_extremes(q):
     _check_gated(codes[rows], scale[:, rows], a[rows], sa[:, rows], g, sg, u, su)
 
 
+@pytest.mark.parametrize("M", [3, 70, 3000])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gated_gates_near_the_largest_float(q, M, sign):
+    """silu(g) is g for g = 2.8e38, whose multiple by log2 e overflows, and 0 for -2.8e38."""
+    I, K = 1152, 128
+    a, sa = _operand(M, K, 1, False)
+    u, su = _operand(I, K, 2, True)
+    a[:], sa[:] = 1.0, 2.0 ** 60
+    g, sg = torch.full((I, K), sign, device=DEV).to(E4M3), torch.full((9, 1), 1.9e18, device=DEV)
+    su.mul_(2.0 ** -110)
+    codes, scale = q.quarot_fp8_gated_gemm(a, sa, g, sg, u, su)
+    q.quarot_check_error()
+    if sign > 0:
+        _check_gated(codes, scale, a, sa, g, sg, u, su)
+    else:
+        assert (codes.float() == 0).all()
+
+
 # ---------------------------------------------------------------- as they are used
 def _weights(N, K, seed):
     return (_rand((N, K), FP16, seed, loud=False).float() * K ** -0.5).to(FP16)

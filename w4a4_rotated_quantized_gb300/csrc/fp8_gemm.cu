@@ -212,21 +212,26 @@ __device__ __forceinline__ void sts(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// g / (1 + exp(-g)) to a few 2^-23: exp(-g) = 2^h 2^l with h = rn(-g log2 e) and
-// 2^l = 1 + l ln 2 for the rounding error l of h (exact by fma), 2^h and 1 / x by the
-// hardware approximations, 1 / x improved by a Newton step.  Far below zero h stops at
-// 126, where the result times any |u| < 1e23 stays below the quantizer's floor.  The
-// library's expf and division cost 25 % of the gated kernel.
-__device__ __forceinline__ float silu(float g) {
+// silu(g) u = g u / (1 + exp(-g)) of two columns, to a few 2^-23.  exp(n) = 2^h 2^l
+// with h = rn(n log2 e) and 2^l = 1 + l ln 2 for the rounding error l of h (exact by
+// fma); 2^h and 1 / x by the hardware approximations, 1 / x improved by a Newton step.
+// n = -g is held to [-88, 88.5], where 2^h is finite.  Below g = -87.4 (1 + exp(n) >
+// 2^126) 1 / x is flushed to zero and silu(g), under 1.1e-36, with it.
+__device__ __forceinline__ float2 silu_mul(float2 g, float2 u) {
   constexpr float kL2E = 1.44269502f, kL2ELow = 1.92596299e-8f;  // log2 e in two parts
-  const float h = fminf(-g * kL2E, 126.f);
-  const float l = h < 126.f ? fmaf(-g, kL2ELow, fmaf(-g, kL2E, -h)) : 0.f;
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
-  const float d = 1.0f + fmaf(e, l * 0.693147181f, e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  r = fmaf(r, fmaf(-d, r, 1.0f), r);
-  return g * r;
+  constexpr float kLn2 = 0.693147181f;
+  const float2 n = make_float2(fminf(fmaxf(-g.x, -88.f), 88.5f), fminf(fmaxf(-g.y, -88.f), 88.5f));
+  const float2 nh = __fmul2_rn(n, make_float2(-kL2E, -kL2E));
+  const float2 l = __ffma2_rn(n, make_float2(kL2ELow, kL2ELow), __ffma2_rn(n, make_float2(kL2E, kL2E), nh));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-nh.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-nh.y));
+  const float2 one = make_float2(1.f, 1.f), m1 = make_float2(-1.f, -1.f);
+  const float2 nd = __ffma2_rn(e, __ffma2_rn(l, make_float2(-kLn2, -kLn2), m1), m1);  // -(1 + exp(n))
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-nd.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-nd.y));
+  r = __ffma2_rn(r, __ffma2_rn(nd, r, one), r);
+  return __fmul2_rn(__fmul2_rn(g, r), u);
 }
 
 // ===================================================================== wide
@@ -542,7 +547,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          acc[j] = make_float2(silu(acc[j].x) * acc[32 + j].x, silu(acc[j].y) * acc[32 + j].y);
+          acc[j] = silu_mul(acc[j], acc[32 + j]);
           m = max_nan(m, max_nan(fabsf(acc[j].x), fabsf(acc[j].y)));
         }
         // the block's other 64 columns are the other half's: exchange the abs-max
@@ -631,7 +636,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           sum16(128 + 16 * c, u);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            z[n][i] = make_float2(silu(z[n][i].x) * u[i].x, silu(z[n][i].y) * u[i].y);
+            z[n][i] = silu_mul(z[n][i], u[i]);
             m = max_nan(m, max_nan(fabsf(z[n][i].x), fabsf(z[n][i].y)));
           }
         }
@@ -930,8 +935,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         if (n0 + 3 < N) yr[3] = uint16_t(hi >> 16);
       }
     } else {
-      const float2 z0 = make_float2(silu(v[0][0].x) * v[1][0].x, silu(v[0][0].y) * v[1][0].y);
-      const float2 z1 = make_float2(silu(v[0][1].x) * v[1][1].x, silu(v[0][1].y) * v[1][1].y);
+      const float2 z0 = silu_mul(v[0][0], v[1][0]);
+      const float2 z1 = silu_mul(v[0][1], v[1][1]);
       // weight rows past N were read as zeros: z = 0 there
       float m = max_nan(max_nan(fabsf(z0.x), fabsf(z0.y)), max_nan(fabsf(z1.x), fabsf(z1.y)));
       m = n0 < N ? m : 0.f;
@@ -1049,9 +1054,10 @@ static int run(const Args& p) {
   if (!get_encoder()) return QUAROT_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return QUAROT_ERR_CUDA;
-  // Narrow up to here: at 64 tokens (gated: 32) it and the split wide form take
-  // the same time; beyond, a token tile's sums crowd out its stages (50 MB of
-  // weights: 15.8 us at 64 tokens, 35 at 100, the wide form 16 to 19 and 17).
+  // Narrow up to here, where one token tile's sums still fit two CTAs' registers
+  // (a second tile would read the weights again).  It and the split wide form:
+  // 64 x 4096 x 12288 13.8 and 17.1 us, 16 x 12288 x 4096 11.6 and 17.6 us;
+  // gated 32 x 12288 x 4096 21.0 and 21.9 us, 16 x 12288 x 4096 20.1 and 27.7 us.
   constexpr int kNarrow = GATED ? 32 : 64;
   const int64_t wbs = (p.N + 127) / 128, nkb = (p.K + BK - 1) / BK;
   if (p.M <= kNarrow) {
