@@ -133,7 +133,8 @@ def test_quant_edge_values(q, dtype):
 
 
 @pytest.mark.parametrize("dtype", [FP16, BF16])
-@pytest.mark.parametrize("M,d", [(1, 16), (1, 4096), (3, 272), (5, 1008), (130, 4096), (17, 12288), (2, 65552)])
+@pytest.mark.parametrize("M,d", [(1, 16), (1, 4096), (3, 272), (5, 1008), (130, 4096), (17, 12288), (2, 65552),
+                                 (1025, 272), (1030, 2064), (5, 8208)])
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("weighted", [True, False])
 def test_norm(q, dtype, M, d, residual, weighted):

@@ -554,7 +554,7 @@ def _fp8_call(name, dev, stream, *args):
     tensors' device current, and checks its status."""
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     fn = getattr(_lib if _lib is not None else load(), name)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -642,6 +642,11 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
     di = dev.index
     ld_r = ld_h = d
     res = h = w = None
+    if residual_out is not None:
+        ld_h = _rows(residual_out, "residual_out", di, dt)
+        if residual_out.shape != x.shape:
+            raise QuarotError(1, f"residual_out has shape {tuple(residual_out.shape)}, expected {tuple(x.shape)}")
+        h = residual_out.data_ptr()
     if residual is not None:
         ld_r = _rows(residual, "residual", di, dt)
         if residual.shape != x.shape:
@@ -649,11 +654,7 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
         res = residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty((M, d), dtype=dt, device=dev)
-    if residual_out is not None:
-        ld_h = _rows(residual_out, "residual_out", di, dt)
-        if residual_out.shape != x.shape:
-            raise QuarotError(1, f"residual_out has shape {tuple(residual_out.shape)}, expected {tuple(x.shape)}")
-        h = residual_out.data_ptr()
+            h = residual_out.data_ptr()
     if weight is not None:
         w = _dense(weight, dt, (d,), "weight", di)
     q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)

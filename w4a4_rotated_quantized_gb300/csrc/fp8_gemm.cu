@@ -687,7 +687,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }  // namespace wide
 
 // ===================================================================== narrow
-// Few tokens: the time is that of reading the weights once.  A CTA takes 128
+// Few tokens: the time is that of reading the weights once, 1 x 4096 x 12288 in
+// 11.2 us (4.5 TB/s), gated 4 x 12288 x 4096 in 18.7 us (5.4 TB/s), of which some
+// 4 us are launch, set-up, first load and join.  A CTA takes 128
 // weight rows (gated: 128 gate and 128 up rows) as the MMA's M, the tokens, up
 // to TN, as its N, and 1 / cluster_size of the depth.  Its thread (lane quadrant, lane)
 // holds one weight row's sums of the tokens.  At the end every CTA writes
@@ -1041,7 +1043,15 @@ static int launch_narrow(const Args& p, int cluster) {
 
 // Over how many CTAs a tile's depth is split: as many as find an SM at once,
 // with two k-blocks each at least.  A cluster of 8 finds room on 4/5 of the SMs
-// only (the SMs of a GPC are not a multiple of 8), one of 4 on 18/19.
+// only (the SMs of a GPC are not a multiple of 8), one of 4 on 18/19.  In us:
+//
+//   tiles, k-blocks                     1     2     4     8 ranks
+//     8, 96    128 x 2048 x 12288    38.5  24.3  17.2  16.4
+//    16, 32    128 x 4096 x 4096     15.9  13.1  11.5  24.1
+//    32, 96    256 x 4096 x 12288    38.8  25.3  20.1  47.8
+//    64, 32    512 x 4096 x 4096     16.3  13.9  24.3  59.9
+//    96, 32    700 x 4096 x 4096     16.9  26.0  34.5  78.3
+//    64, 32    gated 256 x 4096 x 4096  17.1  15.9  27.4  64.9
 static int split_ranks(int64_t tiles, int64_t nkb, int sms) {
   if (tiles * 8 <= sms * 15 / 19 && nkb >= 16) return 8;
   if (tiles * 4 <= sms * 18 / 19 && nkb >= 8) return 4;
@@ -1061,6 +1071,9 @@ static int run(const Args& p) {
   constexpr int kNarrow = GATED ? 32 : 64;
   const int64_t wbs = (p.N + 127) / 128, nkb = (p.K + BK - 1) / BK;
   if (p.M <= kNarrow) {
+    // The depth over as many CTAs as two on every SM, of four k-blocks at least:
+    // 1 x 4096 x 12288 24.7, 14.9, 11.3, 11.2 us over 1, 2, 4, 8; 37 x 12288 x 4096
+    // (96 blocks of rows) 14.7, 12.8, 16.7, 21.6; gated 4 x 12288 x 4096 20.5, 18.8, 22.5, 27.3.
     int cl = 1;
     while (cl < 8 && wbs * cl * 2 <= 2 * sms && nkb / (2 * cl) >= 4) cl *= 2;
     if (p.M <= 16) return launch_narrow<GATED, 16, T>(p, cl);
