@@ -444,6 +444,32 @@ def test_calls_in_a_row_wait_for_one_another(q, M):
     q.quarot_check_error()
 
 
+def test_a_given_streams_memory_is_its_own(q):
+    """What a call on a given stream allocates is not what work still queued on the current stream writes."""
+    x = _rand((64, 512), FP16, 20)
+    lin = q.QuarotFp8Linear(_weights(512, 512, 21))
+    mlp = q.QuarotFp8GatedMLP(_weights(512, 512, 21), _weights(512, 512, 22), _weights(512, 512, 23))
+    side = torch.cuda.Stream()
+
+    def all_of(stream):
+        a, sa = q.quarot_quant_fp8(x, stream=stream)
+        return [a.view(torch.uint8), sa, q.quarot_fp8_gemm(a, sa, lin.w_q, lin.w_scale, stream=stream),
+                lin(x, stream=stream), *mlp(x, x, stream=stream)]
+
+    want = all_of(None)
+    torch.cuda.synchronize()
+    old = [torch.empty_like(t) for t in want for _ in range(4)]
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for t in old:
+        t.fill_(7)
+    del old, t
+    got = all_of(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, r) for p, r in zip(got, want))
+    with pytest.raises(q.QuarotError):
+        q.quarot_quant_fp8(x.cpu(), stream=side)
+
+
 def test_refusals(q):
     a, sa = _operand(4, 256, 1, False)
     w, sw = _operand(130, 256, 2, True)

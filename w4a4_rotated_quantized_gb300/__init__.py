@@ -549,10 +549,10 @@ _E4M3 = torch.float8_e4m3fn
 # A decode step makes a handful of these calls with microseconds of GPU work
 # each: the checks read each attribute once, and only a tensor that fails is
 # looked at again, by the checks that say what is wrong with it.
-def _fp8_call(name, dev, stream, *args):
-    """Calls the entry point on `stream` (default: the current one) with the
-    tensors' device current, and checks its status."""
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _fp8_call(name, dev, *args):
+    """Calls the entry point on the current stream with the tensors' device
+    current, and checks its status."""
+    raw = torch._C._cuda_getCurrentRawStream(dev)
     fn = getattr(_lib if _lib is not None else load(), name)
     if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
@@ -561,6 +561,14 @@ def _fp8_call(name, dev, stream, *args):
             st = fn(*args, raw)
     if st != QUAROT_OK:
         raise QuarotError(st, name)
+
+
+def _on(stream, t):
+    """With `stream` current: what a call allocates is then the stream's, as
+    what it launches is, and no other stream's work touches the same memory."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != stream.device.index:
+        raise QuarotError(1, "the stream is not on the tensors' device")
+    return torch.cuda.stream(stream)
 
 
 def _rows(t, name, dev=None, dtype=None) -> int:
@@ -607,11 +615,14 @@ def _fp8_outputs(M, d, scale_shape, q_out, scale_out, dev):
 def quarot_quant_fp8(x, q_out=None, scale_out=None, stream=None):
     """x: fp16 or bf16 [M, d], rows contiguous (any row stride) -> (e4m3 codes
     [M, d], fp32 scales [ceil(d / 128), M], one for each token and 128 columns)."""
+    if stream is not None:
+        with _on(stream, x):
+            return quarot_quant_fp8(x, q_out, scale_out)
     ld = _rows(x, "x")
     M, d = x.shape
     dev = x.device
     q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
-    _fp8_call("quarot_quant_fp8", dev.index, stream, x.data_ptr(), _DTYPES[x.dtype], M, d, ld, q_out.data_ptr(),
+    _fp8_call("quarot_quant_fp8", dev.index, x.data_ptr(), _DTYPES[x.dtype], M, d, ld, q_out.data_ptr(),
               scale_out.data_ptr())
     return q_out, scale_out
 
@@ -619,11 +630,14 @@ def quarot_quant_fp8(x, q_out=None, scale_out=None, stream=None):
 def quarot_quant_fp8_block(w, q_out=None, scale_out=None, stream=None):
     """w: fp16 or bf16 [N, K], rows contiguous (any row stride) -> (e4m3 codes
     [N, K], fp32 scales [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block)."""
+    if stream is not None:
+        with _on(stream, w):
+            return quarot_quant_fp8_block(w, q_out, scale_out)
     ld = _rows(w, "w")
     N, K = w.shape
     dev = w.device
     q_out, scale_out = _fp8_outputs(N, K, (_blocks(N), _blocks(K)), q_out, scale_out, dev)
-    _fp8_call("quarot_quant_fp8_block", dev.index, stream, w.data_ptr(), _DTYPES[w.dtype], N, K, ld, q_out.data_ptr(),
+    _fp8_call("quarot_quant_fp8_block", dev.index, w.data_ptr(), _DTYPES[w.dtype], N, K, ld, q_out.data_ptr(),
               scale_out.data_ptr())
     return q_out, scale_out
 
@@ -636,6 +650,9 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
     [M, d], rows contiguous (any row stride); weight [d] or None.
     residual_out may be x or residual itself; without a residual h is x,
     and is copied only if residual_out is given."""
+    if stream is not None:
+        with _on(stream, x):
+            return quarot_add_rmsnorm_quant_fp8(x, residual, weight, eps, residual_out, q_out, scale_out)
     ld = _rows(x, "x")
     M, d = x.shape
     dev, dt = x.device, x.dtype
@@ -658,7 +675,7 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
     if weight is not None:
         w = _dense(weight, dt, (d,), "weight", di)
     q_out, scale_out = _fp8_outputs(M, d, (_blocks(d), M), q_out, scale_out, dev)
-    _fp8_call("quarot_add_rmsnorm_quant_fp8", di, stream, x.data_ptr(), ld, res, ld_r, w, _DTYPES[dt], M, d,
+    _fp8_call("quarot_add_rmsnorm_quant_fp8", di, x.data_ptr(), ld, res, ld_r, w, _DTYPES[dt], M, d,
               float(eps), h, ld_h, q_out.data_ptr(), scale_out.data_ptr())
     return q_out, scale_out, x if residual_out is None else residual_out
 
@@ -685,6 +702,9 @@ def _fp8_tokens(a_q, a_scale):
 def quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y=None, out_dtype=torch.float16, stream=None):
     """Token codes [M, K] and scales x weight codes [N, K] and scales ->
     y fp16 or bf16 [M, N] (``out_dtype``, or the type of ``y``)."""
+    if stream is not None:
+        with _on(stream, a_q):
+            return quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y, out_dtype)
     a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
     w, sw = _fp8_weight(w_q, w_scale, "w_q", K, dev)
     N = w_q.shape[0]
@@ -696,13 +716,16 @@ def quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y=None, out_dtype=torch.float16,
         if not isinstance(y, torch.Tensor) or y.dtype not in _DTYPES:
             raise QuarotError(1, "y must be fp16 or bf16")
         _dense(y, y.dtype, (M, N), "y", dev)
-    _fp8_call("quarot_fp8_gemm", dev, stream, a, sa, w, sw, M, N, K, y.data_ptr(), _DTYPES[y.dtype])
+    _fp8_call("quarot_fp8_gemm", dev, a, sa, w, sw, M, N, K, y.data_ptr(), _DTYPES[y.dtype])
     return y
 
 
 def quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out=None, scale_out=None, stream=None):
     """silu(A Wg^T) * (A Wu^T) of block-scaled codes (weights [I, K]) ->
     (e4m3 codes [M, I], fp32 scales [ceil(I / 128), M])."""
+    if stream is not None:
+        with _on(stream, a_q):
+            return quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out, scale_out)
     a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
     g, sg = _fp8_weight(wg_q, wg_scale, "wg_q", K, dev)
     u, su = _fp8_weight(wu_q, wu_scale, "wu_q", K, dev)
@@ -710,7 +733,7 @@ def quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out=No
     if wu_q.shape[0] != I:
         raise QuarotError(1, "wg_q and wu_q disagree on their shapes")
     q_out, scale_out = _fp8_outputs(M, I, (_blocks(I), M), q_out, scale_out, a_q.device)
-    _fp8_call("quarot_fp8_gated_gemm", dev, stream, a, sa, g, sg, u, su, M, I, K, q_out.data_ptr(),
+    _fp8_call("quarot_fp8_gated_gemm", dev, a, sa, g, sg, u, su, M, I, K, q_out.data_ptr(),
               scale_out.data_ptr())
     return q_out, scale_out
 
@@ -730,11 +753,14 @@ class QuarotFp8Linear:
     def __call__(self, x, y=None, stream=None):
         if x.shape[-1] != self.in_features:
             raise QuarotError(1, f"x has {x.shape[-1]} features, the layer {self.in_features}")
+        if stream is not None:
+            with _on(stream, x):
+                return self(x, y)
         lead = x.shape[:-1]
-        a_q, a_scale = quarot_quant_fp8(x.reshape(-1, self.in_features), stream=stream)
+        a_q, a_scale = quarot_quant_fp8(x.reshape(-1, self.in_features))
         if y is not None:
             y = y.view(-1, self.out_features)
-        return self.from_codes(a_q, a_scale, y=y, out_dtype=x.dtype, stream=stream).view(*lead, self.out_features)
+        return self.from_codes(a_q, a_scale, y=y, out_dtype=x.dtype).view(*lead, self.out_features)
 
     def from_codes(self, a_q, a_scale, y=None, out_dtype=torch.float16, stream=None):
         return quarot_fp8_gemm(a_q, a_scale, self.w_q, self.w_scale, y=y, out_dtype=out_dtype, stream=stream)
@@ -760,12 +786,14 @@ class QuarotFp8GatedMLP:
     def __call__(self, x, residual=None, stream=None):
         if x.shape[-1] != self.features:
             raise QuarotError(1, f"x has {x.shape[-1]} features, the block {self.features}")
+        if stream is not None:
+            with _on(stream, x):
+                return self(x, residual)
         x2 = x.reshape(-1, self.features)
         r2 = None if residual is None else residual.reshape(-1, self.features)
-        a_q, a_scale, h = quarot_add_rmsnorm_quant_fp8(x2, r2, self.norm_weight, eps=self.eps, stream=stream)
-        z_q, z_scale = quarot_fp8_gated_gemm(a_q, a_scale, self.gate_q, self.gate_scale, self.up_q, self.up_scale,
-                                             stream=stream)
-        y = self.down.from_codes(z_q, z_scale, out_dtype=x.dtype, stream=stream)
+        a_q, a_scale, h = quarot_add_rmsnorm_quant_fp8(x2, r2, self.norm_weight, eps=self.eps)
+        z_q, z_scale = quarot_fp8_gated_gemm(a_q, a_scale, self.gate_q, self.gate_scale, self.up_q, self.up_scale)
+        y = self.down.from_codes(z_q, z_scale, out_dtype=x.dtype)
         return y.view(x.shape), h.view(x.shape)
 
 
