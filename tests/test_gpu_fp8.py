@@ -209,7 +209,7 @@ GEMM = [(1, 1, 16), (1, 4096, 4096), (2, 127, 144), (5, 129, 128), (8, 1000, 122
         (64, 256, 256), (65, 300, 528), (100, 129, 4096), (128, 128, 384), (129, 1025, 640), (200, 777, 2064),
         (256, 512, 512), (257, 2048, 1040), (513, 1031, 272), (1000, 257, 4096), (1500, 2500, 400),
         (2600, 2100, 144), (2601, 2101, 1168), (20000, 300, 128), (150, 40000, 272),
-        (300, 8, 256), (4000, 1, 16), (3000, 24, 4096)]
+        (300, 8, 256), (4000, 1, 16), (3000, 24, 4096), (100, 25000, 272), (70, 40001, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -260,7 +260,7 @@ def test_gemm_nan_stays_in_its_row_and_column(q, M):
 
 GATED = [(1, 16, 16), (1, 4096, 4096), (3, 144, 272), (7, 272, 128), (16, 1040, 4096), (33, 400, 1008), (64, 256, 512),
          (65, 656, 528), (130, 1024, 640), (257, 272, 1040), (333, 1040, 2064), (600, 784, 400),
-         (2600, 1040, 144), (2601, 1168, 1296), (20000, 144, 128), (150, 20000, 272)]
+         (2600, 1040, 144), (2601, 1168, 1296), (20000, 144, 128), (150, 20000, 272), (70, 12304, 272), (100, 20000, 400)]
 
 
 @pytest.mark.parametrize("M,I,K", GATED)
