@@ -470,6 +470,47 @@ def test_a_given_streams_memory_is_its_own(q):
         q.quarot_quant_fp8(x.cpu(), stream=side)
 
 
+@pytest.mark.parametrize("M", [1, 129, 600])
+def test_forked_and_joined_streams(q, M):
+    """Calls that follow an event of another stream, two kernels at once, a fill or a copy, eagerly and as graph nodes."""
+    K, N = 768, 640
+    w = [_operand(N, K, 60 + i, True) for i in range(2)]
+    d, sd = _operand(K, N, 62, True)
+    x = _rand((M, K), BF16, 63)
+    side = torch.cuda.Stream()
+
+    def passes():
+        here = torch.cuda.current_stream()
+        h = torch.zeros_like(x)
+        for _ in range(4):
+            a, sa = q.quarot_quant_fp8(x)            # after a fill, and after the join below
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                y1 = q.quarot_fp8_gemm(a, sa, *w[1], out_dtype=BF16)
+                c1, s1 = q.quarot_quant_fp8(y1)
+            y0 = q.quarot_fp8_gemm(a, sa, *w[0], out_dtype=BF16)
+            c0, s0 = q.quarot_quant_fp8(y0)
+            here.wait_stream(side)                   # both quantizers are what the next call follows
+            g = q.quarot_fp8_gemm(c1, s1, d, sd, out_dtype=BF16)
+            c, s, h = q.quarot_add_rmsnorm_quant_fp8(g, h)
+            h = h.clone()
+            for t in (a, sa, y1, c1, s1):
+                t.record_stream(side)
+        return [y0, c0.view(torch.uint8), s0, g, c.view(torch.uint8), s, h]
+
+    want = [t.clone() for t in passes()]
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, r) for p, r in zip(passes(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = passes()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, r) for p, r in zip(got, want))
+    q.quarot_check_error()
+
+
 def test_refusals(q):
     a, sa = _operand(4, 256, 1, False)
     w, sw = _operand(130, 256, 2, True)
