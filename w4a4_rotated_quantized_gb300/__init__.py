@@ -24,12 +24,14 @@ e4m3 codes with a scale for each block of 128.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libquarot.so")
+CALLS_PATH = os.path.join(_HERE, "_fp8_calls.so")
 
 QUAROT_OK = 0
 QUAROT_ERR_TIMEOUT = 5
@@ -37,6 +39,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported size", 3: "misaligned 
           4: "kernel launch failed", 5: "device-side wait timed out", 6: "CUDA error"}
 
 _lib = None
+_calls = None  # compiled form of the 8-bit calls
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -89,19 +92,30 @@ class QuarotError(RuntimeError):
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
-    """Loads libquarot.so (once) and declares the ABI signatures."""
-    global _lib
+    """Loads libquarot.so (once) and declares the ABI signatures; the compiled
+    form of the 8-bit calls comes with it."""
+    global _lib, _calls
     if _lib is not None:
         return _lib
     p = path or LIB_PATH
     if not os.path.exists(p):
         raise QuarotError(6, f"libquarot.so not found at {p}; build it with "
                              "w4a4_rotated_quantized_gb300.build.build()")
+    if not os.path.exists(CALLS_PATH):
+        raise QuarotError(6, f"_fp8_calls.so not found at {CALLS_PATH}; build it with "
+                             "w4a4_rotated_quantized_gb300.build.build()")
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    spec = importlib.util.spec_from_file_location("_fp8_calls", CALLS_PATH)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "quarot_quant_fp8", "quarot_quant_fp8_block", "quarot_add_rmsnorm_quant_fp8", "quarot_fp8_gemm",
+        "quarot_fp8_gated_gemm")))
+    _calls = calls
     _lib = lib
     return lib
 
@@ -547,8 +561,14 @@ _E4M3 = torch.float8_e4m3fn
 
 
 # A decode step makes a handful of these calls with microseconds of GPU work
-# each: the checks read each attribute once, and only a tensor that fails is
-# looked at again, by the checks that say what is wrong with it.
+# each, so what they mostly get (dense tensors on the current device and
+# stream) goes through the compiled _calls; it returns None for anything else,
+# which the checks here then take, or say what is wrong with.
+def _loaded():
+    load()
+    return _calls
+
+
 def _fp8_call(name, dev, *args):
     """Calls the entry point on the current stream with the tensors' device
     current, and checks its status."""
@@ -573,13 +593,6 @@ def _on(stream, t):
 
 def _rows(t, name, dev=None, dtype=None) -> int:
     """A 2-D fp16 or bf16 input read row by row; returns its row stride."""
-    try:
-        d = t.get_device()  # -1 off the GPU
-        if (d >= 0 if dev is None else d == dev) and t.is_contiguous() and t.dim() == 2 and (
-                t.dtype in _DTYPES if dtype is None else t.dtype is dtype):
-            return t.shape[1]
-    except AttributeError:
-        pass
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise QuarotError(1, f"{name} must be an fp16 or bf16 CUDA tensor")
     return _need_rows(t, t.dtype if dtype is None else dtype, name, None if dev is None else torch.device("cuda", dev))
@@ -587,13 +600,10 @@ def _rows(t, name, dev=None, dtype=None) -> int:
 
 def _dense(t, dtype, shape, name, dev):
     """A contiguous tensor of this type and shape on CUDA device `dev`; its address."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
     _need(t, dtype, name, torch.device("cuda", dev))
-    raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
 
 
 def _blocks(n: int) -> int:
@@ -618,6 +628,9 @@ def quarot_quant_fp8(x, q_out=None, scale_out=None, stream=None):
     if stream is not None:
         with _on(stream, x):
             return quarot_quant_fp8(x, q_out, scale_out)
+    done = (_calls or _loaded()).quant(x, q_out, scale_out, False)
+    if done is not None:
+        return done
     ld = _rows(x, "x")
     M, d = x.shape
     dev = x.device
@@ -633,6 +646,9 @@ def quarot_quant_fp8_block(w, q_out=None, scale_out=None, stream=None):
     if stream is not None:
         with _on(stream, w):
             return quarot_quant_fp8_block(w, q_out, scale_out)
+    done = (_calls or _loaded()).quant(w, q_out, scale_out, True)
+    if done is not None:
+        return done
     ld = _rows(w, "w")
     N, K = w.shape
     dev = w.device
@@ -653,6 +669,9 @@ def quarot_add_rmsnorm_quant_fp8(x, residual=None, weight=None, eps: float = 1e-
     if stream is not None:
         with _on(stream, x):
             return quarot_add_rmsnorm_quant_fp8(x, residual, weight, eps, residual_out, q_out, scale_out)
+    done = (_calls or _loaded()).norm(x, residual, weight, eps, residual_out, q_out, scale_out)
+    if done is not None:
+        return done
     ld = _rows(x, "x")
     M, d = x.shape
     dev, dt = x.device, x.dtype
@@ -705,6 +724,9 @@ def quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y=None, out_dtype=torch.float16,
     if stream is not None:
         with _on(stream, a_q):
             return quarot_fp8_gemm(a_q, a_scale, w_q, w_scale, y, out_dtype)
+    done = (_calls or _loaded()).gemm(a_q, a_scale, w_q, w_scale, y, _DTYPES.get(out_dtype, -1))
+    if done is not None:
+        return done
     a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
     w, sw = _fp8_weight(w_q, w_scale, "w_q", K, dev)
     N = w_q.shape[0]
@@ -726,6 +748,9 @@ def quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out=No
     if stream is not None:
         with _on(stream, a_q):
             return quarot_fp8_gated_gemm(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out, scale_out)
+    done = (_calls or _loaded()).gated(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out, scale_out)
+    if done is not None:
+        return done
     a, sa, M, K, dev = _fp8_tokens(a_q, a_scale)
     g, sg = _fp8_weight(wg_q, wg_scale, "wg_q", K, dev)
     u, su = _fp8_weight(wu_q, wu_scale, "wu_q", K, dev)

@@ -1,8 +1,9 @@
-"""Builds libquarot.so in-tree for sm_103a with nvcc (no CMake, no torch).
+"""Builds libquarot.so in-tree for sm_103a with nvcc (no CMake, no torch), and
+beside it the Python module of the 8-bit calls (host code against torch).
 
 Each translation unit under csrc/ is compiled in parallel, as relocatable
 device code or (WHOLE_PROGRAM) by itself, then linked into a shared library next to this file.  A rebuild is
-skipped when the library is newer than every source and header.
+skipped when both are newer than every source and header.
 """
 from __future__ import annotations
 
@@ -11,12 +12,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libquarot.so")
+CALLS_SRC = os.path.join(CSRC, "fp8_calls.cpp")
+CALLS = os.path.join(HERE, "_fp8_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 WHOLE_PROGRAM = {"fp8_gemm.cu"}  # ptxas honours setmaxnreg only there
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
@@ -34,15 +38,32 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "quarot.h"),
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [CALLS_SRC, os.path.join(ROOT, "include", "quarot.h"),
                                                                   os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_calls(nvcc: str) -> None:
+    """The Python module of the 8-bit calls; torch is loaded before it, so its libraries need no path."""
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_CUDA",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(t, "include"),
+           "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), CALLS_SRC, "-o", tmp,
+           "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(CALLS_SRC)}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +84,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        calls = ex.submit(_build_calls, nvcc)
         logs = list(ex.map(compile_one, zip(srcs, objs)))
+        calls.result()
     if verbose:
         for log in logs:
             if log.strip():
