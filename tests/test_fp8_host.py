@@ -152,3 +152,19 @@ def test_product_brute_force():
     for i, j in ((0, 0), (1, 127), (0, 128), (1, 129)):
         want = sum(sa[k // 128, i] * sw[j // 128, k // 128] * a[i, k] * w[j, k] for k in range(K))
         assert math.isclose(y[i, j], want, rel_tol=1e-12) and mag[i, j] >= abs(want)
+
+
+def test_compiled_calls_leave_what_they_do_not_take(lib):
+    c = q._calls
+    x = torch.zeros(4, 256, dtype=torch.float16)
+    e = x.to(torch.float8_e4m3fn)
+    s = torch.ones(2, 4)
+    for bad in (x, None, 7, "x", np.zeros((4, 256), np.float16), torch.zeros(4, 256, dtype=torch.float16, device="meta")):
+        assert c.quant(bad, None, None, False) is None and c.quant(bad, None, None, True) is None
+        assert c.norm(bad, None, None, 1e-6, None, None, None) is None
+        assert c.gemm(bad, s, e, s, None, 0) is None and c.gated(bad, s, e, s, e, s, None, None) is None
+    assert c.quant(x) is None and c.norm() is None and c.gemm(e, s, e, s, None) is None and c.gated(e) is None
+    with pytest.raises(TypeError):
+        c.bind(1, 2)
+    with pytest.raises(TypeError):
+        c.bind(1, 2, 3, 4, "x")

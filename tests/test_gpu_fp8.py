@@ -511,6 +511,38 @@ def test_forked_and_joined_streams(q, M):
     q.quarot_check_error()
 
 
+class _Sub(torch.Tensor):
+    """A subclass, which the compiled form leaves to the general one."""
+
+
+def test_compiled_and_general_forms_agree(q):
+    M, K, N = 21, 272, 144
+    x, r, w = _rand((M, K), BF16, 40), _rand((M, K), BF16, 41), _rand((1, K), BF16, 42, loud=False)[0]
+    wt, wu = _weights(N, K, 43), _weights(N, K, 44)
+    wq, ws = q.quarot_quant_fp8_block(wt)
+    uq, us = q.quarot_quant_fp8_block(wu)
+
+    def all_of(x, r, wt):
+        a, sa, h = q.quarot_add_rmsnorm_quant_fp8(x, r, w)
+        b, sb, h0 = q.quarot_add_rmsnorm_quant_fp8(x)
+        assert h0 is x
+        b, sb, h1 = q.quarot_add_rmsnorm_quant_fp8(x, residual_out=torch.empty_like(r.as_subclass(torch.Tensor)))
+        a2, s2 = q.quarot_quant_fp8(x)
+        w2, ws2 = q.quarot_quant_fp8_block(wt)
+        like = (lambda t: t.as_subclass(_Sub)) if type(x) is _Sub else lambda t: t
+        y = q.quarot_fp8_gemm(like(a), sa, wq, ws, out_dtype=BF16)
+        z, sz = q.quarot_fp8_gated_gemm(like(a), sa, wq, ws, uq, us)
+        return a, sa, h, b, sb, h1, a2, s2, w2, ws2, y, z, sz
+
+    raw = lambda t: t.as_subclass(torch.Tensor).contiguous().view(torch.uint8)  # noqa: E731
+    got = all_of(x, r, wt)
+    want = all_of(x.as_subclass(_Sub), r.as_subclass(_Sub), wt.as_subclass(_Sub))
+    assert all(g.dtype == v.dtype and g.shape == v.shape and torch.equal(raw(g), raw(v)) for g, v in zip(got, want))
+    out = torch.empty((M, N), dtype=FP16, device=DEV)
+    assert q.quarot_fp8_gemm(got[0], got[1], wq, ws, y=out) is out
+    assert q.quarot_fp8_gemm(got[0].as_subclass(_Sub), got[1], wq, ws, y=out) is out
+
+
 def test_refusals(q):
     a, sa = _operand(4, 256, 1, False)
     w, sw = _operand(130, 256, 2, True)
