@@ -749,7 +749,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 
 // ===================================================================== narrow
 // Few tokens: the time is that of reading the weights once: 1 x 4096 x 12288 in
-// 11.8 us (4.3 TB/s), gated 4 x 12288 x 4096 in 18.8 us (5.4 TB/s), of which some
+// 11.3 us (4.5 TB/s), gated 4 x 12288 x 4096 in 18.7 us (5.4 TB/s), of which some
 // 4 us are launch, set-up, first load and join.
 //
 // A CTA takes 128 weight rows (gated: 128 gate and 128 up rows) as the MMA's M,
