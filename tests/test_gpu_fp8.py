@@ -511,6 +511,28 @@ def test_forked_and_joined_streams(q, M):
     q.quarot_check_error()
 
 
+@pytest.mark.parametrize("M,N,K", [(4200, 2304, 1040), (4096, 1536, 128), (700, 4000, 2064)])
+def test_many_tokens_repeat(q, M, N, K):
+    """Several tiles for each pair of CTAs, launch after launch and beside small calls of another stream: the same bits."""
+    a, sa = _operand(M, K, 70, False)
+    w, sw = _operand(N, K, 71, True)
+    u, su = _operand(N, K, 72, True)
+    sw.mul_(2.0 ** -8)
+    b, sb = _operand(9, K, 73, False)
+    want = q.quarot_fp8_gemm(a, sa, w, sw), *q.quarot_fp8_gated_gemm(a, sa, w, sw, u, su), q.quarot_fp8_gemm(b, sb, w, sw)
+    rows = torch.randint(0, M, (64,), generator=torch.Generator().manual_seed(74)).to(DEV)
+    _check_product(want[0][rows], a.view(torch.uint8)[rows].view(E4M3), sa[:, rows], w, sw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(25):
+        small = [q.quarot_fp8_gemm(b, sb, w, sw, stream=side) for _ in range(3)]
+        got = q.quarot_fp8_gemm(a, sa, w, sw), *q.quarot_fp8_gated_gemm(a, sa, w, sw, u, su)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g.view(torch.uint8), v.view(torch.uint8)) for g, v in zip(got, want))
+        assert all(torch.equal(y, want[3]) for y in small)
+    q.quarot_check_error()
+
+
 class _Sub(torch.Tensor):
     """A subclass, which the compiled form leaves to the general one."""
 

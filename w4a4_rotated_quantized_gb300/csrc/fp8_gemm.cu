@@ -1155,7 +1155,7 @@ static int run(const Args& p) {
   // empty: gated 333 x 4096 x 4096 (3 tiles of tokens) 17.1 us without, 17.8 with
   // pairs; gated 512 x 12288 x 4096 (4) 61.2 and 55.5.
   const int64_t pairs = ((p.M + 255) / 256) * ((p.N + TN - 1) / TN), room = sms / 2;
-  if ((pairs + room - 1) / room <= (tiles + sms - 1) / sms && 16 * pairs <= 9 * tiles) {
+  if (room > 0 && (pairs + room - 1) / room <= (tiles + sms - 1) / sms && 16 * pairs <= 9 * tiles) {
     static AttrCache attr;
     return launch(p, wide::wide_kernel<GATED, wide::PAIR, T>, attr, dim3(unsigned(2 * (pairs < room ? pairs : room))),
                   wide::NT, 2, wide::SMEM, 128, 128, static_cast<T*>(p.y));
