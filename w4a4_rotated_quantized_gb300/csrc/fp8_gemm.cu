@@ -53,13 +53,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// The same on the barriers at this place in both CTAs of a pair.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(uint16_t(3))
-      : "memory");
-}
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -98,16 +91,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-// One box at (x, y) into the same place of both CTAs of a pair; each one's own
-// barrier at `bar` counts the bytes.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-      "[%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "h"(uint16_t(3))
       : "memory");
 }
 
@@ -272,19 +255,18 @@ __device__ __forceinline__ float2 silu_mul(float2 g, float2 u) {
 // memory traffic, lose more to their remote barriers than they gain), and a
 // k-block's scale is read from shared memory while the one before is summed.
 //
-// PAIR: the CTAs of a cluster of two take two tiles with the same weight rows,
-// and each loads 128 of them into both (32 KB of loads for a stage of 48).  A
-// stage is empty when both have used it; all other barriers stay local.  Loads
-// from L2 had held the tensor cores up and the clock down: gated 4096 x 12288 x
-// 4096 412 -> 362 us, 8192 x 12288 x 4096 340 -> 330 us, 2048 x 4096 x 12288 86.4
-// -> 84.4 us, hot.
+// Every CTA loads its own weight rows, 48 KB a stage from L2, which holds the
+// tensor cores up a little and costs power.  (A cluster of two that loads each
+// row once for both was 2 to 6 % faster on the plain products, 77.1 and 295 us
+// below, and no faster on the gated one.  It needs loads into another CTA's shared
+// memory, which are left to programs on a single GPU.)
 //
-// 2048 x 4096 x 12288: 77.5 us, 2660 TFLOP/s, 69 % of twice the bf16 rate, with 1.68
-// rounds of tiles; 8192 x 12288 x 4096: 294 us, 73 %; gated 4096 x 12288 x 4096: 311
-// us, 69 %, with silu and the quantizer between tiles.  Hot, at the power limit:
-// 86, 334, 342 us.
+// 2048 x 4096 x 12288: 78.7 us, 2620 TFLOP/s, 68 % of twice the bf16 rate, with 1.68
+// rounds of tiles; 8192 x 12288 x 4096: 302 us, 71 %; gated 4096 x 12288 x 4096: 340
+// us, 63 %, with silu and the quantizer between tiles.  Hot, at the power limit:
+// 87, 316, 330 us.
 //
-// SPLIT_DEPTH: fewer tiles than SMs.  A cluster takes one tile, each CTA a share of
+// SPLIT: fewer tiles than SMs.  A cluster takes one tile, each CTA a share of
 // the depth; the sums are joined through distributed shared memory in rank
 // order (no workspace, no atomics, the same bits every time).
 namespace wide {
@@ -309,19 +291,12 @@ constexpr uint32_t TMEM_COLS = 512;
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(128 * REG_LO + 256 * REG_HI <= NT * 168, "register split");
 
-enum Form { SINGLE, SPLIT_DEPTH, PAIR };
-
-// A k-block at depth x of 128 tokens from m0 and of the tile's weight rows
-// (in a pair each CTA brings 128 of them to both).
-template <bool GATED, Form FORM>
+// A k-block at depth x of 128 tokens from m0 and of the tile's weight rows.
+template <bool GATED>
 __device__ __forceinline__ void load_stage(const CUtensorMap* tmA, const CUtensorMap* tmW0, const CUtensorMap* tmW1,
-                                           uint32_t bar, uint32_t st, int m0, int w0, int x, int rank) {
+                                           uint32_t bar, uint32_t st, int m0, int w0, int x) {
   mbar_arrive_expect_tx(bar, STAGE);
   tma_load(st, tmA, x, m0, bar);
-  if constexpr (FORM == PAIR) {
-    tma_load_pair(st + A_BYTES + rank * (B_BYTES / 2), GATED && rank ? tmW1 : tmW0, x, GATED ? w0 : w0 + 128 * rank, bar);
-    return;
-  }
   tma_load(st + A_BYTES, tmW0, x, w0, bar);
   tma_load(st + A_BYTES + B_BYTES / 2, GATED ? tmW1 : tmW0, x, GATED ? w0 : w0 + 128, bar);
 }
@@ -329,8 +304,9 @@ __device__ __forceinline__ void load_stage(const CUtensorMap* tmA, const CUtenso
 // Tile number `tile` as (tile of tokens, tile of columns): GM tiles of tokens by all
 // the columns, then the next GM, so that what the CTAs work on at one time needs
 // little of either operand: gated 4096 x 12288 x 4096, whose weights are 100 MB,
-// 362 us column by column (GM = 1), 346 with 8, 342 with 16, 342 with 32.
-constexpr int GM = 16;
+// 351 us with GM = 4, 348 with 8, 343 with 16, 334 with 32, 333 with 64; 2048 x 4096 x
+// 12288, hot, 91, 90, 90, 87, 87.
+constexpr int GM = 32;
 __device__ __forceinline__ int2 tile_at(int tile, int tiles_m, int tiles_n) {
   const int g = tile / (GM * tiles_n), rows = min(GM, tiles_m - g * GM), i = tile - g * GM * tiles_n;
   return make_int2(g * GM + i % rows, i / rows);
@@ -351,7 +327,7 @@ __device__ __forceinline__ void store16(const CUtensorMap* tm, int x, int y, uin
   }
 }
 
-template <bool GATED, Form FORM, typename T>
+template <bool GATED, bool SPLIT, typename T>
 __global__ void __launch_bounds__(NT, 1)
 wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW0,
             const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmY, const float* __restrict__ as, const float* __restrict__ ws0,
@@ -372,16 +348,12 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   // the shuffles tell the compiler what is the same in all lanes: the roles'
   // branches, the barriers' and the tensor memory's addresses (20 % of the time)
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  constexpr bool SPLIT = FORM == SPLIT_DEPTH;
-  constexpr int TN = GATED ? 128 : 256;           // output columns of a tile
-  constexpr int TM = FORM == PAIR ? 256 : 128;    // tokens of a CTA's, or a pair's, tile
+  constexpr int TM = 128, TN = GATED ? 128 : 256;  // tokens and output columns of a tile
   const int tiles_n = (N + TN - 1) / TN, nblk = (N + BLK - 1) / BLK;
   const int tiles_m = (M + TM - 1) / TM, n_tiles = tiles_m * tiles_n;
-  // tiles of this CTA (or pair), and its k-blocks of each
-  const int ranks = SPLIT ? int(cluster_size()) : 1, rank = FORM == SINGLE ? 0 : int(cluster_rank());
-  const int group = FORM == PAIR ? 2 : ranks;
-  const int tile0 = int(blockIdx.x) / group, tstep = SPLIT ? n_tiles : int(gridDim.x) / group;
-  const int mr = FORM == PAIR ? 128 * rank : 0;  // this CTA's first token of a tile
+  // tiles of this CTA, and its k-blocks of each
+  const int ranks = SPLIT ? int(cluster_size()) : 1, rank = SPLIT ? int(cluster_rank()) : 0;
+  const int tile0 = int(blockIdx.x) / ranks, tstep = SPLIT ? n_tiles : int(gridDim.x);
   const int kb0 = SPLIT ? nkb * rank / ranks : 0, kb1 = SPLIT ? nkb * (rank + 1) / ranks : nkb;
 
   if (threadIdx.x == 0) {
@@ -390,7 +362,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     if (GATED) prefetch_map(&tmW1);
     for (int s = 0; s < S; ++s) {
       mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, FORM == PAIR ? 2 : 1);
+      mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8 * i, 1);
@@ -405,15 +377,14 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       wait_for_previous();
       for (int s = 0; s < min(S, kb1 - kb0); ++s)
-        load_stage<GATED, FORM>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE),
-                                tile_at(tile0, tiles_m, tiles_n).x * TM, tile_at(tile0, tiles_m, tiles_n).y * TN,
-                                (kb0 + s) * BK, rank);
+        load_stage<GATED>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE),
+                          tile_at(tile0, tiles_m, tiles_n).x * TM, tile_at(tile0, tiles_m, tiles_n).y * TN,
+                          (kb0 + s) * BK);
     }
   }
   if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(slot)), TMEM_COLS);
   fence_before_sync();
   __syncthreads();
-  if constexpr (FORM == PAIR) cluster_sync();  // the other CTA's barriers are set up
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
   wait_for_previous();
@@ -428,21 +399,18 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint32_t par = 0, it = 0;
         for (int tile = tile0; ok && tile < n_tiles; tile += tstep) {
           const int2 at = tile_at(tile, tiles_m, tiles_n);
-          const int m0 = at.x * TM + mr, w0 = at.y * TN;
+          const int m0 = at.x * TM, w0 = at.y * TN;
           for (int kb = kb0; kb < kb1; ++kb, ++it) {
             if (!SPLIT || it >= S) {
               ok = wait_one(empty + 8 * s, par ^ 1u);
               if (!ok) break;
-              load_stage<GATED, FORM>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE), m0, w0, kb * BK, rank);
+              load_stage<GATED>(&tmA, &tmW0, &tmW1, full + 8 * s, smem_u32(sm + s * STAGE), m0, w0, kb * BK);
             }
             if (++s == S) { s = 0; par ^= 1u; }
           }
         }
         // whatever happens elsewhere, no copy is in flight when the CTA ends
-        for (uint32_t j = it > S ? it - S : 0; j < it; ++j) {
-          ok = wait_one(full + 8 * (j % S), (j / S) & 1) && ok;
-          if constexpr (FORM == PAIR) ok = wait_one(empty + 8 * (j % S), (j / S) & 1) && ok;  // nor an arrival
-        }
+        for (uint32_t j = it > S ? it - S : 0; j < it; ++j) ok = wait_one(full + 8 * (j % S), (j / S) & 1) && ok;
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -461,8 +429,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk) mma(tmem + 256u * b, ad + 2 * kk, bd + 2 * kk, idesc(128, 256), kk != 0);
             commit(acc_full + 8 * b);
-            if constexpr (FORM == PAIR) commit_pair(empty + 8 * s);
-            else commit(empty + 8 * s);
+            commit(empty + 8 * s);
             if (++s == S) { s = 0; par ^= 1u; }
           }
         commit(drain);
@@ -479,7 +446,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       uint32_t it = 0;
       for (int tile = tile0; ok && tile < n_tiles; tile += tstep) {
         const int2 at = tile_at(tile, tiles_m, tiles_n);
-        const int nt = at.y, m = at.x * TM + mr + lane;
+        const int nt = at.y, m = at.x * TM + lane;
         const float* pa = as + size_t(kb0) * M + m;
         const float* pw = kb0 + (lane == 0 ? ws0 + size_t(GATED ? nt : 2 * nt) * nkb
                                     : (GATED ? ws1 + size_t(nt) * nkb : ws0 + size_t(min(2 * nt + 1, nblk - 1)) * nkb));
@@ -525,7 +492,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     if (last > 0) next_scales();
     for (int tile = tile0; ok && tile < n_tiles; tile += tstep, ++ti) {
       const int2 at = tile_at(tile, tiles_m, tiles_n);
-      const int gm = at.x * TM + mr + r, nt = at.y;
+      const int gm = at.x * TM + r, nt = at.y;
       const bool in = gm < M;
       float2 acc[64];
 #pragma unroll
@@ -741,8 +708,6 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     fence_after_sync();
     tmem_free(tmem, TMEM_COLS);
   }
-  // the other CTA neither loads into this one's shared memory nor arrives there any more
-  if constexpr (FORM == PAIR) cluster_sync();
 }
 
 }  // namespace wide
@@ -1148,20 +1113,11 @@ static int run(const Args& p) {
   const int ranks = split_ranks(tiles, nkb, sms);
   if (ranks > 1) {
     static AttrCache attr;
-    return launch(p, wide::wide_kernel<GATED, wide::SPLIT_DEPTH, T>, attr, dim3(unsigned(tiles * ranks)), wide::NT, ranks, wide::SMEM,
+    return launch(p, wide::wide_kernel<GATED, true, T>, attr, dim3(unsigned(tiles * ranks)), wide::NT, ranks, wide::SMEM,
                   128, 128, static_cast<T*>(p.y));
   }
-  // Pairs where they take as few rounds and leave at most an eighth of the work
-  // empty: gated 333 x 4096 x 4096 (3 tiles of tokens) 17.1 us without, 17.8 with
-  // pairs; gated 512 x 12288 x 4096 (4) 61.2 and 55.5.
-  const int64_t pairs = ((p.M + 255) / 256) * ((p.N + TN - 1) / TN), room = sms / 2;
-  if (room > 0 && (pairs + room - 1) / room <= (tiles + sms - 1) / sms && 16 * pairs <= 9 * tiles) {
-    static AttrCache attr;
-    return launch(p, wide::wide_kernel<GATED, wide::PAIR, T>, attr, dim3(unsigned(2 * (pairs < room ? pairs : room))),
-                  wide::NT, 2, wide::SMEM, 128, 128, static_cast<T*>(p.y));
-  }
   static AttrCache attr;
-  return launch(p, wide::wide_kernel<GATED, wide::SINGLE, T>, attr, dim3(unsigned(tiles < sms ? tiles : sms)), wide::NT, 1,
+  return launch(p, wide::wide_kernel<GATED, false, T>, attr, dim3(unsigned(tiles < sms ? tiles : sms)), wide::NT, 1,
                 wide::SMEM, 128, 128, static_cast<T*>(p.y));
 }
 
