@@ -22,11 +22,11 @@ unsigned long long current_context_id() {
   std::call_once(g_fn_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 4000, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       g_get_ctx = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn);
     fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPointByVersion("cuCtxGetId", &fn, 12000, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       g_get_id = reinterpret_cast<PFN_cuCtxGetId_v12000>(fn);
   });
@@ -64,10 +64,10 @@ extern "C" const char* quarot_status_string(int status) {
 extern "C" int quarot_version(void) { return (1 << 16) | 1; }
 
 extern "C" int quarot_check_error(void* stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QUAROT_ERR_CUDA;
+  if (!quarot::cuda_ok(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)))) return QUAROT_ERR_CUDA;
   unsigned int word = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&word, quarot::g_error_word, sizeof(word)) != cudaSuccess) return QUAROT_ERR_CUDA;
-  if (word != 0 && cudaMemcpyToSymbol(quarot::g_error_word, &zero, sizeof(zero)) != cudaSuccess)
+  if (!quarot::cuda_ok(cudaMemcpyFromSymbol(&word, quarot::g_error_word, sizeof(word)))) return QUAROT_ERR_CUDA;
+  if (word != 0 && !quarot::cuda_ok(cudaMemcpyToSymbol(quarot::g_error_word, &zero, sizeof(zero))))
     return QUAROT_ERR_CUDA;
   unsigned int fp8_word = 0;
   if (!quarot::take_fp8_error_word(&fp8_word)) return QUAROT_ERR_CUDA;

@@ -36,6 +36,15 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 constexpr int kDecodeHeadDim = 128;
 constexpr int kDecodeMaxGroup = 8;
 
+// Whether a runtime call succeeded.  A failed one leaves its error for the
+// thread's next cudaGetLastError(), which the next kernel launch would take for
+// its own: it is cleared here, and the caller returns its status.
+inline bool cuda_ok(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  return false;
+}
+
 // Unique id (cuCtxGetId) of the calling thread's current CUDA context, or 0
 // when no context is current or the driver cannot say.  Defined in abi.cu.
 unsigned long long current_context_id();
@@ -51,13 +60,13 @@ struct AttrCache {
 template <typename Kernel>
 inline bool smem_attr_once(Kernel* kern, int bytes, AttrCache& done) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (!cuda_ok(cudaGetDevice(&dev))) return false;
   const bool cached = dev >= 0 && dev < 64;
   if (cached) {
     const unsigned long long id = current_context_id();
     if (id != 0 && done.ctx[dev].load(std::memory_order_acquire) == id) return true;
   }
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (!cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return false;
   if (cached) done.ctx[dev].store(current_context_id(), std::memory_order_release);
   return true;
 }

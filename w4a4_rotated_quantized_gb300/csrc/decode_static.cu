@@ -41,7 +41,7 @@ Cached g_cache[kMaxDevices];
 void* scratch_on_current_device(cudaError_t* err) {
   int dev = -1;
   *err = cudaGetDevice(&dev);
-  if (*err != cudaSuccess) return nullptr;
+  if (!cuda_ok(*err)) return nullptr;
   if (dev < 0 || dev >= kMaxDevices) {
     *err = cudaErrorInvalidDevice;
     return nullptr;
@@ -54,7 +54,7 @@ void* scratch_on_current_device(cudaError_t* err) {
   // the device's primary context current)
   void* p = nullptr;
   *err = cudaGetSymbolAddress(&p, g_decode_scratch);
-  if (*err != cudaSuccess) return nullptr;
+  if (!cuda_ok(*err)) return nullptr;
   id = current_context_id();
   if (id == 0) {
     *err = cudaErrorContextIsDestroyed;

@@ -124,7 +124,7 @@ inline int launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, siz
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  return cuda_ok(e) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }
 
 }  // namespace fp8

@@ -991,7 +991,7 @@ static bool get_encoder() {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult r;
     void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r)) &&
         r == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
@@ -1022,8 +1022,8 @@ static bool make_out_map(CUtensorMap* tm, void* base, int64_t rows, int64_t N) {
 
 static int sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (!cuda_ok(cudaGetDevice(&dev))) return 0;
+  if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
   return n;
 }
 
@@ -1129,8 +1129,8 @@ using namespace quarot;
 
 bool quarot::take_fp8_error_word(unsigned int* word) {
   const unsigned int zero = 0;
-  if (cudaMemcpyFromSymbol(word, g_error_word, sizeof(zero)) != cudaSuccess) return false;
-  return *word == 0 || cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) == cudaSuccess;
+  if (!cuda_ok(cudaMemcpyFromSymbol(word, g_error_word, sizeof(zero)))) return false;
+  return *word == 0 || cuda_ok(cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)));
 }
 
 extern "C" int quarot_fp8_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q, const float* w_scale,

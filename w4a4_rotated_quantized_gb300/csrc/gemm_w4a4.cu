@@ -1640,8 +1640,7 @@ static bool get_encoder() {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
@@ -1732,8 +1731,8 @@ static void plan(int64_t M, int64_t N, int64_t K, int sms, int* form, int* bn) {
 
 static int sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (!cuda_ok(cudaGetDevice(&dev))) return 0;
+  if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
   return n;
 }
 
@@ -1801,7 +1800,7 @@ static int w4a4_gemm_impl(const uint8_t* a_q, const void* a_scale, const int32_t
                                              static_cast<const __half*>(a_scale), static_cast<const __half*>(w_scale),
                                              int(M), int(N), int(K), bn, static_cast<__half*>(y), acc_out,
                                              pre ? a_rowsum : nullptr, pre ? w_rowsum : nullptr);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+    return cuda_ok(e) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
   }
   CUtensorMap ta, tb;
   if (!make_map(&ta, a_q, M, K, BM) || !make_map(&tb, w_q, N, K, bn)) return QUAROT_ERR_CUDA;
@@ -1912,7 +1911,7 @@ extern "C" int quarot_w4a4_gemm_a8(const uint8_t* a8, const int32_t* a_rowsum, c
                                            static_cast<const __half*>(a_scale), a_rowsum,
                                            static_cast<const __half*>(w_scale), int(M), int(N), int(K), bn,
                                            static_cast<__half*>(y), acc_out);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  return cuda_ok(e) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }
 
 extern "C" int quarot_w4a4_gemm_plan(int64_t M, int64_t N, int64_t K, int sms, int* form, int* bn) {

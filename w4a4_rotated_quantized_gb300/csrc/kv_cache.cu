@@ -702,7 +702,7 @@ int decode_ctas_per_sm(int G) {
       case 4: e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<4, ASYM>, DT, decode_smem_bytes<4>()); break;
       default: e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<8, ASYM>, DT, decode_smem_bytes<8>()); break;
     }
-    cache[slot] = (e == cudaSuccess && n > 0) ? n : 1;
+    cache[slot] = (cuda_ok(e) && n > 0) ? n : 1;
   }
   return cache[slot];
 }
@@ -714,7 +714,7 @@ int kv_write_ctas_per_sm() {
   static std::atomic<int> cache{0};
   int n = cache.load(std::memory_order_relaxed);
   if (n < 1) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_write_kernel<D, ASYM, true>, 256, 0) != cudaSuccess || n < 1)
+    if (!cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_write_kernel<D, ASYM, true>, 256, 0)) || n < 1)
       n = 1;
     cache.store(n, std::memory_order_relaxed);
   }
@@ -742,7 +742,8 @@ static int kv_write_impl(bool asym, const void* k, const void* v, int64_t B, int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t threads = B * Hkv * T_new * (d / 32);
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (!quarot::cuda_ok(cudaGetDevice(&dev)) ||
+      !quarot::cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return QUAROT_ERR_CUDA;
   const int64_t need = (threads + 255) / 256;
   auto go = [&](auto kern_one, auto kern_strided, int per_sm) {
@@ -802,7 +803,7 @@ static int decode_impl(const void* q, const uint8_t* k_q, const void* k_s, const
   if (!q || !out) return QUAROT_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) {
-    return cudaMemsetAsync(out, 0, size_t(B * Hq * d) * 2, st) == cudaSuccess ? QUAROT_OK : QUAROT_ERR_CUDA;
+    return quarot::cuda_ok(cudaMemsetAsync(out, 0, size_t(B * Hq * d) * 2, st)) ? QUAROT_OK : QUAROT_ERR_CUDA;
   }
   if (!k_q || !k_s || !v_q || !v_s || !workspace || (ASYM && (!k_z || !v_z))) return QUAROT_ERR_INVALID_ARG;
   if (ws_bytes < quarot_decode_workspace_bytes(B, Hq, d, T)) return QUAROT_ERR_INVALID_ARG;
@@ -816,7 +817,8 @@ static int decode_impl(const void* q, const uint8_t* k_q, const void* k_s, const
   // tokens; chunks are multiples of 16 tokens.
   const int G = int(Hq / Hkv);
   int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (quarot::cuda_ok(cudaGetDevice(&dev)))
+    (void)quarot::cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const int per_sm = kv::decode_ctas_per_sm<ASYM>(G);
   const int64_t max_splits = kv::num_splits(T);
   int64_t want = (int64_t(per_sm) * sms) / (B * Hkv);
@@ -866,9 +868,9 @@ static int decode_impl(const void* q, const uint8_t* k_q, const void* k_s, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv::decode_combine_kernel, static_cast<const float*>(ws_o),
-                         static_cast<const float*>(ws_ml), splits, unrotate_out, static_cast<__half*>(out)) !=
-      cudaSuccess)
+  if (!quarot::cuda_ok(cudaLaunchKernelEx(&cfg, kv::decode_combine_kernel, static_cast<const float*>(ws_o),
+                                          static_cast<const float*>(ws_ml), splits, unrotate_out,
+                                          static_cast<__half*>(out))))
     return QUAROT_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }

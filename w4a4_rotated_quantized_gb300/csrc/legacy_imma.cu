@@ -99,8 +99,8 @@ extern "C" int quarot_legacy_imma_probe(int bits, int iters, int32_t* sink, int6
     return QUAROT_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(sink) & 3) return QUAROT_ERR_ALIGNMENT;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+  if (!quarot::cuda_ok(cudaGetDevice(&dev)) ||
+      !quarot::cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
     return QUAROT_ERR_CUDA;
   const int blocks = sms * kBlocksPerSm;
   const int64_t k = bits == 8 ? 32 : bits == 4 ? 64 : 16;

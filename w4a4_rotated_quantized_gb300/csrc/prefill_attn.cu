@@ -865,7 +865,7 @@ extern "C" int quarot_prefill_attn(const void* q, const uint8_t* k_q, const void
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_attn_kernel<true>, qh, k_q, ksh, v_q, vsh, int(B),
                                              int(Hq), int(Hkv), int(T), int(T_max), qscale, causal, oh);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+    return quarot::cuda_ok(e) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
   }
   static quarot::AttrCache attr1;
   if (!quarot::smem_attr_once(prefill_attn_kernel<false>, Plan<false>::SMEM_BYTES, attr1)) return QUAROT_ERR_LAUNCH;

@@ -895,12 +895,13 @@ static int launch_seg16(const void* x, int64_t M, int64_t ld_x, const int8_t* si
   if (!smem_attr_once(kern, int(PL::SMEM), attr_done)) return QUAROT_ERR_LAUNCH;
   if ((reinterpret_cast<uintptr_t>(x) & 15) || ((ld_x * 2) & 15)) return QUAROT_ERR_ALIGNMENT;
   int dev = 0, sms = 1;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (!quarot::cuda_ok(cudaGetDevice(&dev)) ||
+      !quarot::cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return QUAROT_ERR_CUDA;
   const bool known = dev >= 0 && dev < 64;
   int per_sm = known ? per_sm_dev[dev].load(std::memory_order_relaxed) : 0;
   if (per_sm < 1) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, PL::NT, PL::SMEM) != cudaSuccess || per_sm < 1)
+    if (!quarot::cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, PL::NT, PL::SMEM)) || per_sm < 1)
       per_sm = 1;
     if (known) per_sm_dev[dev].store(per_sm, std::memory_order_relaxed);
   }
@@ -923,12 +924,13 @@ static int launch_seg_t(const void* x, int64_t M, int64_t ld_x, const int8_t* si
   int64_t blocks = (M + PL::RPC - 1) / PL::RPC;
   if constexpr (STAGED) {
     int dev = 0, sms = 1;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    if (!quarot::cuda_ok(cudaGetDevice(&dev)) ||
+        !quarot::cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
       return QUAROT_ERR_CUDA;
     const bool known = dev >= 0 && dev < 64;
     int per_sm = known ? per_sm_dev[dev].load(std::memory_order_relaxed) : 0;
     if (per_sm < 1) {
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, PL::NT, PL::SMEM) != cudaSuccess || per_sm < 1)
+      if (!quarot::cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, PL::NT, PL::SMEM)) || per_sm < 1)
         per_sm = 1;
       if (known) per_sm_dev[dev].store(per_sm, std::memory_order_relaxed);
     }
