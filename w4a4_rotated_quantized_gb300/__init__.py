@@ -115,6 +115,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
         "quarot_quant_fp8", "quarot_quant_fp8_block", "quarot_add_rmsnorm_quant_fp8", "quarot_fp8_gemm",
         "quarot_fp8_gated_gemm")))
+    calls.error = QuarotError
     _calls = calls
     _lib = lib
     return lib
@@ -563,7 +564,7 @@ _E4M3 = torch.float8_e4m3fn
 # A decode step makes a handful of these calls with microseconds of GPU work
 # each, so what they mostly get (dense tensors on the current device and
 # stream) goes through the compiled _calls; it returns None for anything else,
-# which the checks here then take, or say what is wrong with.
+# with nothing launched, which the checks here then take, or say what is wrong with.
 def _loaded():
     load()
     return _calls

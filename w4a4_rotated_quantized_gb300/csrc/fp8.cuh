@@ -106,6 +106,7 @@ __device__ __forceinline__ uint32_t cvt_e4m3x4(float2 a, float2 b) { return cvt_
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The status is that of this launch alone.
 template <typename... P, typename... A>
 inline int launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
                             cudaStream_t st, A... args) {
@@ -123,8 +124,7 @@ inline int launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, siz
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
-  return cuda_ok(e) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kern, P(args)...)) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }
 
 }  // namespace fp8

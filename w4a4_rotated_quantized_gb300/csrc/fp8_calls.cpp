@@ -6,8 +6,10 @@
 // of which the launch is 2.
 //
 // Whatever is not plainly right (a shape, a type, a stride, a device that is
-// not the current one, a refused size) gives None, without side effects: the
-// package's general path then handles the call or says what is wrong with it.
+// not the current one, a refused size) gives None, and nothing has been
+// launched: the package's general path then handles the call or says what is
+// wrong with it.  An entry point that got as far as its launch and failed
+// raises, so that no call is ever made twice.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -86,12 +88,25 @@ PyObject* tuple_of(std::initializer_list<PyObject*> items) {
   if (t != nullptr && i != Py_ssize_t(items.size())) Py_CLEAR(t);
   return t;
 }
+// What a status other than OK gives.  The first three are refusals, found
+// before anything is launched: None.  The others raise the module's `error`.
+PyObject* refused(PyObject* module, int status, const char* where) {
+  if (status == QUAROT_ERR_INVALID_ARG || status == QUAROT_ERR_UNSUPPORTED || status == QUAROT_ERR_ALIGNMENT)
+    Py_RETURN_NONE;
+  PyObject* type = PyObject_GetAttrString(module, "error");
+  if (type == nullptr) return nullptr;
+  PyObject* e = PyObject_CallFunction(type, "is", status, where);
+  if (e != nullptr) PyErr_SetObject(type, e);
+  Py_XDECREF(e);
+  Py_DECREF(type);
+  return nullptr;
+}
 void* stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 uint8_t* u8(const Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
 float* f32(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 
 // quant(x, q_out, scale_out, weights)
-PyObject* quant(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* quant(PyObject* module, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 4 || g_quant == nullptr) Py_RETURN_NONE;
   const int dev = device_of(args[0]);
@@ -105,13 +120,13 @@ PyObject* quant(PyObject*, PyObject* const* args, Py_ssize_t n) {
       !output(args[2], kScale, weights ? blocks(M) : blocks(d), weights ? blocks(d) : M, dev, s))
     Py_RETURN_NONE;
   const int st = (weights ? g_quant_block : g_quant)(x->data_ptr(), dtype_of(*x), M, d, d, u8(q), f32(s), stream(dev));
-  if (st != QUAROT_OK) Py_RETURN_NONE;
+  if (st != QUAROT_OK) return refused(module, st, weights ? "quarot_quant_fp8_block" : "quarot_quant_fp8");
   return tuple_of({back(args[1], q), back(args[2], s)});
   END_HANDLE_TH_ERRORS
 }
 
 // norm(x, residual, weight, eps, residual_out, q_out, scale_out)
-PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* norm(PyObject* module, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 7 || g_norm == nullptr || !PyFloat_CheckExact(args[3])) Py_RETURN_NONE;
   const int dev = device_of(args[0]);
@@ -140,7 +155,7 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int st = g_norm(x->data_ptr(), d, r != nullptr ? r->data_ptr() : nullptr, d, w, dtype_of(*x), M, d,
                         float(PyFloat_AS_DOUBLE(args[3])), has_h ? h.data_ptr() : nullptr, d, u8(q), f32(s), stream(dev));
-  if (st != QUAROT_OK) Py_RETURN_NONE;
+  if (st != QUAROT_OK) return refused(module, st, "quarot_add_rmsnorm_quant_fp8");
   return tuple_of({back(args[5], q), back(args[6], s), has_h ? back(args[4], h) : back(args[0], *x)});
   END_HANDLE_TH_ERRORS
 }
@@ -154,7 +169,7 @@ bool weights(const Tensor* w, const Tensor* ws, int64_t K) {
 }
 
 // gemm(a_q, a_scale, w_q, w_scale, y, dtype): dtype is that of an output that is not given
-PyObject* gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* gemm(PyObject* module, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 6 || g_gemm == nullptr || !PyLong_CheckExact(args[5])) Py_RETURN_NONE;
   const int dev = device_of(args[0]);
@@ -171,13 +186,13 @@ PyObject* gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Tensor y;
   if (!output(args[4], dt == QUAROT_FP16 ? ScalarType::Half : ScalarType::BFloat16, M, N, dev, y)) Py_RETURN_NONE;
   const int st = g_gemm(u8(*a), f32(*as), u8(*w), f32(*ws), M, N, K, y.data_ptr(), int(dt), stream(dev));
-  if (st != QUAROT_OK) Py_RETURN_NONE;
+  if (st != QUAROT_OK) return refused(module, st, "quarot_fp8_gemm");
   return back(args[4], y);
   END_HANDLE_TH_ERRORS
 }
 
 // gated(a_q, a_scale, wg_q, wg_scale, wu_q, wu_scale, q_out, scale_out)
-PyObject* gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* gated(PyObject* module, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 8 || g_gated == nullptr) Py_RETURN_NONE;
   const int dev = device_of(args[0]);
@@ -192,7 +207,7 @@ PyObject* gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!output(args[6], kCode, M, I, dev, q) || !output(args[7], kScale, blocks(I), M, dev, s)) Py_RETURN_NONE;
   const int st = g_gated(u8(*t[0]), f32(*t[1]), u8(*t[2]), f32(*t[3]), u8(*t[4]), f32(*t[5]), M, I, K, u8(q), f32(s),
                          stream(dev));
-  if (st != QUAROT_OK) Py_RETURN_NONE;
+  if (st != QUAROT_OK) return refused(module, st, "quarot_fp8_gated_gemm");
   return tuple_of({back(args[6], q), back(args[7], s)});
   END_HANDLE_TH_ERRORS
 }
