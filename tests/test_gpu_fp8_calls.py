@@ -76,3 +76,14 @@ def test_in_place_after_an_earlier_error_adds_once(q, target):  # noqa: F811
     assert torch.equal(h, want[2]) and torch.equal(scale, want[1])
     assert torch.equal(codes.view(torch.uint8), want[0].view(torch.uint8)) and codes.dtype == E4M3
     q.quarot_check_error()
+
+
+def test_the_general_path_alone_gives_the_same_bits(q, monkeypatch):  # noqa: F811
+    raw = lambda v: [t.view(torch.uint8).clone() for t in (v if isinstance(v, tuple) else (v,))]  # noqa: E731
+    calls = _all_calls(q)
+    calls["quarot_add_rmsnorm_quant_fp8"] = lambda: q.quarot_add_rmsnorm_quant_fp8(_rand((4, 256), FP16, 1), _rand((4, 256), FP16, 2))
+    want = {n: raw(c()) for n, c in calls.items()}
+    monkeypatch.setattr(q, "_calls", q._GeneralOnly())
+    for n, c in calls.items():
+        got = raw(c())
+        assert len(got) == len(want[n]) and all(torch.equal(g, w) for g, w in zip(got, want[n]))

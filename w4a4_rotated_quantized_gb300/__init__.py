@@ -26,12 +26,12 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libquarot.so")
-CALLS_PATH = os.path.join(_HERE, "_fp8_calls.so")
 
 QUAROT_OK = 0
 QUAROT_ERR_TIMEOUT = 5
@@ -91,9 +91,41 @@ class QuarotError(RuntimeError):
         self.status = status
 
 
+class _GeneralOnly:
+    """In the place of the compiled form of the 8-bit calls where there is none: takes nothing."""
+
+    def quant(self, *args):
+        return None
+
+    norm = gemm = gated = quant
+
+
+def _load_calls(lib):
+    """The compiled form of the 8-bit calls, bound to `lib`.  Where it was not
+    built for this Python and torch, or does not load, every call takes the
+    general path, which gives the same results."""
+    from .build import calls_path
+
+    path = calls_path()
+    if not os.path.exists(path):
+        return _GeneralOnly()
+    try:
+        spec = importlib.util.spec_from_file_location("_fp8_calls", path)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+    except ImportError as e:
+        warnings.warn(f"the compiled 8-bit calls do not load, the general path takes them: {e}", RuntimeWarning)
+        return _GeneralOnly()
+    calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "quarot_quant_fp8", "quarot_quant_fp8_block", "quarot_add_rmsnorm_quant_fp8", "quarot_fp8_gemm",
+        "quarot_fp8_gated_gemm")))
+    calls.error = QuarotError
+    return calls
+
+
 def load(path: str | None = None) -> ctypes.CDLL:
     """Loads libquarot.so (once) and declares the ABI signatures; the compiled
-    form of the 8-bit calls comes with it."""
+    form of the 8-bit calls comes with it where it was built."""
     global _lib, _calls
     if _lib is not None:
         return _lib
@@ -101,22 +133,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise QuarotError(6, f"libquarot.so not found at {p}; build it with "
                              "w4a4_rotated_quantized_gb300.build.build()")
-    if not os.path.exists(CALLS_PATH):
-        raise QuarotError(6, f"_fp8_calls.so not found at {CALLS_PATH}; build it with "
-                             "w4a4_rotated_quantized_gb300.build.build()")
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    spec = importlib.util.spec_from_file_location("_fp8_calls", CALLS_PATH)
-    calls = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(calls)
-    calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-        "quarot_quant_fp8", "quarot_quant_fp8_block", "quarot_add_rmsnorm_quant_fp8", "quarot_fp8_gemm",
-        "quarot_fp8_gated_gemm")))
-    calls.error = QuarotError
-    _calls = calls
+    _calls = _load_calls(lib)
     _lib = lib
     return lib
 
