@@ -58,9 +58,10 @@ const char* quarot_status_string(int status);
 /* ABI version: (major << 16) | minor.  1.1 adds, with every 1.0 entry point
  * unchanged: quarot_w4a4_gemm_plan, quarot_legacy_imma_probe,
  * quarot_rotate_quant_a8, quarot_w4a4_gemm_a8, quarot_rotate_quant_rowsum,
- * quarot_int4_rowsum and quarot_w4a4_gemm_rowsums; and the 8-bit layer
- * quarot_quant_fp8, quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8,
- * quarot_fp8_gemm and quarot_fp8_gated_gemm. */
+ * quarot_int4_rowsum and quarot_w4a4_gemm_rowsums.  1.2 adds, with every 1.1
+ * entry point unchanged, the 8-bit layer: quarot_quant_fp8,
+ * quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8, quarot_fp8_gemm and
+ * quarot_fp8_gated_gemm. */
 int quarot_version(void);
 
 /* Synchronizes `stream`, then returns and clears the device error word of the

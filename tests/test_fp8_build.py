@@ -26,6 +26,15 @@ def test_no_bulk_load_writes_another_cta():
     assert found == []
 
 
+def test_the_version_tells_of_the_8_bit_layer():
+    __graft_entry__.build()
+    assert q.quarot_version() >> 16 == 1 and q.quarot_version() & 0xFFFF >= 2
+    with open(os.path.join(os.path.dirname(CSRC), os.pardir, "include", "quarot.h")) as f:
+        told = " ".join(f.read().split("1.2 adds")[1].split("*/")[0].replace("*", " ").split())
+    for name in ("quant_fp8", "quant_fp8_block", "add_rmsnorm_quant_fp8", "fp8_gemm", "fp8_gated_gemm"):
+        assert f"quarot_{name}" in told
+
+
 # ---------------------------------------------------------------- without the compiled form
 def _load_again(monkeypatch, path):
     monkeypatch.setattr(B, "calls_path", lambda: str(path))
