@@ -834,6 +834,8 @@ class QuarotFp8GatedMLP:
     def __call__(self, x, residual=None, stream=None):
         if x.shape[-1] != self.features:
             raise QuarotError(1, f"x has {x.shape[-1]} features, the block {self.features}")
+        if residual is not None and residual.shape != x.shape:
+            raise QuarotError(1, f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
         if stream is not None:
             with _on(stream, x):
                 return self(x, residual)
