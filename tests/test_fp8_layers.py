@@ -17,3 +17,18 @@ def test_mlp_refuses_a_residual_of_another_shape(shape):
     x = torch.zeros((2, 3, 256), dtype=torch.float16)
     with pytest.raises(q.QuarotError, match="residual has shape"):
         _mlp(256)(x, torch.zeros(shape, dtype=torch.float16))
+
+
+def _linear(N, K):
+    lin = object.__new__(q.QuarotFp8Linear)
+    lin.out_features, lin.in_features, lin.w_q, lin.w_scale = N, K, None, None
+    return lin
+
+
+@pytest.mark.parametrize("y", [torch.zeros((300, 18)), torch.zeros(5400), torch.zeros((9, 600)), torch.zeros(()),
+                               torch.zeros((300, 18)).t(), torch.zeros((18, 600))[:, ::2]])
+def test_linear_refuses_an_output_of_other_columns(y):
+    """[N, M] has as many elements as [M, N], and is not the output."""
+    x = torch.zeros((2, 9, 256), dtype=torch.float16)
+    with pytest.raises(q.QuarotError, match="y must be contiguous with 300 columns"):
+        _linear(300, 256)(x, y=y.half())

@@ -801,6 +801,8 @@ class QuarotFp8Linear:
     def __call__(self, x, y=None, stream=None):
         if x.shape[-1] != self.in_features:
             raise QuarotError(1, f"x has {x.shape[-1]} features, the layer {self.in_features}")
+        if y is not None and (y.shape[-1:] != (self.out_features,) or not y.is_contiguous()):
+            raise QuarotError(1, f"y must be contiguous with {self.out_features} columns, it is {tuple(y.shape)}")
         if stream is not None:
             with _on(stream, x):
                 return self(x, y)
