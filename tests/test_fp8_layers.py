@@ -25,10 +25,14 @@ def _linear(N, K):
     return lin
 
 
-@pytest.mark.parametrize("y", [torch.zeros((300, 18)), torch.zeros(5400), torch.zeros((9, 600)), torch.zeros(()),
-                               torch.zeros((300, 18)).t(), torch.zeros((18, 600))[:, ::2]])
+H = torch.float16
+
+
+@pytest.mark.parametrize("y", [torch.zeros((300, 18), dtype=H), torch.zeros(5400, dtype=H), torch.zeros((9, 600), dtype=H),
+                               torch.zeros((), dtype=H), torch.zeros((300, 18), dtype=H).t(),
+                               torch.zeros((18, 600), dtype=H)[:, ::2]])
 def test_linear_refuses_an_output_of_other_columns(y):
     """[N, M] has as many elements as [M, N], and is not the output."""
-    x = torch.zeros((2, 9, 256), dtype=torch.float16)
+    x = torch.zeros((2, 9, 256), dtype=H)
     with pytest.raises(q.QuarotError, match="y must be contiguous with 300 columns"):
-        _linear(300, 256)(x, y=y.half())
+        _linear(300, 256)(x, y=y)
