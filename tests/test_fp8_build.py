@@ -26,6 +26,18 @@ def test_no_bulk_load_writes_another_cta():
     assert found == []
 
 
+def test_accumulators_are_handed_over_behind_a_fence():
+    """A read of tensor memory comes before another thread's next MMA into it only across a fence on both sides of the
+    barrier: every arrival on acc_empty has one before it, and the MMA loops one after their wait."""
+    with open(os.path.join(CSRC, "fp8_gemm.cu")) as f:
+        lines = [ln.strip() for ln in f]
+    arrivals = [i for i, ln in enumerate(lines) if ln.startswith("mbar_arrive_if(acc_empty")]
+    waits = [i for i, ln in enumerate(lines) if "wait_one(acc_empty" in ln]
+    assert len(arrivals) == len(waits) == 2
+    assert all(lines[i - 1] == "fence_before_sync();" for i in arrivals)
+    assert all("fence_after_sync();" in lines[i + 1:i + 3] for i in waits)
+
+
 def test_the_version_tells_of_the_8_bit_layer():
     __graft_entry__.build()
     assert q.quarot_version() >> 16 == 1 and q.quarot_version() & 0xFFFF >= 2

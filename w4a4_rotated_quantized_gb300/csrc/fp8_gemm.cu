@@ -512,6 +512,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           if (c < 128 / CW - 1) {
             tmem_ld(t + col(CW * (c + 1)), v[(c + 1) & 1]);
           } else {  // the last read is done: the buffer is free
+            fence_before_sync();
             mbar_arrive_if(acc_empty + 8 * b, lane == 0);
             if (++it < last) next_scales();
           }
@@ -902,6 +903,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           tmem_ld(tm_row + uint32_t((b * NW + p) * TN + c * CW), v);
           wait_ld();
           if (p == NW - 1 && c == TN / CW - 1) {
+            fence_before_sync();
             mbar_arrive_if(acc_empty + 8 * b, lane == 0);
           }
 #pragma unroll
