@@ -1,5 +1,6 @@
 """A failed call's error is its own: it is reported once, and the next call starts from a clean state."""
 import ctypes
+import time
 
 import pytest
 import torch
@@ -45,4 +46,17 @@ def test_the_call_after_a_failed_one(q, op):  # noqa: F811
     failed_wait(q)
     for w, v in zip(want, call()):
         assert torch.equal(w.view(torch.uint8), v.view(torch.uint8))
+    q.quarot_check_error()
+
+
+def test_both_bounded_waits_end_after_about_a_second(q):  # noqa: F811
+    """The self-test runs the library's wait and the 8-bit products' own, one after the other: a second each."""
+    q.quarot_check_error()
+    t0 = time.perf_counter()
+    q.quarot_selftest_wait()
+    with pytest.raises(q.QuarotError) as e:
+        q.quarot_check_error()
+    dt = time.perf_counter() - t0
+    assert e.value.status == q.QUAROT_ERR_TIMEOUT
+    assert 1.7 <= dt <= 3.5, dt
     q.quarot_check_error()

@@ -199,7 +199,7 @@ def quarot_check_error(stream=None, device=None) -> None:
 
 
 def quarot_selftest_wait(stream=None, device=None) -> None:
-    """Launches the bounded-wait self-test (one device thread, about one second);
+    """Launches the bounded-wait self-test (one device thread for each of the two kinds of wait, about a second each);
     the next quarot_check_error() raises QuarotError with QUAROT_ERR_TIMEOUT."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _check(load().quarot_selftest_wait(_stream(stream, dev)), "quarot_selftest_wait")

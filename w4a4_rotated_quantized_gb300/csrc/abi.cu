@@ -38,8 +38,9 @@ unsigned long long current_context_id() {
 }
 
 // One thread waits on a shared-memory barrier that nothing completes: the
-// bounded wait every kernel uses gives up after kWaitLimitNs, records
-// QUAROT_ERR_TIMEOUT and returns, and the kernel ends normally.
+// bounded wait every kernel uses (fp8_gemm.cu's have one of their own, tested
+// beside it) gives up after kWaitLimitNs, records QUAROT_ERR_TIMEOUT and
+// returns, and the kernel ends normally.
 __global__ void selftest_wait_kernel() {
   __shared__ __align__(8) uint64_t bar;
   mbar_init(&bar, 1);
@@ -78,5 +79,6 @@ extern "C" int quarot_check_error(void* stream) {
 
 extern "C" int quarot_selftest_wait(void* stream) {
   quarot::selftest_wait_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>();
-  return cudaGetLastError() == cudaSuccess ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  if (cudaGetLastError() != cudaSuccess) return QUAROT_ERR_LAUNCH;
+  return quarot::launch_fp8_selftest_wait(static_cast<cudaStream_t>(stream)) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }

@@ -26,6 +26,8 @@ extern __device__ unsigned int g_error_word;
 
 // Reads and clears the error word of fp8_gemm.cu; false on a CUDA error.
 bool take_fp8_error_word(unsigned int* word);
+// The self-test of fp8_gemm.cu's bounded wait; false on a CUDA error.
+bool launch_fp8_selftest_wait(cudaStream_t stream);
 
 // ~1 s: far above any legitimate wait, short enough to keep a shared GPU
 // usable if a barrier is never satisfied.

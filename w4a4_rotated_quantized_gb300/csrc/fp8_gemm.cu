@@ -159,12 +159,12 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded waits: a try_wait sleeps for up to about 1.3 us, and kTries of them
-// are a little over the wait limit.  They are on every k-block's path, so they
+// Bounded waits: a try_wait that finds nothing sleeps for 3.8 us, and kTries of
+// them are the wait limit, about a second.  They are on every k-block's path, so they
 // are a handful of instructions: the caller records an expired one where its
 // loop ends.  wait_one is for one thread, wait_warp for a converged warp, whose
 // loop the vote keeps uniform.
-constexpr int kTries = 1 << 20;
+constexpr int kTries = 1 << 18;
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (int n = 0; n < kTries; ++n)
@@ -985,6 +985,14 @@ narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
 }  // namespace narrow
 
+// One thread's wait on a barrier that nothing completes.
+__global__ void selftest_wait_kernel() {
+  __shared__ __align__(8) uint64_t bar;
+  mbar_init(smem_u32(&bar), 1);
+  fence_barrier_init();
+  if (!wait_one(smem_u32(&bar), 0)) record_error(QUAROT_ERR_TIMEOUT);
+}
+
 // ------------------------------------------------------------------ host
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 static std::once_flag g_encode_once;
@@ -1128,6 +1136,11 @@ static int run(const Args& p) {
 }  // namespace quarot
 
 using namespace quarot;
+
+bool quarot::launch_fp8_selftest_wait(cudaStream_t stream) {
+  fp8::gemm::selftest_wait_kernel<<<1, 1, 0, stream>>>();
+  return cudaGetLastError() == cudaSuccess;
+}
 
 bool quarot::take_fp8_error_word(unsigned int* word) {
   const unsigned int zero = 0;
