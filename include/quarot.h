@@ -474,6 +474,7 @@ int quarot_add_rmsnorm_quant_fp8(const void* x, int64_t ld_x, const void* residu
  *                         sum_{k in block b} a[i, k] w[j, k])
  * Products of codes accumulate in fp32 on the tensor cores within a block of
  * 128, blocks are scaled and summed in fp32, one rounding to dtype at the end.
+ * a_scale * w_scale is formed first and has to stay inside the fp32 range.
  *   a_q, a_scale  token codes [M, K] and scales; w_q, w_scale weight codes
  *                 [N, K] and scales
  *   y             [M, N] of dtype
@@ -485,7 +486,7 @@ int quarot_fp8_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q
 /*
  * quarot_fp8_gated_gemm -- the gated half of a feed-forward block in one
  * kernel: with g = A Wg^T and u = A Wu^T as in quarot_fp8_gemm, kept in fp32,
- *   z = g / (1 + exp(-g)) * u,
+ *   z = g / (1 + exp(-g)) * u      (g / (1 + exp(-g)) is 0 below g = -87.4),
  * quantized to q_out uint8 [M, I] and scale_out fp32 [ceil(I / 128), M] by the
  * block quantizer: the operand of the down projection's quarot_fp8_gemm.
  *   wg_q, wu_q    weight codes [I, K]; wg_scale, wu_scale their scales

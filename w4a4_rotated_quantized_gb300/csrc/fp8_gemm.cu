@@ -261,10 +261,10 @@ __device__ __forceinline__ float2 silu_mul(float2 g, float2 u) {
 // below, and no faster on the gated one.  It needs loads into another CTA's shared
 // memory, which are left to programs on a single GPU.)
 //
-// 2048 x 4096 x 12288: 78.7 us, 2620 TFLOP/s, 68 % of twice the bf16 rate, with 1.68
-// rounds of tiles; 8192 x 12288 x 4096: 302 us, 71 %; gated 4096 x 12288 x 4096: 340
-// us, 63 %, with silu and the quantizer between tiles.  Hot, at the power limit:
-// 87, 316, 330 us.
+// 2048 x 4096 x 12288: 86 us a call among others, at the power limit, 62 % of twice
+// the bf16 rate, with 1.68 rounds of tiles; 8192 x 12288 x 4096: 336 us, 63 %; gated
+// 4096 x 12288 x 4096: 338 us, 63 %, with silu and the quantizer between tiles.  On a
+// cool GPU 78.8, 302 and 306 to 320 us.
 //
 // SPLIT: fewer tiles than SMs.  A cluster takes one tile, each CTA a share of
 // the depth; the sums are joined through distributed shared memory in rank

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256, 4) quant_block_kernel(const T* __restrict
 // + 2 B read, 2 + 1 B written for each element.
 //
 // A thread has NU chunks in flight.  8192 x 12288 fp16: 103.5 us, 6.8 TB/s, as
-// fast as a copy; 8192 x 4096: 36.9 us, 6.4 TB/s; 509 x 12288: 9.7 us, one
+// fast as a copy; 8192 x 4096: 36.9 us, 6.4 TB/s; 509 x 12288: 9.6 us, one
 // wave of CTAs that waits for its loads six chunks a thread; 1 x 4096: 2.1 us,
 // the latency of one row.
 template <typename T, bool RES, bool WGT, int NU>
@@ -256,7 +256,7 @@ static int launch_norm(const void* x, int64_t ld_x, const void* res, int64_t ld_
   // times (8192 x 4096: 36.9 us with 128 threads, 41.6 with 256; 8192 x 1024: 12.1
   // with 64, 14.5 with 128).  Long rows: 256 threads with three chunks in flight, at
   // any number of rows (8192 x 12288: 103.5 us, with two 109.2, with two and 128
-  // threads 105.9; 509 x 12288: 9.7, 9.8, 14.4).
+  // threads 105.9; 509 x 12288: 9.6, 9.8, 14.4).
   const bool is_long = chunks > 1024;
   const int64_t most = is_long || M < 1024 ? 256 : chunks > 256 ? 128 : 64;
   const unsigned threads = unsigned(chunks < most ? (chunks + 31) / 32 * 32 : most);
