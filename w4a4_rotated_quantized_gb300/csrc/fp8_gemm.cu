@@ -257,9 +257,10 @@ __device__ __forceinline__ float2 silu_mul(float2 g, float2 u) {
 //
 // Every CTA loads its own weight rows, 48 KB a stage from L2, which holds the
 // tensor cores up a little and costs power.  (A cluster of two that loads each
-// row once for both was 2 to 6 % faster on the plain products, 77.1 and 295 us
-// below, and no faster on the gated one.  It needs loads into another CTA's shared
-// memory, which are left to programs on a single GPU.)
+// row once for both was 2 to 5 % faster on the plain products below, 77.1 and 295
+// us on a cool GPU, and no faster on the gated one.  It needs loads that write
+// another CTA's shared memory, which a library that replicas on several GPUs load
+// does without.)
 //
 // 2048 x 4096 x 12288: 86 us a call among others, at the power limit, 62 % of twice
 // the bf16 rate, with 1.68 rounds of tiles; 8192 x 12288 x 4096: 336 us, 63 %; gated
