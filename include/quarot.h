@@ -49,7 +49,7 @@ enum {
   QUAROT_ERR_CUDA = 6         /* another CUDA runtime/driver error            */
 };
 
-/* 16-bit element types of the 8-bit entry points (their `dtype` argument). */
+/* 16-bit element types of the 8-bit and the paged entry points (their `dtype` argument). */
 enum { QUAROT_FP16 = 0, QUAROT_BF16 = 1 };
 
 /* Human-readable text for a status code (static storage, never NULL). */
@@ -61,12 +61,15 @@ const char* quarot_status_string(int status);
  * quarot_int4_rowsum and quarot_w4a4_gemm_rowsums.  1.2 adds, with every 1.1
  * entry point unchanged, the 8-bit layer: quarot_quant_fp8,
  * quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8, quarot_fp8_gemm and
- * quarot_fp8_gated_gemm. */
+ * quarot_fp8_gated_gemm.  1.3 adds, with every 1.2 entry point unchanged,
+ * rotary positions and the paged cache: quarot_rope, quarot_paged_append,
+ * quarot_paged_read, quarot_paged_workspace_bytes and quarot_paged_attn. */
 int quarot_version(void);
 
 /* Synchronizes `stream`, then returns and clears the device error word of the
- * current device (QUAROT_OK if no kernel recorded an error), or
- * QUAROT_ERR_CUDA if the synchronization itself failed. */
+ * current device (QUAROT_OK if no kernel recorded an error;
+ * QUAROT_ERR_INVALID_ARG where a paged call met a page table that lacks a
+ * page), or QUAROT_ERR_CUDA if the synchronization itself failed. */
 int quarot_check_error(void* stream);
 
 /* Self-test of the bounded waits the kernels rely on, the 8-bit products' and
@@ -495,6 +498,112 @@ int quarot_fp8_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q
 int quarot_fp8_gated_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* wg_q, const float* wg_scale,
                           const uint8_t* wu_q, const float* wu_scale, int64_t M, int64_t I, int64_t K, uint8_t* q_out,
                           float* scale_out, void* stream);
+
+/*
+ * Rotary positions and the paged INT4 cache.  [S] Stage 1d rotates keys and
+ * queries head-wise after the position rotation, Stage 2c caches them; the
+ * pages fix neither the position rotation nor where a cache lies.
+ *
+ * Tokens: [N, H, d] tensors of `dtype` (QUAROT_FP16 or QUAROT_BF16), heads one
+ * after the other, tokens `ld` elements apart (a multiple of 8, at least H d;
+ * a slice of a joint projection's output will do), 16-byte aligned.
+ *
+ * Position rotation: the first `rot` elements of a head (a multiple of 16, 0
+ * for none) are rot / 2 pairs, (i, i + rot / 2) or, interleaved, (2i, 2i + 1).
+ * At position p pair i becomes
+ *   (a cos - b sin, b cos + a sin) * scale,   angle p * inv_freq[i],
+ * in fp32 with the angle's whole turns taken off exactly (inv_freq is fp64,
+ * rot / 2 of them, 8-byte aligned); the other elements stay.  Scaled
+ * frequencies for long contexts are just other inv_freq.
+ *
+ * Pages: codes k_q, v_q uint8 [n_pages, Hkv, page_size, d / 2] (16-byte
+ * aligned), scales k_s, v_s fp16 [n_pages, Hkv, page_size], the codes and
+ * scales of quarot_kv_write.  page_size is a multiple of 16, at most 65536.
+ * Token p of sequence b is slot p % page_size of page
+ * page_table[b * max_pages + p / page_size] (int32).
+ *
+ * Batch: lengths int32 [B], the tokens of each sequence, new ones included;
+ * cu_q int32 [B + 1], from 0 up: sequence b's new tokens are tokens
+ * cu_q[b] .. cu_q[b + 1] - 1 of the N, its last ones.  Without cu_q (NULL)
+ * every sequence has one, N == B.  All of it is read on the device, so a
+ * captured call follows what the arrays hold when it is replayed.
+ *   - Tokens from cu_q[B] on belong to no sequence: what a call would write
+ *     for them stays as it was.
+ *   - New tokens of a sequence that is shorter than they are (length 0: an
+ *     empty slot of the batch) are stored nowhere, and give zeros.
+ *   - A page that the table does not have, or outside 0 .. n_pages - 1, is an
+ *     error that quarot_check_error() reports (QUAROT_ERR_INVALID_ARG): its
+ *     tokens are neither written nor attended, reading them gives zeros.
+ * Two tokens with one slot (a table with the same page twice) leave either's
+ * value.  d is 64 or 128, N and B at most 2^24 (QUAROT_ERR_UNSUPPORTED
+ * otherwise).  N == 0 or B == 0 is a no-op.
+ */
+
+/*
+ * quarot_rope -- the position rotation of queries q [N, Hq, d] and keys
+ * k [N, Hk, d] (Hk = 0: none) by positions int32 [N] (any sign) into q_out and
+ * k_out, which may be q and k themselves.  d is a multiple of 16 up to 1024.
+ */
+int quarot_rope(const void* q, int64_t Hq, int64_t ld_q, void* q_out, int64_t ld_qo, const void* k, int64_t Hk,
+                int64_t ld_k, void* k_out, int64_t ld_ko, int dtype, int64_t N, int64_t d, const int32_t* positions,
+                const double* inv_freq, int64_t rot, int interleaved, float scale, void* stream);
+
+/*
+ * quarot_paged_append -- "Append" into pages: new keys and values k, v
+ * [N, Hkv, d]; each key is turned by its position (rot = 0: not), then keys
+ * and values are rotated and quantized as by quarot_kv_write, all in fp32 with
+ * no rounding between, and stored.  Queries q [N, Hq, d] (Hq = 0 and NULL:
+ * none) are turned into q_out, which may be q.
+ */
+int quarot_paged_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* q, int64_t Hq, int64_t ld_q,
+                        void* q_out, int64_t ld_qo, int dtype, int64_t N, int64_t Hkv, int64_t d, const double* inv_freq,
+                        int64_t rot, int interleaved, float scale, uint8_t* k_q, void* k_s, uint8_t* v_q, void* v_s,
+                        int64_t n_pages, int64_t page_size, const int32_t* page_table, int64_t B, int64_t max_pages,
+                        const int32_t* lengths, const int32_t* cu_q, void* stream);
+
+/*
+ * quarot_paged_read -- the values code * scale of the batch's new tokens (all
+ * tokens of its sequences, with cu_q the running sums of lengths) into k_out,
+ * v_out [N, Hkv, d] of dtype, dense; unrotate = 1: rotated back by H_d /
+ * sqrt(d).
+ */
+int quarot_paged_read(const uint8_t* k_q, const void* k_s, const uint8_t* v_q, const void* v_s, int64_t n_pages,
+                      int64_t page_size, int64_t Hkv, int64_t d, const int32_t* page_table, int64_t B, int64_t max_pages,
+                      const int32_t* lengths, const int32_t* cu_q, int64_t N, int unrotate, void* k_out, void* v_out,
+                      int dtype, void* stream);
+
+/*
+ * quarot_paged_workspace_bytes -- bytes of scratch that quarot_paged_attn
+ * needs for these sizes on the current device (0 on invalid ones).
+ */
+size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_q,
+                                    int64_t shared_len);
+
+/*
+ * quarot_paged_attn -- attention of the batch's new tokens over the pages.
+ * Query head h of token i at position p of sequence b, g = h / (Hq / Hkv):
+ *   q~ = q H_d / sqrt(d);  s_t = sm_scale * (q~ . (k_s[t] * kcode_t)), t <= p
+ *   o  = sum_t softmax(s)_t * v_s[t] * vcode_t;
+ *   unrotate_out: o <- o H_d / sqrt(d)
+ * (0: o stays in the rotated basis, as quarot_decode_attn's).
+ *
+ *   q, out      [N, Hq, d] of dtype, tokens ld_q and ld_out elements apart;
+ *               Hq a multiple of Hkv
+ *   max_q       the most new tokens that a sequence has (a hint that chooses
+ *               the kernel: any value > 0 gives right results)
+ *   shared_len  tokens 0 .. shared_len - 1 of all sequences are the same and
+ *               are read from sequence 0's pages, once for the whole batch;
+ *               0: nothing is shared
+ *   sm_scale    softmax scale; <= 0 selects 1/sqrt(d)
+ *   workspace   device scratch of ws_bytes >= quarot_paged_workspace_bytes(),
+ *               256-byte aligned, owned by the caller until the call is over;
+ *               needs no initialisation and is clobbered
+ */
+int quarot_paged_attn(const void* q, int64_t ld_q, int dtype, int64_t N, int64_t Hq, int64_t Hkv, int64_t d,
+                      const uint8_t* k_q, const void* k_s, const uint8_t* v_q, const void* v_s, int64_t n_pages,
+                      int64_t page_size, const int32_t* page_table, int64_t B, int64_t max_pages, const int32_t* lengths,
+                      const int32_t* cu_q, int64_t max_q, int64_t shared_len, float sm_scale, int unrotate_out, void* out,
+                      int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* quarot_legacy_imma_probe -- a measurement utility: one launch that issues
  * nothing but one legacy warp-level tensor-core instruction, mma.sync s8

@@ -12,19 +12,24 @@ Functions (same names as the C entry points):
     and the tensor-core operand form of the layer: quarot_rotate_quant_a8,
     quarot_w4a4_gemm_a8; the 8-bit layer: quarot_quant_fp8,
     quarot_quant_fp8_block, quarot_add_rmsnorm_quant_fp8, quarot_fp8_gemm,
-    quarot_fp8_gated_gemm
+    quarot_fp8_gated_gemm; rotary positions and the paged cache: quarot_rope,
+    quarot_paged_append, quarot_paged_read, quarot_paged_attn,
+    quarot_paged_workspace_bytes
 
 ``QuarotLinear`` composes them into the W4A4 linear layer: weight rows
 rotated and quantized once, then per call the tokens rotated and quantized
 and the INT4 GEMM with its dequant epilogue.  ``QuarotKVCache`` holds the
 rotated INT4 KV cache with its append, decode and prompt-attention calls.
 ``QuarotFp8Linear`` and ``QuarotFp8GatedMLP`` are the layers kept at 8 bits:
-e4m3 codes with a scale for each block of 128.
+e4m3 codes with a scale for each block of 128.  ``QuarotPagedKVCache`` holds
+the same rotated INT4 cache in pages, ``QuarotRope`` the frequencies of the
+position rotation.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 import warnings
 
@@ -80,6 +85,17 @@ _SIGS = {
                                             _P, _P, _P, _P]),
     "quarot_decode_attn_asym": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                                ctypes.c_float, ctypes.c_int, _P, _P, ctypes.c_size_t, _P]),
+    "quarot_rope": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, ctypes.c_int, _I64, _I64, _P, _P, _I64,
+                                   ctypes.c_int, ctypes.c_float, _P]),
+    "quarot_paged_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, ctypes.c_int, _I64, _I64, _I64, _P,
+                                           _I64, ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _I64, _I64, _P, _I64, _I64,
+                                           _P, _P, _P]),
+    "quarot_paged_read": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, ctypes.c_int,
+                                         _P, _P, ctypes.c_int, _P]),
+    "quarot_paged_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _I64, _I64]),
+    "quarot_paged_attn": (ctypes.c_int, [_P, _I64, ctypes.c_int, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I64,
+                                         _I64, _P, _P, _I64, _I64, ctypes.c_float, ctypes.c_int, _P, _I64, _P,
+                                         ctypes.c_size_t, _P]),
 }
 DECODE_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024  # QUAROT_DECODE_STATIC_SCRATCH_BYTES
 EXPORTED = tuple(_SIGS)
@@ -847,6 +863,277 @@ class QuarotFp8GatedMLP:
         z_q, z_scale = quarot_fp8_gated_gemm(a_q, a_scale, self.gate_q, self.gate_scale, self.up_q, self.up_scale)
         y = self.down.from_codes(z_q, z_scale, out_dtype=x.dtype)
         return y.view(x.shape), h.view(x.shape)
+
+
+# ---------------------------------------------------------------- rotary positions and the paged cache
+def _heads(t, name, dev=None, dtype=None) -> int:
+    """An fp16 or bf16 [N, H, d] CUDA tensor, heads one after the other, any token stride; returns that stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES:
+        raise QuarotError(1, f"{name} must be an fp16 or bf16 CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise QuarotError(1, f"{name} must be {dtype}, got {t.dtype}")
+    if dev is not None and t.get_device() != dev:
+        raise QuarotError(1, f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.dim() != 3 or 0 in t.shape[1:]:
+        raise QuarotError(1, f"{name} must be [tokens, heads, d], it is {tuple(t.shape)}")
+    N, H, d = t.shape
+    sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (N > 1 and sn < H * d):
+        raise QuarotError(1, f"{name} must have its heads one after the other")
+    return sn if N > 1 else H * d
+
+
+def _heads_out(t, shape, name, dev, dtype):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev)), shape[1] * shape[2]
+    ld = _heads(t, name, dev, dtype)
+    if t.shape != shape:
+        raise QuarotError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t, ld
+
+
+def _rotation(inv_freq, scale, dev):
+    """(address of the frequencies, rotated elements, scale)."""
+    if inv_freq is None:
+        return None, 0, 1.0
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise QuarotError(1, "inv_freq must be a 1-D tensor")
+    return _dense(inv_freq, torch.float64, inv_freq.shape, "inv_freq", dev), 2 * inv_freq.shape[0], float(scale)
+
+
+def _pages(k_q, k_s, v_q, v_s):
+    """(the four addresses, pages, page size, heads, d, device) of a paged cache."""
+    if not isinstance(k_q, torch.Tensor) or not k_q.is_cuda or k_q.dim() != 4:
+        raise QuarotError(1, "k_q must be a [pages, heads, page size, d / 2] CUDA tensor")
+    dev, codes = k_q.get_device(), k_q.shape
+    P, H, ps, half = codes
+    return (_dense(k_q, torch.uint8, codes, "k_q", dev), _dense(k_s, torch.float16, (P, H, ps), "k_s", dev),
+            _dense(v_q, torch.uint8, codes, "v_q", dev), _dense(v_s, torch.float16, (P, H, ps), "v_s", dev)), P, ps, H, 2 * half, dev
+
+
+def _batch(page_table, lengths, cu_q, dev):
+    """(addresses of the table, lengths and cu_q, sequences, pages of a sequence)."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise QuarotError(1, "page_table must be [sequences, pages]")
+    B, P = page_table.shape
+    return (_dense(page_table, torch.int32, (B, P), "page_table", dev), _dense(lengths, torch.int32, (B,), "lengths", dev),
+            None if cu_q is None else _dense(cu_q, torch.int32, (B + 1,), "cu_q", dev), B, P)
+
+
+def quarot_rope(q, k, positions, inv_freq, interleaved: bool = False, scale: float = 1.0, q_out=None, k_out=None,
+                stream=None):
+    """q, k (or None): fp16 or bf16 [N, H, d], heads one after the other, any
+    token stride -> (q, k) turned by positions (int32 [N]) and frequencies
+    (fp64 [rot / 2]; see QuarotRope): pairs (i, i + rot / 2), or neighbours
+    where interleaved; the outputs may be the inputs."""
+    if stream is not None:
+        with _on(stream, q):
+            return quarot_rope(q, k, positions, inv_freq, interleaved, scale, q_out, k_out)
+    ld = _heads(q, "q")
+    (N, Hq, d), dt, dev = q.shape, q.dtype, q.get_device()
+    q_out, ld_o = _heads_out(q_out, q.shape, "q_out", dev, dt)
+    Hk = ld_k = ld_ko = 0
+    kp = ko = None
+    if k is not None:
+        ld_k = _heads(k, "k", dev, dt)
+        if k.shape[0] != N or k.shape[2] != d:
+            raise QuarotError(1, f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        Hk, kp = k.shape[1], k.data_ptr()
+        k_out, ld_ko = _heads_out(k_out, k.shape, "k_out", dev, dt)
+        ko = k_out.data_ptr()
+    elif k_out is not None:
+        raise QuarotError(1, "k_out without k")
+    pos = _dense(positions, torch.int32, (N,), "positions", dev)
+    f, rot, sc = _rotation(inv_freq, scale, dev)
+    _fp8_call("quarot_rope", dev, q.data_ptr(), Hq, ld, q_out.data_ptr(), ld_o, kp, Hk, ld_k, ko, ld_ko, _DTYPES[dt], N, d, pos,
+              f, rot, int(bool(interleaved)), sc)
+    return q_out, k_out
+
+
+def quarot_paged_append(k, v, k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, q=None, inv_freq=None,
+                        interleaved: bool = False, scale: float = 1.0, q_out=None, stream=None):
+    """New keys and values k, v [N, Hkv, d] (fp16 or bf16, heads one after the
+    other, any token stride) into pages k_q, v_q uint8 [pages, Hkv, page size,
+    d / 2] and k_s, v_s fp16 [pages, Hkv, page size]: keys turned by their
+    positions (inv_freq fp64 [rot / 2], or None), both rotated and quantized.
+    page_table int32 [B, pages of a sequence]; lengths int32 [B], new tokens
+    included; cu_q int32 [B + 1], whose tokens are whose (None: one each).
+    Returns the queries q [N, Hq, d] turned likewise (q_out, or a new tensor),
+    or None without q."""
+    if stream is not None:
+        with _on(stream, k):
+            return quarot_paged_append(k, v, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, q, inv_freq, interleaved, scale,
+                                       q_out)
+    cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
+    ld_k = _heads(k, "k", dev)
+    dt, N = k.dtype, k.shape[0]
+    ld_v = _heads(v, "v", dev, dt)
+    if k.shape != (N, H, d) or v.shape != (N, H, d):
+        raise QuarotError(1, f"k and v are {tuple(k.shape)} and {tuple(v.shape)}, the cache has {H} heads of {d}")
+    tab, lens, cu, B, mp = _batch(page_table, lengths, cu_q, dev)
+    f, rot, sc = _rotation(inv_freq, scale, dev)
+    Hq = ld_q = ld_o = 0
+    qp = op = None
+    if q is not None:
+        ld_q = _heads(q, "q", dev, dt)
+        if q.shape[0] != N or q.shape[2] != d:
+            raise QuarotError(1, f"q has shape {tuple(q.shape)}, k {tuple(k.shape)}")
+        Hq, qp = q.shape[1], q.data_ptr()
+        q_out, ld_o = _heads_out(q_out, q.shape, "q_out", dev, dt)
+        op = q_out.data_ptr()
+    elif q_out is not None:
+        raise QuarotError(1, "q_out without q")
+    _fp8_call("quarot_paged_append", dev, k.data_ptr(), ld_k, v.data_ptr(), ld_v, qp, Hq, ld_q, op, ld_o, _DTYPES[dt], N, H, d, f,
+              rot, int(bool(interleaved)), sc, *cache, P, ps, tab, B, mp, lens, cu)
+    return q_out
+
+
+def quarot_paged_read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, n=None, unrotate: bool = False,
+                      out_dtype=torch.float16, k_out=None, v_out=None, stream=None):
+    """The values of the batch's new tokens in the pages: (k, v) [n, Hkv, d] of
+    out_dtype, in the rotated basis or (unrotate) the original one.  n: the
+    number of tokens, cu_q[-1] (None without cu_q: one a sequence)."""
+    if stream is not None:
+        with _on(stream, k_q):
+            return quarot_paged_read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, n, unrotate, out_dtype, k_out, v_out)
+    cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
+    tab, lens, cu, B, mp = _batch(page_table, lengths, cu_q, dev)
+    if n is None:
+        if cu_q is not None:
+            raise QuarotError(1, "n is needed with cu_q")
+        n = B
+    if out_dtype not in _DTYPES:
+        raise QuarotError(1, "out_dtype must be float16 or bfloat16")
+    shape = (int(n), H, d)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty(shape, dtype=out_dtype, device=k_q.device)
+        else:
+            _dense(t, out_dtype, shape, name, dev)
+        outs.append(t)
+    _fp8_call("quarot_paged_read", dev, *cache, P, ps, H, d, tab, B, mp, lens, cu, shape[0], int(bool(unrotate)),
+              outs[0].data_ptr(), outs[1].data_ptr(), _DTYPES[out_dtype])
+    return outs[0], outs[1]
+
+
+def quarot_paged_workspace_bytes(N: int, B: int, Hq: int, Hkv: int, d: int, max_q: int = 1, shared_len: int = 0) -> int:
+    return int(load().quarot_paged_workspace_bytes(N, B, Hq, Hkv, d, max_q, shared_len))
+
+
+def quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, max_q=None, shared_len: int = 0,
+                      sm_scale: float = 0.0, unrotate_out: bool = False, out=None, workspace=None, stream=None):
+    """Attention of the batch's new tokens q [N, Hq, d] (fp16 or bf16, heads
+    one after the other, any token stride) over the pages, each token over its
+    sequence up to itself -> out [N, Hq, d].  page_table, lengths, cu_q as in
+    quarot_paged_append; max_q: the most new tokens of a sequence, where known
+    (it chooses the kernel); the first shared_len tokens of all sequences are
+    the same: they are read from the first sequence's pages, once for all."""
+    if stream is not None:
+        with _on(stream, q):
+            return quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_q, shared_len, sm_scale,
+                                     unrotate_out, out, workspace)
+    cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
+    ld = _heads(q, "q", dev)
+    N, Hq, dq = q.shape
+    if dq != d or Hq % H:
+        raise QuarotError(1, f"q has {Hq} heads of {dq}, the cache {H} of {d}")
+    tab, lens, cu, B, mp = _batch(page_table, lengths, cu_q, dev)
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(N, 1)
+    out, ld_o = _heads_out(out, q.shape, "out", dev, q.dtype)
+    with torch.cuda.device(dev):
+        need = quarot_paged_workspace_bytes(N, B, Hq, H, d, max_q, shared_len)
+    if workspace is None:
+        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise QuarotError(1, f"workspace must be a contiguous tensor on cuda:{dev}")
+    _fp8_call("quarot_paged_attn", dev, q.data_ptr(), ld, _DTYPES[q.dtype], N, Hq, H, d, *cache, P, ps, tab, B, mp, lens, cu,
+              max_q, shared_len, float(sm_scale), int(bool(unrotate_out)), out.data_ptr(), ld_o, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size())
+    return out
+
+
+class QuarotRope:
+    """Frequencies of the position rotation of heads whose first ``rot``
+    elements are turned: pair i by base^(-2i / rot) a position.  For contexts
+    longer than a model was made for, by ``factor``:
+      "linear"  every frequency divided by the factor
+      "ntk"     base * factor^(rot / (rot - 2)) in the place of base
+      "yarn"    pairs that turn more than beta_fast times in original_len
+                positions stay, those below beta_slow times are divided, a
+                ramp over the pairs between; scale 0.1 ln(factor) + 1
+      "smooth"  the same idea over wavelengths: those below original_len /
+                high_freq stay, those above original_len / low_freq are
+                divided, the frequencies between are blended
+    ``inv_freq`` (fp64 on the GPU), ``interleaved`` and ``scale`` are what
+    quarot_rope and quarot_paged_append take; calling it is quarot_rope."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+                 factor: float = 1.0, original_len: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 low_freq: float = 1.0, high_freq: float = 4.0, device=None):
+        if rot <= 0 or rot % 16:
+            raise QuarotError(2, f"{rot} rotated elements: a multiple of 16 is needed")
+        if not base > 1.0 or not factor >= 1.0:
+            raise QuarotError(1, "base must be above 1 and factor at least 1")
+        if scaling not in (None, "linear", "ntk", "yarn", "smooth"):
+            raise QuarotError(1, f"unknown scaling {scaling!r}")
+        if scaling in ("yarn", "smooth") and not (original_len or 0) > 0:
+            raise QuarotError(1, f"{scaling} needs original_len")
+        if scaling == "ntk":
+            base = base * factor ** (rot / (rot - 2))
+        i = torch.arange(rot // 2, dtype=torch.float64)
+        f = float(base) ** (-2.0 * i / rot)
+        self.scale = 1.0
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            edge = lambda turns: rot * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+            lo, hi = max(math.floor(edge(beta_fast)), 0), min(math.ceil(edge(beta_slow)), rot - 1)
+            ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            f = f / factor * ramp + f * (1 - ramp)
+            self.scale = 0.1 * math.log(factor) + 1.0
+        elif scaling == "smooth":
+            turns = original_len * f / (2 * math.pi)
+            keep = ((turns - low_freq) / (high_freq - low_freq)).clamp(0, 1)
+            f = f * keep + f / factor * (1 - keep)
+        self.rot, self.interleaved = int(rot), bool(interleaved)
+        self.inv_freq = f.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+    def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        return quarot_rope(q, k, positions, self.inv_freq, self.interleaved, self.scale, q_out, k_out, stream)
+
+
+class QuarotPagedKVCache:
+    """The rotated INT4 cache in n_pages pages of page_size tokens, Hkv heads
+    of d.  Which pages are whose is the caller's: every call takes the batch
+    (page_table, lengths, cu_q; see quarot_paged_append).  ``append`` stores
+    new tokens, keys and queries turned by ``rope`` on the way; ``attend`` runs
+    their attention; ``read`` gives their values back."""
+
+    def __init__(self, n_pages: int, Hkv: int, page_size: int = 64, d: int = 128, rope: QuarotRope | None = None, device=None):
+        if page_size <= 0 or page_size % 16 or d not in (64, 128):
+            raise QuarotError(2, "page_size must be a multiple of 16, d 64 or 128")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        shape = (int(n_pages), int(Hkv), int(page_size))
+        codes = lambda: torch.zeros(shape + (int(d) // 2,), dtype=torch.uint8, device=device)  # noqa: E731
+        scales = lambda: torch.zeros(shape, dtype=torch.float16, device=device)  # noqa: E731
+        self.tensors = (codes(), scales(), codes(), scales())
+        self.rope = rope
+
+    def append(self, k, v, page_table, lengths, cu_q=None, q=None, q_out=None, stream=None):
+        """Returns the turned queries (None without q)."""
+        r = self.rope
+        turned = {} if r is None else {"inv_freq": r.inv_freq, "interleaved": r.interleaved, "scale": r.scale}
+        return quarot_paged_append(k, v, *self.tensors, page_table, lengths, cu_q, q=q, q_out=q_out, stream=stream, **turned)
+
+    def attend(self, q, page_table, lengths, cu_q=None, max_q=None, shared_len: int = 0, sm_scale: float = 0.0,
+               unrotate_out: bool = False, out=None, workspace=None, stream=None):
+        return quarot_paged_attn(q, *self.tensors, page_table, lengths, cu_q, max_q, shared_len, sm_scale, unrotate_out, out,
+                                 workspace, stream)
+
+    def read(self, page_table, lengths, cu_q=None, n=None, unrotate: bool = False, out_dtype=torch.float16, stream=None):
+        return quarot_paged_read(*self.tensors, page_table, lengths, cu_q, n, unrotate, out_dtype, stream=stream)
 
 
 class QuarotKVCache:

@@ -62,7 +62,7 @@ extern "C" const char* quarot_status_string(int status) {
   }
 }
 
-extern "C" int quarot_version(void) { return (1 << 16) | 2; }
+extern "C" int quarot_version(void) { return (1 << 16) | 3; }
 
 extern "C" int quarot_check_error(void* stream) {
   if (!quarot::cuda_ok(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)))) return QUAROT_ERR_CUDA;
@@ -74,6 +74,7 @@ extern "C" int quarot_check_error(void* stream) {
   if (!quarot::take_fp8_error_word(&fp8_word)) return QUAROT_ERR_CUDA;
   word |= fp8_word;
   if (word & (1u << QUAROT_ERR_TIMEOUT)) return QUAROT_ERR_TIMEOUT;
+  if (word & (1u << QUAROT_ERR_INVALID_ARG)) return QUAROT_ERR_INVALID_ARG;
   return word ? QUAROT_ERR_CUDA : QUAROT_OK;
 }
 
