@@ -138,7 +138,7 @@ inline int check_sizes(int dtype, int64_t N, int64_t Hkv, int64_t d, int64_t n_p
   if (N < 0 || B < 0 || Hkv <= 0 || d <= 0 || n_pages < 0 || ps <= 0 || max_pages < 0) return QUAROT_ERR_INVALID_ARG;
   if (cu == nullptr && N != B) return QUAROT_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return QUAROT_ERR_UNSUPPORTED;
-  if (ps % 16 != 0 || ps > 65536 || n_pages > 0x7fffffff || max_pages > 0x7fffffff / ps) return QUAROT_ERR_UNSUPPORTED;
+  if (ps % 16 != 0 || ps > 65536 || n_pages > 0x7fffffff || max_pages > 0x7fff0000 / ps) return QUAROT_ERR_UNSUPPORTED;
   if (N > kMaxTokens || B > kMaxTokens || Hkv > kMaxHeads) return QUAROT_ERR_UNSUPPORTED;
   return QUAROT_OK;
 }

@@ -4,89 +4,864 @@
 // g = h / (Hq / Hkv):
 //   q~ = q H_d / sqrt(d),  s_t = sm_scale * q~ . (k_s[t] kcode_t)  for t <= p
 //   out = sum_t softmax(s)_t v_s[t] vcode_t
+//
+// Rows (a token's heads of one group, R = Hq / Hkv a token) that attend to the
+// same keys are worked on together.  With a shared prefix there are two parts:
+// all rows of the batch against the shared tokens, once, and each sequence's
+// rows against its own tokens; without one there is the second alone.  A part
+// is a list of units, a unit being up to RP rows of one KV head and the tiles
+// of 128 tokens that they see.  The tiles of all units lie in one row, which
+// is cut into equal pieces, one a CTA, whatever the sequences' lengths: a CTA
+// works on the end of one unit, whole ones, and the start of another, and
+// leaves a partial softmax state (o, m, l) of each in the workspace, which the
+// last kernel joins.  The cut depends on the lengths and the number of CTAs
+// alone, so results are the same every time.
 #include "paged.cuh"
 
 namespace quarot {
 namespace paged {
 
-constexpr int SW = 4;  // warps
+// ------------------------------------------------------------------ tcgen05
+// Shared-memory descriptors (addresses and offsets in 16-byte units, version 1):
+// 128-byte swizzle, 8-row groups `sbo` bytes apart; no swizzle, with both offsets.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t sbo) {
+  return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(1) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46);
+}
+// Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 to fp32: M = 128, N = n;
+// a_mn, b_mn: the operand is stored with M (N) running fastest.
+__host__ __device__ constexpr uint32_t idesc8(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
+}
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One CTA per (token, query head); each warp takes every fourth cached token
-// with an online softmax of its own, lanes share a head's dims.
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 16 lanes x 8 N columns: lane l holds columns 8 i + 2 (l % 4) and + 1 of row
+// l / 4 in r[4 i], r[4 i + 1], of row l / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_st_rows4(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_rows2(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 8 offset codes u = v + 8 of a packed word as e4m3 bytes with that bit
+// pattern, whose value is u 2^-9: even dims in lo, odd ones in hi.
+__device__ __forceinline__ void bytes_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  lo = (w & 0x0F0F0F0Fu) ^ 0x08080808u;
+  hi = ((w >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_h2(uint32_t h) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_of_e4m3x2(uint32_t c) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(uint16_t(c)));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_of_f2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// (a - b) * 16 of fp16 pairs, exact where b is a rounded to fewer bits.
+__device__ __forceinline__ uint32_t rest16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(0x4C004C00u));
+  return d;
+}
+// An fp16 pair as three e4m3 pairs, a = c0 + c1 / 16 + c2 / 256: 4 bits of
+// fraction each hold all 11 of an fp16 (below 2^-6 fewer, never below 2^-18).
+__device__ __forceinline__ void pieces_of(uint32_t a, uint32_t* c) {
+  c[0] = e4m3x2_of_h2(a);
+  a = rest16(a, h2_of_e4m3x2(c[0]));
+  c[1] = e4m3x2_of_h2(a);
+  a = rest16(a, h2_of_e4m3x2(c[1]));
+  c[2] = e4m3x2_of_h2(a);
+}
+
+// ------------------------------------------------------------------ units
+constexpr int TILE = 128;  // tokens
+
+// One part of a call: the shared prefix (rows of all N tokens as one list,
+// tokens [0, shared)) or the sequences' own tokens [shared, length).
+struct Part {
+  Batch t;
+  int N, G, Hkv, shared, prefix;
+  int RP;  // rows of a unit
+};
+
+__device__ __forceinline__ int cu_at(const Part& p, int b) {
+  return p.t.cu == nullptr ? b : min(max(__ldcg(p.t.cu + b), 0), p.N);
+}
+// A sequence as a part sees it.
+struct Seq {
+  int tok0, rows;      // first token, rows (tokens * G)
+  int first, len;      // position of token tok0, tokens in the cache
+  int tile0;           // first tile
+};
+__device__ __forceinline__ Seq seq_of(const Part& p, int b, bool tell) {
+  Seq s;
+  if (p.prefix) return {0, p.N * p.G, 0, p.shared, 0};
+  s.tok0 = cu_at(p, b);
+  const int n = max(cu_at(p, b + 1) - s.tok0, 0);
+  const int cap = p.t.max_pages * p.t.ps;
+  const int len = max(__ldcg(p.t.lengths + b), 0);
+  if (len > cap && tell) record_error(QUAROT_ERR_INVALID_ARG);
+  s.rows = n * p.G;
+  s.first = len - n;
+  s.len = min(len, cap);
+  s.tile0 = p.shared / TILE;
+  return s;
+}
+// Tiles of row tile j.
+__device__ __forceinline__ int tiles_of(const Part& p, const Seq& s, int j) {
+  int end = s.len;
+  if (!p.prefix) {
+    const int last = min(p.RP * (j + 1), s.rows) - 1;
+    end = min(end, s.first + last / p.G + 1);
+  }
+  return end <= 0 ? 0 : max((end + TILE - 1) / TILE - s.tile0, 0);
+}
+// Tiles of one KV head of a sequence.
+__device__ __forceinline__ int64_t steps_of(const Part& p, const Seq& s) {
+  const int J = (s.rows + p.RP - 1) / p.RP;
+  if (p.prefix) return int64_t(J) * tiles_of(p, s, 0);
+  int64_t n = 0;
+  for (int j = 0; j < J; ++j) n += tiles_of(p, s, j);
+  return n;
+}
+// Number of a sequence's first unit: ceilings of what lies between two
+// multiples never pass the next number.
+__host__ __device__ inline int64_t unit_base(int64_t tok0, int64_t b, int64_t G, int64_t Hkv, int64_t RP) {
+  return Hkv * (tok0 * G / RP + b);
+}
+__host__ __device__ inline int64_t unit_count(int64_t N, int64_t B, int64_t G, int64_t Hkv, int64_t RP) {
+  return unit_base(N, B, G, Hkv, RP);
+}
+
+// Where a part's states lie in the workspace: unit u's first and last CTA, and
+// for CTA w its state of unit u in slot u + w (one more of either is one more
+// slot), o [slots, RP, d] and (m, l) [slots, RP, 2].
+struct Space {
+  int* span;  // [units, 2]
+  float* ml;
+  float* o;
+};
+constexpr size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+inline size_t space_bytes(int64_t units, int64_t ctas, int64_t RP, int64_t d) {
+  const size_t slots = size_t(units + ctas);
+  return round256(size_t(units) * 8) + round256(slots * RP * 8) + round256(slots * RP * d * 4);
+}
+inline Space space_at(unsigned char* p, int64_t units, int64_t ctas, int64_t RP) {
+  Space s;
+  s.span = reinterpret_cast<int*>(p);
+  p += round256(size_t(units) * 8);
+  s.ml = reinterpret_cast<float*>(p);
+  p += round256(size_t(units + ctas) * RP * 8);
+  s.o = reinterpret_cast<float*>(p);
+  return s;
+}
+
+// A CTA's place in the row of all tiles: found once by all its threads.
+struct Cursor {
+  int b, g, j, tile, tiles;  // unit (b, g, j), next of its tiles, all of them
+  Seq s;
+};
+// Sum over the block; all threads get it.
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t r = 0;
+  for (int w = 0; w < int(blockDim.x >> 5); ++w) r += sh[w];
+  return r;
+}
+// Sets the cursor to tile w * per of the row (per = the row's w-th part) and
+// returns how many tiles the CTA has.
+__device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
+  const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B;
+  int64_t mine = 0;
+  for (int b = threadIdx.x; b < nseq; b += n) mine += steps_of(p, seq_of(p, b, blockIdx.x == 0));
+  const int64_t total = block_sum(mine, sh) * p.Hkv;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t at = per * blockIdx.x;
+  if (at >= total) return 0;
+  // the sequence that holds tile `at`: sequences in blocks of n, then within one
+  __shared__ int found;
+  __shared__ int64_t before;
+  if (threadIdx.x == 0) found = -1;
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < nseq; b0 += n) {
+    const int b = b0 + threadIdx.x;
+    const int64_t v = b < nseq ? steps_of(p, seq_of(p, b, false)) * p.Hkv : 0;
+    int64_t x = v;  // inclusive sum over the block
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (int(threadIdx.x & 31) >= o) x += y;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 31) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < n / 32; ++w) {
+      if (w < int(threadIdx.x >> 5)) x += sh[w];
+      all += sh[w];
+    }
+    if (v > 0 && at >= sum + x - v && at < sum + x) {
+      found = b;
+      before = sum + x - v;
+    }
+    sum += all;
+    __syncthreads();
+    if (found >= 0) break;
+  }
+  c.b = found;
+  c.s = seq_of(p, c.b, false);
+  const int64_t head = steps_of(p, c.s);
+  int64_t rest = at - before;
+  c.g = int(rest / head);
+  rest -= c.g * head;
+  c.j = 0;
+  while (rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
+    rest -= c.tiles;
+    ++c.j;
+  }
+  c.tile = int(rest);
+  return min(per, total - at);
+}
+// The next unit that has tiles; without one (the batch changed under the call) c.tiles is 0.
+__device__ __forceinline__ void next_unit(const Part& p, Cursor& c) {
+  c.tile = 0;
+  for (;;) {
+    if (++c.j * p.RP >= c.s.rows) {
+      c.j = 0;
+      if (++c.g == p.Hkv) {
+        c.g = 0;
+        do {
+          if (++c.b >= (p.prefix ? 1 : p.t.B)) {
+            c.tiles = 0;
+            return;
+          }
+          c.s = seq_of(p, c.b, false);
+        } while (c.s.rows == 0);
+      }
+    }
+    c.tiles = tiles_of(p, c.s, c.j);
+    if (c.tiles > 0) return;
+  }
+}
+
+// A row: its token, its query head within the group, and how many tokens it sees.
+struct Row {
+  int tok, hh, end;
+};
+__device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
+  Row r = {-1, 0, 0};
+  if (rr >= s.rows) return r;
+  const int i = rr / p.G;
+  r.hh = rr - i * p.G;
+  r.tok = s.tok0 + i;
+  int pos = s.first + i;
+  if (p.prefix) {
+    const Place w = place_of(p.t, r.tok);
+    pos = w.b < 0 ? -1 : w.pos;
+  }
+  r.end = min(max(pos + 1, 0), s.len);
+  return r;
+}
+
+// ===================================================================== few
+// Up to 16 rows.  Everything that would be multiplied is small against the
+// cache's bytes, so the kernel is made to read them at the memory's rate:
+//   - a packed word becomes 8 operand bytes in 3 instructions (bytes_of), 8 bits
+//     being what the tensor cores take: queries and probabilities, which need
+//     more, are three e4m3 pieces each, in columns of their own;
+//   - S^T [tokens, 3 RP] = K Q^T with the tokens as the MMA's M: the keys go
+//     from registers to tensor memory (the A operand), never through shared
+//     memory; a thread then holds one token's scores, so the token's scales are
+//     its own registers;
+//   - O^T [dims, 3 RP] += V^T P^T: values lie in shared memory as they come,
+//     token after token (the A operand, M running fastest), and a thread writes
+//     its token's 3 RP probability bytes with one or a few 16-byte stores.
+// The offset of the codes (u = v + 8) is taken out of the results: 8 sum q~ of
+// each score, 8 sum p' of each output.
+//
+// Softmax: p' = 2^(s - m) v_s, with m raised only when some s + log2 v_s
+// exceeds it by 8, so p' <= 2^8 and the largest is at least 1 (fp16, then its
+// pieces, hold it to 2^-12).  Sums of 2^(s - m) and of p' stay in fp32.
+//
+// A CTA is four warps that do it all in turn; the overlap of loads, tensor
+// cores and arithmetic comes from several CTAs on an SM, and the next tile's
+// loads, which are in registers before this tile's scores are.
+namespace few {
+
+constexpr int NT = 128;
+
+template <int RP, int D>
+struct Cfg {
+  static constexpr int NC = RP == 4 ? 16 : RP == 8 ? 32 : 48;  // columns: piece * RP + row
+  static constexpr int KC = D / 4;                             // tensor-memory columns of a key
+  static constexpr uint32_t COLS = KC + 2 * NC <= 64 ? 64 : 128;
+  static constexpr int WPT = D / 32;                           // packed words a thread has of a token
+  static constexpr int OFF_V = 0;                              // [128 tokens][128 bytes], swizzled
+  static constexpr int OFF_Q = OFF_V + TILE * 128;             // [NC][128 bytes], swizzled
+  static constexpr int OFF_P = (OFF_Q + NC * 128 + 1023) / 1024 * 1024;  // [NC / 16][128 tokens][16 bytes]
+  static constexpr int OFF_ROW = OFF_P + NC * TILE;            // per row: factor, offset, end
+  static constexpr int OFF_M = OFF_ROW + RP * 12;              // reference m of each row
+  static constexpr int OFF_X = OFF_M + RP * 4;                 // float [4][2 RP] exchange
+  static constexpr int OFF_BAR = (OFF_X + 4 * 2 * RP * 4 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_BAR + 32 + 1024;             // + alignment slack
+};
+
+template <typename T, int RP, int D>
+__global__ void __launch_bounds__(NT, RP == 4 ? 5 : RP == 8 ? 4 : 3)
+few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s,
+           const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int behind) {
+  using C = Cfg<RP, D>;
+  constexpr int NC = C::NC, WPT = C::WPT;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sma = smem_u32(sm);
+  float* rowf = reinterpret_cast<float*>(sm + C::OFF_ROW);
+  float* rowo = rowf + RP;
+  int* rowe = reinterpret_cast<int*>(rowo + RP);
+  float* mref = reinterpret_cast<float*>(sm + C::OFF_M);
+  float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
+  uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  uint64_t* bar_o = bar_s + 1;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(bar_s + 2);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(bar_s + 3);
+  __shared__ int64_t sums[NT / 32];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    mbar_init(bar_s, 1);
+    mbar_init(bar_o, 1);
+    *gave_up = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(const_cast<uint32_t*>(slot))),
+                 "r"(C::COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  // behind the prefix part of the same call, what this part reads was there
+  // before that part's CTAs let it start
+  if (!behind) fp8::wait_for_previous();
+  fp8::next_may_start();
+
+  const uint32_t tm_k = tmem, tm_s = tmem + C::KC, tm_o = tm_s + NC;
+  const uint32_t quad = uint32_t(32 * warp) << 16;
+  const Batch& bt = part.t;
+  Cursor cur;
+  int64_t left = find_start(part, cur, sums);
+  uint32_t ph_s = 0, ph_o = 0;  // phases that were waited for
+
+  const int r4 = lane >> 2, c4 = lane & 3;
+  while (left > 0) {
+    // ---------------------------------------------------------------- a unit's tiles
+    const int t_lo = cur.s.tile0 + cur.tile;
+    const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+    const int seq_row = part.prefix ? 0 : cur.b;
+    const int lo = part.prefix ? 0 : part.shared, hi = cur.s.len;  // tokens of this part
+
+    // Registers of one tile: packed words of tokens 16 gi + r4 (+ 8) of the
+    // warp's 32, scales of token `lane`.
+    uint32_t kw[4][WPT], vw[4][WPT];
+    __half ks, vs;
+    bool there;
+    auto load = [&](int tile) {
+      int64_t at[2];
+      bool in[2];
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        const int tb = tile * TILE + 32 * warp + 16 * gi;
+        in[gi] = tb < hi && tb + 16 > lo;
+        int page = -1;
+        if (in[gi]) {
+          const int index = tb / bt.ps;
+          page = index < bt.max_pages ? __ldcg(bt.table + int64_t(seq_row) * bt.max_pages + index) : -1;
+          if (page < 0 || page >= bt.n_pages) {
+            record_error(QUAROT_ERR_INVALID_ARG);
+            in[gi] = false;
+          }
+        }
+        at[gi] = in[gi] ? (int64_t(page) * part.Hkv + cur.g) * bt.ps + tb % bt.ps : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = at[i >> 1] + r4 + 8 * (i & 1);
+        const bool ok = in[i >> 1];
+        if constexpr (WPT == 4) {
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 a = ok ? __ldcg(reinterpret_cast<const uint4*>(k_q + row * (D / 2)) + c4) : z;
+          const uint4 b = ok ? __ldcg(reinterpret_cast<const uint4*>(v_q + row * (D / 2)) + c4) : z;
+          kw[i][0] = a.x, kw[i][1] = a.y, kw[i][2] = a.z, kw[i][3] = a.w;
+          vw[i][0] = b.x, vw[i][1] = b.y, vw[i][2] = b.z, vw[i][3] = b.w;
+        } else {
+          const uint2 z = make_uint2(0u, 0u);
+          const uint2 a = ok ? __ldcg(reinterpret_cast<const uint2*>(k_q + row * (D / 2)) + c4) : z;
+          const uint2 b = ok ? __ldcg(reinterpret_cast<const uint2*>(v_q + row * (D / 2)) + c4) : z;
+          kw[i][0] = a.x, kw[i][1] = a.y;
+          vw[i][0] = b.x, vw[i][1] = b.y;
+        }
+      }
+      const int tok = tile * TILE + 32 * warp + lane;
+      there = (lane < 16 ? in[0] : in[1]) && tok >= lo && tok < hi;
+      const int64_t row = (lane < 16 ? at[0] : at[1]) + (lane & 15);
+      ks = vs = __ushort_as_half(0);
+      if (there) {
+        ks = __ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(k_s) + row));
+        vs = __ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(v_s) + row));
+      }
+    };
+    load(t_lo);
+
+    // ---- the rows' queries: a warp takes rows warp, warp + 4, ...; lane l
+    // holds dims E l .. E l + E - 1, E = d / 32
+    {
+      constexpr int E = D / 32;
+      for (int r = warp; r < RP; r += 4) {
+        const Row row = row_of(part, cur.s, cur.j * RP + r);
+        float x[E];
+        if (row.tok >= 0) {
+          const T* src = q + row.tok * ld_q + int64_t(cur.g * part.G + row.hh) * D + E * lane;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 f = fp8::to_f2<T>(__ldcg(reinterpret_cast<const unsigned int*>(src + e)));
+            x[e] = f.x;
+            x[e + 1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = 0.f;
+        }
+#pragma unroll
+        for (int s = 1; s < E; s <<= 1)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if ((e & s) == 0) {
+              const float a = x[e], b = x[e + s];
+              x[e] = a + b;
+              x[e + s] = a - b;
+            }
+        float amax = 0.f;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float other = __shfl_xor_sync(0xffffffffu, x[e], s);
+            x[e] = (lane & s) ? other - x[e] : x[e] + other;
+          }
+#pragma unroll
+        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+        // pieces of x * 256 / amax: the first of up to 256, the others' sixteenths
+        const float up = amax > 0.f ? 256.0f / amax : 0.f;
+        uint32_t c[E / 2][3];
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          float a = x[e] * up, b = x[e + 1] * up;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            c[e / 2][k] = fp8::cvt_e4m3x2(make_float2(a, b));
+            const float2 f = h2_to_f2(h2_of_e4m3x2(c[e / 2][k]));
+            const float w = k == 0 ? 1.f : k == 1 ? 0.0625f : 0.00390625f;
+            sum += (f.x + f.y) * w;
+            a = (a - f.x) * 16.f;
+            b = (b - f.y) * 16.f;
+          }
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        // dim 8 w + 2 byte + h lies in byte 4 (8 (w % WPT) + 2 (w / WPT) + h) + byte
+        const int w = E * lane / 8;
+        const uint32_t col = 8u * (w % WPT) + 2u * (w / WPT);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t n = k * RP + r;
+          auto put = [&](uint32_t pos) { return sma + C::OFF_Q + n * 128 + ((((pos >> 4) ^ n) & 7) << 4) + (pos & 15); };
+          if constexpr (E == 4) {
+            const uint32_t v = c[0][k] | (c[1][k] << 16);  // dims 0 1 2 3 of this lane
+            const uint32_t ev = (v & 0xFF) | ((v >> 8) & 0xFF00), od = ((v >> 8) & 0xFF) | ((v >> 16) & 0xFF00);
+            const uint32_t pos = 4 * col + 2 * (lane & 1);
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos)), "h"(uint16_t(ev)) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos + 4)), "h"(uint16_t(od)) : "memory");
+          } else {
+            const uint32_t pos = 4 * col + (lane & 3);
+            asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos)), "r"(c[0][k] & 0xFF) : "memory");
+            asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos + 4)), "r"(c[0][k] >> 8) : "memory");
+          }
+        }
+        if (lane == 0) {
+          rowf[r] = 2.0f * amax * qscale;       // 2^9 of the codes, 1 / 256 of the pieces
+          rowo[r] = sum * (8.0f / 512.0f);
+          rowe[r] = row.end;
+          mref[r] = -INFINITY;
+        }
+      }
+    }
+    to_async_proxy();
+
+    float l[RP], z[RP];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) l[r] = z[r] = 0.f;
+
+    for (int it = 0; it < nt; ++it) {
+      // ---- keys to tensor memory
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        uint32_t a[4 * WPT];
+#pragma unroll
+        for (int j = 0; j < WPT; ++j) {
+          bytes_of(kw[2 * gi][j], a[4 * j], a[4 * j + 1]);
+          bytes_of(kw[2 * gi + 1][j], a[4 * j + 2], a[4 * j + 3]);
+        }
+        if constexpr (WPT == 4) tmem_st_rows4(tm_k + quad + (uint32_t(16 * gi) << 16), a);
+        else tmem_st_rows2(tm_k + quad + (uint32_t(16 * gi) << 16), a);
+      }
+      tc_wait_st();
+      tc_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma8_ts(tm_s, tm_k + 8 * kk, desc_sw128(sma + C::OFF_Q + 32 * kk, 1024), idesc8(NC, false, false), kk > 0);
+        mma_commit(bar_s);
+      }
+      // ---- values to shared memory, once the products of the tile before have read theirs
+      if (it > 0) {
+        mbar_wait_bounded(bar_o, ph_o, const_cast<volatile int*>(gave_up));
+        ph_o ^= 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 32 * warp + 8 * i + r4;
+        uint32_t b[2 * WPT];
+#pragma unroll
+        for (int j = 0; j < WPT; ++j) bytes_of(vw[i][j], b[2 * j], b[2 * j + 1]);
+#pragma unroll
+        for (int h = 0; h < WPT / 2; ++h) {
+          const uint32_t chunk = uint32_t(WPT / 2 * c4 + h);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_V + t * 128 + ((chunk ^ (t & 7)) << 4)),
+                       "r"(b[4 * h]), "r"(b[4 * h + 1]), "r"(b[4 * h + 2]), "r"(b[4 * h + 3])
+                       : "memory");
+        }
+      }
+      const float ksf = __half2float(ks), vsf = __half2float(vs);
+      const bool seen = there;
+      const int tok = (t_lo + it) * TILE + tid;
+      if (it + 1 < nt) load(t_lo + it + 1);
+
+      // ---- scores of this thread's token
+      mbar_wait_bounded(bar_s, ph_s, const_cast<volatile int*>(gave_up));
+      ph_s ^= 1;
+      tc_after();
+      float s[RP];
+      {
+        uint32_t v[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
+        tc_wait_ld();
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float x = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
+                               fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r]))) - rowo[r];
+          s[r] = seen && tok < rowe[r] ? x * (rowf[r] * ksf) : -INFINITY;
+        }
+      }
+      const float lv = lg2(fmaxf(vsf, 5.9604645e-8f));
+      bool above = false;
+#pragma unroll
+      for (int r = 0; r < RP; ++r) above |= s[r] + lv > mref[r] + 8.0f;
+      if (__syncthreads_or(above)) {
+        // ---- raise the references that some score exceeds
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float v = s[r] + lv;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          if (lane == 0) xch[warp * RP + r] = v;
+        }
+        __syncthreads();
+        float al[RP];
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float mo = mref[r];
+          const float v = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
+          al[r] = v > mo + 8.0f ? ex2(mo - v) : 1.0f;
+          l[r] *= al[r];
+          z[r] *= al[r];
+        }
+        if (it > 0) {
+          uint32_t v[NC];
+          tc_after();
+#pragma unroll
+          for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, v + c);
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int r = 0; r < RP; ++r) v[k * RP + r] = __float_as_uint(__uint_as_float(v[k * RP + r]) * al[r]);
+#pragma unroll
+          for (int c = 0; c < NC; c += 16) tmem_st16(tm_o + quad + c, v + c);
+          tc_wait_st();
+        }
+        __syncthreads();
+        if (tid < RP) {
+          const float mo = mref[tid];
+          const float v = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
+          if (v > mo + 8.0f) mref[tid] = v;
+        }
+        __syncthreads();
+      }
+      // ---- probabilities: sums, and pieces to shared memory
+      uint32_t pw[3][RP / 4];
+#pragma unroll
+      for (int r = 0; r < RP; r += 4) {
+        uint32_t c[2][3];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float p[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rr = r + 2 * h + e;
+            const float m = mref[rr];
+            const float w = ex2(s[rr] - (m == -INFINITY ? 0.f : m));
+            l[rr] += w;
+            p[e] = w * vsf;
+            z[rr] += p[e];
+          }
+          pieces_of(h2_of_f2(p[0], p[1]), c[h]);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) pw[k][r / 4] = c[0][k] | (c[1][k] << 16);
+      }
+      uint32_t words[NC / 4];
+#pragma unroll
+      for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
+#pragma unroll
+      for (int i = 0; i < NC / 16; ++i)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_P + i * (16 * TILE) + tid * 16),
+                     "r"(words[4 * i]), "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
+                     : "memory");
+      to_async_proxy();
+      tc_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < TILE / 32; ++kk)
+          mma8_ss(tm_o, desc_sw128(sma + C::OFF_V + 4096 * kk, 1024), desc_plain(sma + C::OFF_P + 512 * kk, 128, 16 * TILE),
+                  idesc8(NC, true, true), it > 0 || kk > 0);
+        mma_commit(bar_o);
+      }
+    }
+
+    // ---------------------------------------------------------------- the unit's state
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
+      }
+      if (lane == 0) {
+        xch[warp * 2 * RP + r] = l[r];
+        xch[warp * 2 * RP + RP + r] = z[r];
+      }
+    }
+    __syncthreads();
+    mbar_wait_bounded(bar_o, ph_o, const_cast<volatile int*>(gave_up));
+    ph_o ^= 1;
+    tc_after();
+    uint32_t v[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, v + c);
+    tc_wait_ld();
+    const int J = (cur.s.rows + RP - 1) / RP;
+    const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, RP) + int64_t(cur.g) * J + cur.j;
+    const int64_t at = (unit + blockIdx.x) * RP;
+    const int dim = (tid & ~7) + 2 * (tid & 3) + ((tid >> 2) & 1);  // of byte tid of a token's row
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      const float zz = (xch[RP + r] + xch[3 * RP + r]) + (xch[5 * RP + r] + xch[7 * RP + r]);
+      const float o = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
+                           fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])));
+      if (tid < D) ws.o[(at + r) * D + dim] = fmaf(o, 512.0f, -8.0f * zz);
+    }
+    if (tid < RP) {
+      const float ll = (xch[tid] + xch[2 * RP + tid]) + (xch[4 * RP + tid] + xch[6 * RP + tid]);
+      *reinterpret_cast<float2*>(ws.ml + (at + tid) * 2) = make_float2(mref[tid], ll);
+    }
+    if (tid == 0) {
+      if (cur.tile == 0) ws.span[2 * unit] = blockIdx.x;
+      if (cur.tile + nt == cur.tiles) ws.span[2 * unit + 1] = blockIdx.x;
+    }
+    tc_before();
+    __syncthreads();  // the exchange, the rows and the references are read
+    left -= nt;
+    cur.tile += nt;
+    if (left > 0) {
+      next_unit(part, cur);
+      if (cur.tiles == 0) break;
+    }
+  }
+  if (behind) fp8::wait_for_previous();  // the prefix part is over before this part is
+  __syncthreads();
+  if (warp == 0) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
+  }
+}
+
+}  // namespace few
+
+// ------------------------------------------------------------------ join
+// One CTA per (token, query head), a thread a dim: the states of the row's
+// unit of each part, o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * SW)
-attn_kernel(const T* __restrict__ q, int64_t ld_q, int Hq, int Hkv, const uint8_t* __restrict__ k_q,
-            const __half* __restrict__ k_s, const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Batch t,
-            int shared_len, float qscale, int unrotate, T* __restrict__ out, int64_t ld_out) {
-  constexpr int E = D / 32;
-  __shared__ float qs[D], os[SW][D], ms[SW], ls[SW];
-  const int n = blockIdx.x / Hq, h = blockIdx.x % Hq, g = h / (Hq / Hkv);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place p = place_of(t, n);
-  if (p.b < 0) return;
-  const int len = p.pos + 1;
-  auto hadamard = [&](float* x) {
+__global__ void __launch_bounds__(D)
+join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __restrict__ out, int64_t ld_out) {
+  __shared__ float x[D];
+  fp8::wait_for_previous();
+  const int n = blockIdx.x / Hq, h = blockIdx.x % Hq, e = threadIdx.x;
+  const int g = h / own.G;
+  const Place pl = place_of(own.t, n);
+  if (pl.b < 0) return;
+  // slots of either part that hold a state of this row
+  const float *ml[2], *o[2];
+  int cnt[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Part& p = k == 0 ? pre : own;
+    const Space& s = k == 0 ? sp : so;
+    ml[k] = s.ml;
+    o[k] = s.o;
+    if (k == 0 && p.shared == 0) continue;
+    const Seq q = seq_of(p, pl.b, false);
+    const int rr = (n - q.tok0) * p.G + h - g * p.G;
+    if (pl.pos < 0 || rr < 0 || rr >= q.rows) continue;
+    const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
+    if (tiles_of(p, q, j) == 0) continue;
+    const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
+    const int first = __ldcg(s.span + 2 * unit), last = __ldcg(s.span + 2 * unit + 1);
+    cnt[k] = last - first + 1;
+    const int64_t at = (unit + first) * p.RP + rr - j * p.RP;
+    ml[k] += at * 2;
+    o[k] += at * D;
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < cnt[k]; ++i) m = fmaxf(m, __ldcg(ml[k] + int64_t(i) * (k == 0 ? pre.RP : own.RP) * 2));
+  float num = 0.f, den = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < cnt[k]; ++i) {
+      const int64_t r = int64_t(i) * (k == 0 ? pre.RP : own.RP);
+      const float2 s = __ldcg(reinterpret_cast<const float2*>(ml[k] + r * 2));
+      const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
+      den = fmaf(f, s.y, den);
+      num = fmaf(f, s.x == -INFINITY ? 0.f : __ldcg(o[k] + r * D + e), num);
+    }
+  float y = den > 0.f ? num / den : 0.f;
+  if (unrotate) {
     for (int span = 1; span < D; span <<= 1) {
-      float y = 0.f;
-      const int e = threadIdx.x;
-      if (e < D) y = (e & span) ? x[e ^ span] - x[e] : x[e] + x[e ^ span];
+      x[e] = y;
       __syncthreads();
-      if (e < D) x[e] = y;
+      const float other = x[e ^ span];
+      y = (e & span) ? other - y : y + other;
       __syncthreads();
     }
-  };
-  if (threadIdx.x < D) {
-    const T v = q[n * ld_q + int64_t(h) * D + threadIdx.x];
-    qs[threadIdx.x] = float(v);
+    y *= 1.0f / sqrtf(float(D));
   }
-  __syncthreads();
-  hadamard(qs);
-  float x[E], o[E], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i) {
-    x[i] = qs[lane * E + i] * qscale;
-    o[i] = 0.f;
-  }
-  for (int tok = warp; tok < len; tok += SW) {
-    const int page = page_at(t, tok < shared_len ? 0 : p.b, tok / t.ps);
-    if (page < 0) continue;
-    const int64_t at = (int64_t(page) * Hkv + g) * t.ps + tok % t.ps;
-    float s = 0.f;
-    for (int i = 0; i < E; i += 2) {
-      const uint8_t c = k_q[at * (D / 2) + (lane * E + i) / 2];
-      s += x[i] * float(int(c << 28) >> 28) + x[i + 1] * float(int(c << 24) >> 28);
-    }
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    s *= __half2float(k_s[at]);
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), e = exp2f(s - mn);
-    const float w = e * __half2float(v_s[at]);
-    m = mn;
-    l = l * a + e;
-    for (int i = 0; i < E; i += 2) {
-      const uint8_t c = v_q[at * (D / 2) + (lane * E + i) / 2];
-      o[i] = o[i] * a + w * float(int(c << 28) >> 28);
-      o[i + 1] = o[i + 1] * a + w * float(int(c << 24) >> 28);
-    }
-  }
-  for (int i = 0; i < E; ++i) os[warp][lane * E + i] = o[i];
-  if (lane == 0) {
-    ms[warp] = m;
-    ls[warp] = l;
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float mm = -INFINITY, num = 0.f, den = 0.f;
-    for (int w = 0; w < SW; ++w) mm = fmaxf(mm, ms[w]);
-    for (int w = 0; w < SW; ++w) {
-      const float f = mm == -INFINITY ? 0.f : exp2f(ms[w] - mm);
-      num += f * os[w][threadIdx.x];
-      den += f * ls[w];
-    }
-    qs[threadIdx.x] = den > 0.f ? num / den : 0.f;
-  }
-  __syncthreads();
-  if (unrotate) hadamard(qs);
-  if (threadIdx.x < D)
-    out[n * ld_out + int64_t(h) * D + threadIdx.x] = T(qs[threadIdx.x] * (unrotate ? 1.0f / sqrtf(float(D)) : 1.0f));
+  out[n * ld_out + int64_t(h) * D + e] = T(y);
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  int RP, ctas;
+  int64_t units;
+};
+inline int rows_of_unit(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+inline int ctas_per_sm(int RP) { return RP == 4 ? 5 : RP == 8 ? 4 : 3; }
+inline Plan plan_own(int64_t N, int64_t B, int64_t G, int64_t Hkv, int64_t max_q, int sms) {
+  Plan p;
+  p.RP = rows_of_unit(max_q * G);
+  p.ctas = sms * ctas_per_sm(p.RP);
+  p.units = unit_count(N, B, G, Hkv, p.RP);
+  return p;
+}
+inline Plan plan_prefix(int64_t N, int64_t G, int64_t Hkv, int64_t shared, int sms) {
+  Plan p = {4, 0, 0};
+  if (shared == 0) return p;
+  p.RP = rows_of_unit(N * G);
+  p.ctas = sms * ctas_per_sm(p.RP);
+  p.units = unit_count(N, 1, G, Hkv, p.RP);
+  return p;
 }
 
 }  // namespace paged
@@ -97,10 +872,36 @@ using namespace quarot::paged;
 
 extern "C" size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_q,
                                                int64_t shared_len) {
-  if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_q <= 0 ||
-      shared_len < 0)
+  if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_q <= 0 || shared_len < 0 ||
+      N > kMaxTokens || B > kMaxTokens || Hq > kMaxHeads)
     return 0;
-  return 256;
+  int sms = 0;
+  if (!sm_count(&sms)) return 0;
+  const int64_t mq = max_q < N ? max_q : N;
+  const Plan own = plan_own(N, B, Hq / Hkv, Hkv, mq, sms), pre = plan_prefix(N, Hq / Hkv, Hkv, shared_len, sms);
+  return space_bytes(own.units, own.ctas, own.RP, d) + space_bytes(pre.units, pre.ctas, pre.RP, d);
+}
+
+template <typename T, int D>
+static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half* k_s, const uint8_t* v_q, const __half* v_s,
+                     const Part& own, const Plan& po, const Space& so, const Part& pre, const Plan& pp, const Space& sp, int Hq,
+                     float qscale, int unrotate, T* out, int64_t ld_out, cudaStream_t st) {
+  auto few_part = [&](const Part& part, const Plan& plan, const Space& ws, int behind) -> int {
+    auto go = [&](auto kern, size_t smem, AttrCache& attr) {
+      if (!smem_attr_once(kern, int(smem), attr)) return int(QUAROT_ERR_LAUNCH);
+      return fp8::launch_dependent(kern, dim3(unsigned(plan.ctas)), few::NT, smem, 1, st, q, ld_q, k_q, k_s, v_q, v_s, part,
+                                   qscale, ws, behind);
+    };
+    static AttrCache attr[3];
+    if (plan.RP == 4) return go(few::few_kernel<T, 4, D>, few::Cfg<4, D>::SMEM, attr[0]);
+    if (plan.RP == 8) return go(few::few_kernel<T, 8, D>, few::Cfg<8, D>::SMEM, attr[1]);
+    return go(few::few_kernel<T, 16, D>, few::Cfg<16, D>::SMEM, attr[2]);
+  };
+  int rc = QUAROT_OK;
+  if (pre.shared > 0 && (rc = few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
+  if ((rc = few_part(own, po, so, pre.shared > 0)) != QUAROT_OK) return rc;
+  return fp8::launch_dependent(join_kernel<T, D>, dim3(unsigned(own.N) * unsigned(Hq)), D, 0, 1, st, own, so, pre, sp, Hq,
+                               unrotate, out, ld_out);
 }
 
 extern "C" int quarot_paged_attn(const void* q, int64_t ld_q, int dtype, int64_t N, int64_t Hq, int64_t Hkv, int64_t d,
@@ -114,27 +915,31 @@ extern "C" int quarot_paged_attn(const void* q, int64_t ld_q, int dtype, int64_t
   if (Hq <= 0 || Hq % Hkv != 0 || max_q <= 0 || shared_len < 0 || shared_len > max_pages * page_size ||
       (unrotate_out != 0 && unrotate_out != 1) || isnan(sm_scale) || isinf(sm_scale))
     return QUAROT_ERR_INVALID_ARG;
-  if (Hq > kMaxHeads) return QUAROT_ERR_UNSUPPORTED;
+  if (Hq > kMaxHeads || N * Hq > 0x7fffffff) return QUAROT_ERR_UNSUPPORTED;
   if (N == 0 || B == 0) return QUAROT_OK;
   if ((rc = check_heads(q, ld_q, Hq, d)) != QUAROT_OK || (rc = check_heads(out, ld_out, Hq, d)) != QUAROT_OK) return rc;
   if ((rc = check_cache(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_pages)) != QUAROT_OK) return rc;
-  if (!workspace || ws_bytes < quarot_paged_workspace_bytes(N, B, Hq, Hkv, d, max_q, shared_len)) return QUAROT_ERR_INVALID_ARG;
+  if (!workspace) return QUAROT_ERR_INVALID_ARG;
   if (misaligned(workspace, 256)) return QUAROT_ERR_ALIGNMENT;
+  if (ws_bytes < quarot_paged_workspace_bytes(N, B, Hq, Hkv, d, max_q, shared_len)) return QUAROT_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
+  const int64_t G = Hq / Hkv, mq = max_q < N ? max_q : N;
+  const Plan po = plan_own(N, B, G, Hkv, mq, sms), pp = plan_prefix(N, G, Hkv, shared_len, sms);
   const Batch t = {page_table, lengths, cu_q, int(B), int(max_pages), int(n_pages), int(page_size)};
+  const Part own = {t, int(N), int(G), int(Hkv), int(shared_len), 0, po.RP}, pre = {t, int(N), int(G), int(Hkv), int(shared_len), 1, pp.RP};
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  const Space so = space_at(w, po.units, po.ctas, po.RP);
+  const Space sp = space_at(w + space_bytes(po.units, po.ctas, po.RP, d), pp.units, pp.ctas, pp.RP);
   const float qscale = (sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(float(d))) * 1.4426950408889634f / sqrtf(float(d));
-  auto go = [&](auto kern, auto* qp, auto* op) {
-    kern<<<unsigned(N * Hq), 32 * SW, 0, static_cast<cudaStream_t>(stream)>>>(
-        qp, ld_q, int(Hq), int(Hkv), k_q, static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), t,
-        int(shared_len), qscale, unrotate_out, op, ld_out);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto* ksh = static_cast<const __half*>(k_s);
+  auto* vsh = static_cast<const __half*>(v_s);
+  auto typed = [&](auto* qp, auto* op) {
+    using T = std::remove_pointer_t<decltype(op)>;
+    return d == 64 ? attn_impl<T, 64>(qp, ld_q, k_q, ksh, v_q, vsh, own, po, so, pre, pp, sp, int(Hq), qscale, unrotate_out, op, ld_out, st)
+                   : attn_impl<T, 128>(qp, ld_q, k_q, ksh, v_q, vsh, own, po, so, pre, pp, sp, int(Hq), qscale, unrotate_out, op, ld_out, st);
   };
-  if (dtype == QUAROT_FP16) {
-    auto* qp = static_cast<const __half*>(q);
-    auto* op = static_cast<__half*>(out);
-    d == 64 ? go(attn_kernel<__half, 64>, qp, op) : go(attn_kernel<__half, 128>, qp, op);
-  } else {
-    auto* qp = static_cast<const __nv_bfloat16*>(q);
-    auto* op = static_cast<__nv_bfloat16*>(out);
-    d == 64 ? go(attn_kernel<__nv_bfloat16, 64>, qp, op) : go(attn_kernel<__nv_bfloat16, 128>, qp, op);
-  }
-  return cuda_ok(cudaGetLastError()) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  if (dtype == QUAROT_FP16) return typed(static_cast<const __half*>(q), static_cast<__half*>(out));
+  return typed(static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out));
 }
