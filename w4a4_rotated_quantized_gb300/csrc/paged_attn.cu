@@ -134,6 +134,8 @@ __device__ __forceinline__ void pieces_of(uint32_t a, uint32_t* c) {
 
 // ------------------------------------------------------------------ units
 constexpr int TILE = 128;  // tokens
+constexpr int kTries = 1 << 18;
+constexpr float kNone = -1e30f;  // reference of a row that has seen nothing: 2^(kNone - s) is 0
 
 // One part of a call: the shared prefix (rows of all N tokens as one list,
 // tokens [0, shared)) or the sequences' own tokens [shared, length).
@@ -220,65 +222,72 @@ struct Cursor {
   int b, g, j, tile, tiles;  // unit (b, g, j), next of its tiles, all of them
   Seq s;
 };
-// Sum over the block; all threads get it.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sums over the block: of the threads up to this one, and (returned) of all.
+__device__ __forceinline__ int64_t block_scan(int64_t& v, int64_t* sh) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (int(threadIdx.x & 31) >= o) v += y;
+  }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 31) sh[threadIdx.x >> 5] = v;
   __syncthreads();
-  int64_t r = 0;
-  for (int w = 0; w < int(blockDim.x >> 5); ++w) r += sh[w];
-  return r;
+  int64_t all = 0;
+  for (int w = 0; w < int(blockDim.x >> 5); ++w) {
+    if (w < int(threadIdx.x >> 5)) v += sh[w];
+    all += sh[w];
+  }
+  return all;
 }
-// Sets the cursor to tile w * per of the row (per = the row's w-th part) and
-// returns how many tiles the CTA has.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // both positive
+  return (a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+// Sets the cursor to this CTA's first tile (the row of all tiles is cut into
+// equal parts, the last ones maybe none) and returns how many it has.
 __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
-  const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B;
-  int64_t mine = 0;
-  for (int b = threadIdx.x; b < nseq; b += n) mine += steps_of(p, seq_of(p, b, blockIdx.x == 0));
-  const int64_t total = block_sum(mine, sh) * p.Hkv;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t at = per * blockIdx.x;
-  if (at >= total) return 0;
-  // the sequence that holds tile `at`: sequences in blocks of n, then within one
+  const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
+  const bool tell = blockIdx.x == 0;
   __shared__ int found;
   __shared__ int64_t before;
-  if (threadIdx.x == 0) found = -1;
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < nseq; b0 += n) {
-    const int b = b0 + threadIdx.x;
-    const int64_t v = b < nseq ? steps_of(p, seq_of(p, b, false)) * p.Hkv : 0;
-    int64_t x = v;  // inclusive sum over the block
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (int(threadIdx.x & 31) >= o) x += y;
+  // sequences in blocks of n, this thread's within the first one kept
+  int64_t first = tid < nseq ? steps_of(p, seq_of(p, tid, tell)) * p.Hkv : 0, sum = first;
+  for (int b = tid + n; b < nseq; b += n) sum += steps_of(p, seq_of(p, b, tell)) * p.Hkv;
+  if (tid == 0) found = -1;
+  const int64_t own = first;
+  int64_t all = block_scan(first, sh), total = all;
+  if (nseq > n) total = block_scan(sum, sh);
+  if (total == 0) return 0;
+  const int64_t per = quotient(total + gridDim.x - 1, gridDim.x), at = per * blockIdx.x;
+  if (at >= total) return 0;
+  int64_t v = own, x = first, done = 0;
+  for (int b0 = 0;;) {
+    if (v > 0 && at >= done + x - v && at < done + x) {
+      found = b0 + tid;
+      before = done + x - v;
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 31) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < n / 32; ++w) {
-      if (w < int(threadIdx.x >> 5)) x += sh[w];
-      all += sh[w];
-    }
-    if (v > 0 && at >= sum + x - v && at < sum + x) {
-      found = b;
-      before = sum + x - v;
-    }
-    sum += all;
     __syncthreads();
     if (found >= 0) break;
+    done += all;
+    b0 += n;
+    x = v = b0 + tid < nseq ? steps_of(p, seq_of(p, b0 + tid, false)) * p.Hkv : 0;
+    all = block_scan(x, sh);
+    if (b0 >= nseq) return 0;  // the batch changed under the call
   }
   c.b = found;
   c.s = seq_of(p, c.b, false);
-  const int64_t head = steps_of(p, c.s);
   int64_t rest = at - before;
-  c.g = int(rest / head);
+  const int64_t head = steps_of(p, c.s);
+  c.g = int(quotient(rest, head));
   rest -= c.g * head;
   c.j = 0;
-  while (rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
-    rest -= c.tiles;
-    ++c.j;
+  if (p.prefix) {
+    c.tiles = tiles_of(p, c.s, 0);
+    c.j = int(quotient(rest, c.tiles));
+    rest -= int64_t(c.j) * c.tiles;
+  } else {
+    while (rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
+      rest -= c.tiles;
+      ++c.j;
+    }
   }
   c.tile = int(rest);
   return min(per, total - at);
@@ -344,9 +353,12 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // exceeds it by 8, so p' <= 2^8 and the largest is at least 1 (fp16, then its
 // pieces, hold it to 2^-12).  Sums of 2^(s - m) and of p' stay in fp32.
 //
-// A CTA is four warps that do it all in turn; the overlap of loads, tensor
-// cores and arithmetic comes from several CTAs on an SM, and the next tile's
-// loads, which are in registers before this tile's scores are.
+// A CTA is four warps that do it all in turn, with one barrier a tile: behind
+// it one thread issues the scores' products of the next tile and the outputs'
+// of this one.  The barrier also tells whether some thread's score passed its
+// reference; then the references are raised and the probabilities made again.
+// Loads are two tiles (keys) and one (values) ahead in registers, the page
+// numbers one more; several CTAs on an SM fill each other's waits.
 namespace few {
 
 constexpr int NT = 128;
@@ -415,67 +427,111 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   Cursor cur;
   int64_t left = find_start(part, cur, sums);
   uint32_t ph_s = 0, ph_o = 0;  // phases that were waited for
+  // A wait ends after about a second (each try sleeps some microseconds), is
+  // recorded, and all later ones end at once.
+  auto wait = [&](uint64_t* bar, uint32_t& phase) {
+    bool ok = mbar_try_wait(bar, phase);
+    for (int n = 0; !ok && n < kTries && !*gave_up; ++n) ok = mbar_try_wait(bar, phase);
+    if (!ok) {
+      *gave_up = 1;
+      record_error(QUAROT_ERR_TIMEOUT);
+    }
+    phase ^= 1;
+  };
 
   const int r4 = lane >> 2, c4 = lane & 3;
+  const int shift = (bt.ps & (bt.ps - 1)) == 0 ? __ffs(bt.ps) - 1 : -1;
+  // Registers of the tiles to come: packed words of tokens 16 gi + r4 (+ 8) of
+  // the warp's 32, scales of token `lane`; whether the token is there.
+  uint32_t kw[4][WPT], vw[4][WPT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < WPT; ++j) kw[i][j] = vw[i][j] = 0u;
   while (left > 0) {
     // ---------------------------------------------------------------- a unit's tiles
     const int t_lo = cur.s.tile0 + cur.tile;
     const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
-    const int seq_row = part.prefix ? 0 : cur.b;
     const int lo = part.prefix ? 0 : part.shared, hi = cur.s.len;  // tokens of this part
+    const int32_t* table = bt.table + int64_t(part.prefix ? 0 : cur.b) * bt.max_pages;
 
-    // Registers of one tile: packed words of tokens 16 gi + r4 (+ 8) of the
-    // warp's 32, scales of token `lane`.
-    uint32_t kw[4][WPT], vw[4][WPT];
-    __half ks, vs;
-    bool there;
-    auto load = [&](int tile) {
-      int64_t at[2];
-      bool in[2];
+    // Rows of the pages that groups of 16 tokens lie in: in [gi], the first
+    // token's row of [n_pages, Hkv, ps], or -1 (out of this part, or no page).
+    auto pages = [&](int tile, int* page) {
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
         const int tb = tile * TILE + 32 * warp + 16 * gi;
-        in[gi] = tb < hi && tb + 16 > lo;
-        int page = -1;
-        if (in[gi]) {
-          const int index = tb / bt.ps;
-          page = index < bt.max_pages ? __ldcg(bt.table + int64_t(seq_row) * bt.max_pages + index) : -1;
-          if (page < 0 || page >= bt.n_pages) {
-            record_error(QUAROT_ERR_INVALID_ARG);
-            in[gi] = false;
-          }
-        }
-        at[gi] = in[gi] ? (int64_t(page) * part.Hkv + cur.g) * bt.ps + tb % bt.ps : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = at[i >> 1] + r4 + 8 * (i & 1);
-        const bool ok = in[i >> 1];
-        if constexpr (WPT == 4) {
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-          const uint4 a = ok ? __ldcg(reinterpret_cast<const uint4*>(k_q + row * (D / 2)) + c4) : z;
-          const uint4 b = ok ? __ldcg(reinterpret_cast<const uint4*>(v_q + row * (D / 2)) + c4) : z;
-          kw[i][0] = a.x, kw[i][1] = a.y, kw[i][2] = a.z, kw[i][3] = a.w;
-          vw[i][0] = b.x, vw[i][1] = b.y, vw[i][2] = b.z, vw[i][3] = b.w;
-        } else {
-          const uint2 z = make_uint2(0u, 0u);
-          const uint2 a = ok ? __ldcg(reinterpret_cast<const uint2*>(k_q + row * (D / 2)) + c4) : z;
-          const uint2 b = ok ? __ldcg(reinterpret_cast<const uint2*>(v_q + row * (D / 2)) + c4) : z;
-          kw[i][0] = a.x, kw[i][1] = a.y;
-          vw[i][0] = b.x, vw[i][1] = b.y;
-        }
-      }
-      const int tok = tile * TILE + 32 * warp + lane;
-      there = (lane < 16 ? in[0] : in[1]) && tok >= lo && tok < hi;
-      const int64_t row = (lane < 16 ? at[0] : at[1]) + (lane & 15);
-      ks = vs = __ushort_as_half(0);
-      if (there) {
-        ks = __ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(k_s) + row));
-        vs = __ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(v_s) + row));
+        const int index = shift >= 0 ? tb >> shift : tb / bt.ps;
+        page[gi] = tb < hi && tb + 16 > lo && tile < t_lo + nt ? (index < bt.max_pages ? __ldcg(table + index) : -1) : -2;
       }
     };
-    load(t_lo);
+    auto rows = [&](int tile, const int* page, int64_t* at) {
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        const int tb = tile * TILE + 32 * warp + 16 * gi;
+        const int off = shift >= 0 ? tb & (bt.ps - 1) : tb % bt.ps;
+        const bool ok = unsigned(page[gi]) < unsigned(bt.n_pages);
+        if (!ok && page[gi] != -2) record_error(QUAROT_ERR_INVALID_ARG);
+        at[gi] = ok ? (int64_t(page[gi]) * part.Hkv + cur.g) * bt.ps + off : -1;
+      }
+    };
+    auto load = [&](uint32_t (*w)[WPT], const uint8_t* src, const int64_t* at) {
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi)
+        if (at[gi] >= 0) {
+          const uint8_t* p = src + (at[gi] + r4) * (D / 2) + c4 * (4 * WPT);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (WPT == 4) {
+              const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p + 8 * h * (D / 2)));
+              w[2 * gi + h][0] = a.x, w[2 * gi + h][1] = a.y, w[2 * gi + h][2] = a.z, w[2 * gi + h][3] = a.w;
+            } else {
+              const uint2 a = __ldcg(reinterpret_cast<const uint2*>(p + 8 * h * (D / 2)));
+              w[2 * gi + h][0] = a.x, w[2 * gi + h][1] = a.y;
+            }
+          }
+        }
+    };
+    // Scales of this thread's token, both 0 where it is not one of this part.
+    auto load_scales = [&](int tile, const int64_t* at) -> uint32_t {
+      const int tok = tile * TILE + tid;
+      const int64_t row = lane < 16 ? at[0] : at[1];
+      uint32_t v = 0xFFFF0000u;  // no token: the value scale's place holds a NaN, which no token's does
+      if (row >= 0 && tok >= lo && tok < hi)
+        v = __ldcg(reinterpret_cast<const unsigned short*>(k_s) + row + (lane & 15)) |
+            uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(v_s) + row + (lane & 15))) << 16;
+      return v;
+    };
+    // the keys of a tile, from registers to tensor memory
+    auto put_keys = [&]() {
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        uint32_t a[4 * WPT];
+#pragma unroll
+        for (int j = 0; j < WPT; ++j) {
+          bytes_of(kw[2 * gi][j], a[4 * j], a[4 * j + 1]);
+          bytes_of(kw[2 * gi + 1][j], a[4 * j + 2], a[4 * j + 3]);
+        }
+        if constexpr (WPT == 4) tmem_st_rows4(tm_k + quad + (uint32_t(16 * gi) << 16), a);
+        else tmem_st_rows2(tm_k + quad + (uint32_t(16 * gi) << 16), a);
+      }
+    };
+    auto issue_scores = [&]() {
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk)
+        mma8_ts(tm_s, tm_k + 8 * kk, desc_sw128(sma + C::OFF_Q + 32 * kk, 1024), idesc8(NC, false, false), kk > 0);
+      mma_commit(bar_s);
+    };
 
+    // tile t_lo: keys and values; pages of the next
+    int64_t at[2], at_n[2];
+    int pg[2];
+    pages(t_lo, pg);
+    rows(t_lo, pg, at);
+    load(kw, k_q, at);
+    load(vw, v_q, at);
+    uint32_t sc = load_scales(t_lo, at), sc_n = 0;
+    pages(t_lo + 1, pg);
     // ---- the rows' queries: a warp takes rows warp, warp + 4, ...; lane l
     // holds dims E l .. E l + E - 1, E = d / 32
     {
@@ -558,44 +614,40 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
           rowf[r] = 2.0f * amax * qscale;       // 2^9 of the codes, 1 / 256 of the pieces
           rowo[r] = sum * (8.0f / 512.0f);
           rowe[r] = row.end;
-          mref[r] = -INFINITY;
+          mref[r] = kNone;
         }
       }
     }
     to_async_proxy();
+
+    // scores of the first tile; keys and scales of the second
+    put_keys();
+    tc_wait_st();
+    tc_before();
+    rows(t_lo + 1, pg, at_n);
+    load(kw, k_q, at_n);
+    sc_n = load_scales(t_lo + 1, at_n);
+    pages(t_lo + 2, pg);
+    __syncthreads();
+    if (tid == 0) {
+      tc_after();
+      issue_scores();
+    }
 
     float l[RP], z[RP];
 #pragma unroll
     for (int r = 0; r < RP; ++r) l[r] = z[r] = 0.f;
 
     for (int it = 0; it < nt; ++it) {
-      // ---- keys to tensor memory
+      // ---- the next tile's keys to tensor memory, once this one's scores are there
+      wait(bar_s, ph_s);
+      tc_after();
+      uint32_t v[NC];
 #pragma unroll
-      for (int gi = 0; gi < 2; ++gi) {
-        uint32_t a[4 * WPT];
-#pragma unroll
-        for (int j = 0; j < WPT; ++j) {
-          bytes_of(kw[2 * gi][j], a[4 * j], a[4 * j + 1]);
-          bytes_of(kw[2 * gi + 1][j], a[4 * j + 2], a[4 * j + 3]);
-        }
-        if constexpr (WPT == 4) tmem_st_rows4(tm_k + quad + (uint32_t(16 * gi) << 16), a);
-        else tmem_st_rows2(tm_k + quad + (uint32_t(16 * gi) << 16), a);
-      }
-      tc_wait_st();
-      tc_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma8_ts(tm_s, tm_k + 8 * kk, desc_sw128(sma + C::OFF_Q + 32 * kk, 1024), idesc8(NC, false, false), kk > 0);
-        mma_commit(bar_s);
-      }
+      for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
+      if (it + 1 < nt) put_keys();
       // ---- values to shared memory, once the products of the tile before have read theirs
-      if (it > 0) {
-        mbar_wait_bounded(bar_o, ph_o, const_cast<volatile int*>(gave_up));
-        ph_o ^= 1;
-      }
+      if (it > 0) wait(bar_o, ph_o);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 32 * warp + 8 * i + r4;
@@ -610,113 +662,121 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
                        : "memory");
         }
       }
-      const float ksf = __half2float(ks), vsf = __half2float(vs);
-      const bool seen = there;
-      const int tok = (t_lo + it) * TILE + tid;
-      if (it + 1 < nt) load(t_lo + it + 1);
-
-      // ---- scores of this thread's token
-      mbar_wait_bounded(bar_s, ph_s, const_cast<volatile int*>(gave_up));
-      ph_s ^= 1;
-      tc_after();
-      float s[RP];
-      {
-        uint32_t v[NC];
-#pragma unroll
-        for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
-        tc_wait_ld();
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float x = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
-                               fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r]))) - rowo[r];
-          s[r] = seen && tok < rowe[r] ? x * (rowf[r] * ksf) : -INFINITY;
+      // ---- loads ahead: values of the next tile, keys and scales of the one after
+      const uint32_t sc0 = sc;
+      if (it + 1 < nt) {
+        load(vw, v_q, at_n);
+        sc = sc_n;
+        if (it + 2 < nt) {
+          rows(t_lo + it + 2, pg, at_n);
+          load(kw, k_q, at_n);
+          sc_n = load_scales(t_lo + it + 2, at_n);
+          pages(t_lo + it + 3, pg);
         }
       }
+
+      // ---- scores of this thread's token
+      const float2 scales = h2_to_f2(sc0);
+      const float ksf = scales.x, vsf = sc0 == 0xFFFF0000u ? 0.f : scales.y;
+      const int tok = sc0 == 0xFFFF0000u ? 0x7fffffff : (t_lo + it) * TILE + tid;
       const float lv = lg2(fmaxf(vsf, 5.9604645e-8f));
+      tc_wait_ld();
+      float s[RP];
       bool above = false;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) above |= s[r] + lv > mref[r] + 8.0f;
+      for (int r = 0; r < RP; ++r) {
+        const float x = fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])) +
+                        fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f, -rowo[r]);
+        s[r] = tok < rowe[r] ? x * (rowf[r] * ksf) : -INFINITY;
+        above |= s[r] + lv > mref[r] + 8.0f;
+      }
+      float p[RP], w[RP];
+      auto probabilities = [&]() {
+        uint32_t pw[3][RP / 4];
+#pragma unroll
+        for (int r = 0; r < RP; r += 4) {
+          uint32_t c[2][3];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int rr = r + 2 * h + e;
+              w[rr] = ex2(s[rr] - mref[rr]);
+              p[rr] = w[rr] * vsf;
+            }
+            pieces_of(h2_of_f2(p[r + 2 * h], p[r + 2 * h + 1]), c[h]);
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k) pw[k][r / 4] = c[0][k] | (c[1][k] << 16);
+        }
+        uint32_t words[NC / 4];
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_P + i * (16 * TILE) + tid * 16),
+                       "r"(words[4 * i]), "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
+                       : "memory");
+        to_async_proxy();
+      };
+      probabilities();
+      if (it + 1 < nt) tc_wait_st();
+      tc_before();
       if (__syncthreads_or(above)) {
-        // ---- raise the references that some score exceeds
+        // ---- raise the references that some score exceeds; sums and outputs so far follow
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          float v = s[r] + lv;
+          float x = s[r] + lv;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          if (lane == 0) xch[warp * RP + r] = v;
+          for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          if (lane == 0) xch[warp * RP + r] = x;
         }
         __syncthreads();
         float al[RP];
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          const float mo = mref[r];
-          const float v = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
-          al[r] = v > mo + 8.0f ? ex2(mo - v) : 1.0f;
+          const float mo = mref[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
+          al[r] = x > mo + 8.0f ? ex2(mo - x) : 1.0f;
           l[r] *= al[r];
           z[r] *= al[r];
         }
         if (it > 0) {
-          uint32_t v[NC];
+          uint32_t o[NC];
           tc_after();
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, v + c);
+          for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, o + c);
           tc_wait_ld();
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll
-            for (int r = 0; r < RP; ++r) v[k * RP + r] = __float_as_uint(__uint_as_float(v[k * RP + r]) * al[r]);
+            for (int r = 0; r < RP; ++r) o[k * RP + r] = __float_as_uint(__uint_as_float(o[k * RP + r]) * al[r]);
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) tmem_st16(tm_o + quad + c, v + c);
+          for (int c = 0; c < NC; c += 16) tmem_st16(tm_o + quad + c, o + c);
           tc_wait_st();
         }
         __syncthreads();
         if (tid < RP) {
-          const float mo = mref[tid];
-          const float v = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
-          if (v > mo + 8.0f) mref[tid] = v;
+          const float mo = mref[tid], x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
+          if (x > mo + 8.0f) mref[tid] = x;
         }
         __syncthreads();
+        probabilities();
+        tc_before();
+        __syncthreads();
       }
-      // ---- probabilities: sums, and pieces to shared memory
-      uint32_t pw[3][RP / 4];
-#pragma unroll
-      for (int r = 0; r < RP; r += 4) {
-        uint32_t c[2][3];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float p[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rr = r + 2 * h + e;
-            const float m = mref[rr];
-            const float w = ex2(s[rr] - (m == -INFINITY ? 0.f : m));
-            l[rr] += w;
-            p[e] = w * vsf;
-            z[rr] += p[e];
-          }
-          pieces_of(h2_of_f2(p[0], p[1]), c[h]);
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) pw[k][r / 4] = c[0][k] | (c[1][k] << 16);
-      }
-      uint32_t words[NC / 4];
-#pragma unroll
-      for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
-#pragma unroll
-      for (int i = 0; i < NC / 16; ++i)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_P + i * (16 * TILE) + tid * 16),
-                     "r"(words[4 * i]), "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
-                     : "memory");
-      to_async_proxy();
-      tc_before();
-      __syncthreads();
       if (tid == 0) {
         tc_after();
+        if (it + 1 < nt) issue_scores();
 #pragma unroll
         for (int kk = 0; kk < TILE / 32; ++kk)
           mma8_ss(tm_o, desc_sw128(sma + C::OFF_V + 4096 * kk, 1024), desc_plain(sma + C::OFF_P + 512 * kk, 128, 16 * TILE),
                   idesc8(NC, true, true), it > 0 || kk > 0);
         mma_commit(bar_o);
+      }
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        l[r] += w[r];
+        z[r] += p[r];
       }
     }
 
@@ -734,8 +794,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
       }
     }
     __syncthreads();
-    mbar_wait_bounded(bar_o, ph_o, const_cast<volatile int*>(gave_up));
-    ph_o ^= 1;
+    wait(bar_o, ph_o);
     tc_after();
     uint32_t v[NC];
 #pragma unroll
@@ -743,18 +802,18 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
     tc_wait_ld();
     const int J = (cur.s.rows + RP - 1) / RP;
     const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, RP) + int64_t(cur.g) * J + cur.j;
-    const int64_t at = (unit + blockIdx.x) * RP;
+    const int64_t dst = (unit + blockIdx.x) * RP;
     const int dim = (tid & ~7) + 2 * (tid & 3) + ((tid >> 2) & 1);  // of byte tid of a token's row
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
       const float zz = (xch[RP + r] + xch[3 * RP + r]) + (xch[5 * RP + r] + xch[7 * RP + r]);
       const float o = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
                            fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])));
-      if (tid < D) ws.o[(at + r) * D + dim] = fmaf(o, 512.0f, -8.0f * zz);
+      if (tid < D) ws.o[(dst + r) * D + dim] = fmaf(o, 512.0f, -8.0f * zz);
     }
     if (tid < RP) {
       const float ll = (xch[tid] + xch[2 * RP + tid]) + (xch[4 * RP + tid] + xch[6 * RP + tid]);
-      *reinterpret_cast<float2*>(ws.ml + (at + tid) * 2) = make_float2(mref[tid], ll);
+      *reinterpret_cast<float2*>(ws.ml + (dst + tid) * 2) = make_float2(mref[tid], ll);
     }
     if (tid == 0) {
       if (cur.tile == 0) ws.span[2 * unit] = blockIdx.x;
@@ -781,11 +840,12 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 
 // ------------------------------------------------------------------ join
 // One CTA per (token, query head), a thread a dim: the states of the row's
-// unit of each part, o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
+// unit of each part, o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, d of them
+// at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
 join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __restrict__ out, int64_t ld_out) {
-  __shared__ float x[D];
+  __shared__ float x[D], top[D / 32], low[D / 32];
   fp8::wait_for_previous();
   const int n = blockIdx.x / Hq, h = blockIdx.x % Hq, e = threadIdx.x;
   const int g = h / own.G;
@@ -807,34 +867,54 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
     const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
     if (tiles_of(p, q, j) == 0) continue;
     const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
-    const int first = __ldcg(s.span + 2 * unit), last = __ldcg(s.span + 2 * unit + 1);
-    cnt[k] = last - first + 1;
-    const int64_t at = (unit + first) * p.RP + rr - j * p.RP;
+    const int2 span = __ldcg(reinterpret_cast<const int2*>(s.span + 2 * unit));
+    cnt[k] = span.y - span.x + 1;
+    const int64_t at = (unit + span.x) * p.RP + rr - j * p.RP;
     ml[k] += at * 2;
     o[k] += at * D;
   }
-  float m = -INFINITY;
+  float m = kNone, num = 0.f, den = 0.f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < cnt[k]; ++i) m = fmaxf(m, __ldcg(ml[k] + int64_t(i) * (k == 0 ? pre.RP : own.RP) * 2));
-  float num = 0.f, den = 0.f;
+  for (int k = 0; k < 2; ++k) {
+    const int64_t step = k == 0 ? pre.RP : own.RP;
+    for (int i0 = 0; i0 < cnt[k]; i0 += D) {
+      const int c = min(cnt[k] - i0, D);
+      float2 s = make_float2(kNone, 0.f);
+      if (e < c) s = __ldcg(reinterpret_cast<const float2*>(ml[k] + (i0 + e) * step * 2));
+      float mx = s.x;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < cnt[k]; ++i) {
-      const int64_t r = int64_t(i) * (k == 0 ? pre.RP : own.RP);
-      const float2 s = __ldcg(reinterpret_cast<const float2*>(ml[k] + r * 2));
-      const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
-      den = fmaf(f, s.y, den);
-      num = fmaf(f, s.x == -INFINITY ? 0.f : __ldcg(o[k] + r * D + e), num);
+      for (int b = 16; b > 0; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
+      __syncthreads();
+      if ((e & 31) == 0) top[e >> 5] = mx;
+      __syncthreads();
+      mx = m;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) mx = fmaxf(mx, top[w]);
+      const float a = ex2(m - mx), f = ex2(s.x - mx);
+      m = mx;
+      x[e] = f;
+      float lw = f * s.y;
+#pragma unroll
+      for (int b = 16; b > 0; b >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, b);
+      if ((e & 31) == 0) low[e >> 5] = lw;
+      __syncthreads();
+      den *= a;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) den += low[w];
+      num *= a;
+      const float* src = o[k] + i0 * step * D + e;
+#pragma unroll 8
+      for (int i = 0; i < c; ++i) num = fmaf(x[i], __ldcg(src + i * step * D), num);
     }
+  }
   float y = den > 0.f ? num / den : 0.f;
   if (unrotate) {
     for (int span = 1; span < D; span <<= 1) {
+      __syncthreads();
       x[e] = y;
       __syncthreads();
       const float other = x[e ^ span];
       y = (e & span) ? other - y : y + other;
-      __syncthreads();
     }
     y *= 1.0f / sqrtf(float(D));
   }
