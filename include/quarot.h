@@ -516,8 +516,8 @@ int quarot_fp8_gated_gemm(const uint8_t* a_q, const float* a_scale, const uint8_
  * rot / 2 of them, 8-byte aligned); the other elements stay.  Scaled
  * frequencies for long contexts are just other inv_freq.
  *
- * Pages: codes k_q, v_q uint8 [n_pages, Hkv, page_size, d / 2] (16-byte
- * aligned), scales k_s, v_s fp16 [n_pages, Hkv, page_size], the codes and
+ * Pages: codes k_q, v_q uint8 [n_pages, Hkv, page_size, d / 2], scales k_s,
+ * v_s fp16 [n_pages, Hkv, page_size] (all 16-byte aligned), the codes and
  * scales of quarot_kv_write.  page_size is a multiple of 16, at most 65536.
  * Token p of sequence b is slot p % page_size of page
  * page_table[b * max_pages + p / page_size] (int32).

@@ -139,14 +139,15 @@ inline int check_sizes(int dtype, int64_t N, int64_t Hkv, int64_t d, int64_t n_p
   if (cu == nullptr && N != B) return QUAROT_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return QUAROT_ERR_UNSUPPORTED;
   if (ps % 16 != 0 || ps > 65536 || n_pages > 0x7fffffff || max_pages > 0x7fff0000 / ps) return QUAROT_ERR_UNSUPPORTED;
-  if (N > kMaxTokens || B > kMaxTokens || Hkv > kMaxHeads) return QUAROT_ERR_UNSUPPORTED;
+  if (N > kMaxTokens || B > kMaxTokens || Hkv > kMaxHeads || n_pages > (int64_t(1) << 35) / (Hkv * ps))
+    return QUAROT_ERR_UNSUPPORTED;
   return QUAROT_OK;
 }
 // The cache's tensors and the batch's, once sizes are right and there is work.
 inline int check_cache(const void* k_q, const void* k_s, const void* v_q, const void* v_s, const void* table,
                        const void* lengths, const void* cu, int64_t max_pages) {
   if (!k_q || !k_s || !v_q || !v_s || !lengths || (!table && max_pages > 0)) return QUAROT_ERR_INVALID_ARG;
-  if (misaligned(k_q, 16) || misaligned(v_q, 16) || misaligned(k_s, 2) || misaligned(v_s, 2) || misaligned(table, 4) ||
+  if (misaligned(k_q, 16) || misaligned(v_q, 16) || misaligned(k_s, 16) || misaligned(v_s, 16) || misaligned(table, 4) ||
       misaligned(lengths, 4) || misaligned(cu, 4))
     return QUAROT_ERR_ALIGNMENT;
   return QUAROT_OK;

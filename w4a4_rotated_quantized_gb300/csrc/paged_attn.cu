@@ -85,6 +85,12 @@ __device__ __forceinline__ void tmem_st_rows2(uint32_t t, const uint32_t* r) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// Bytes (a multiple of 16, like both addresses) from global to this CTA's shared memory.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -96,10 +102,15 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 // 8 offset codes u = v + 8 of a packed word as e4m3 bytes with that bit
-// pattern, whose value is u 2^-9: even dims in lo, odd ones in hi.
-__device__ __forceinline__ void bytes_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = (w & 0x0F0F0F0Fu) ^ 0x08080808u;
-  hi = ((w >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+// pattern, whose value is u 2^-9: even dims in lo, odd ones in hi.  (w & mask)
+// ^ flip is one instruction when both constants are in registers; as literals
+// they make it two, so they come as values that the compiler does not know.
+struct Masks {
+  uint32_t mask, flip;  // 0x0F0F0F0F, 0x08080808
+};
+__device__ __forceinline__ void bytes_of(uint32_t w, Masks m, uint32_t& lo, uint32_t& hi) {
+  lo = (w & m.mask) ^ m.flip;
+  hi = ((w >> 4) & m.mask) ^ m.flip;
 }
 __device__ __forceinline__ uint32_t e4m3x2_of_h2(uint32_t h) {
   uint16_t d;
@@ -222,7 +233,7 @@ struct Cursor {
   int b, g, j, tile, tiles;  // unit (b, g, j), next of its tiles, all of them
   Seq s;
 };
-// Sums over the block: of the threads up to this one, and (returned) of all.
+// Sums over the block: of the threads up to this one, and (returned) of all.  sh: a word a warp, at most 8.
 __device__ __forceinline__ int64_t block_scan(int64_t& v, int64_t* sh) {
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
@@ -242,12 +253,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // both pos
   return (a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
 }
 // Sets the cursor to this CTA's first tile (the row of all tiles is cut into
-// equal parts, the last ones maybe none) and returns how many it has.
+// equal parts, the last ones maybe none) and returns how many it has.  sh: 10 words of shared memory.
 __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
   const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
   const bool tell = blockIdx.x == 0;
-  __shared__ int found;
-  __shared__ int64_t before;
+  int64_t &before = sh[8], &found = sh[9];
   // sequences in blocks of n, this thread's within the first one kept
   int64_t first = tid < nseq ? steps_of(p, seq_of(p, tid, tell)) * p.Hkv : 0, sum = first;
   for (int b = tid + n; b < nseq; b += n) sum += steps_of(p, seq_of(p, b, tell)) * p.Hkv;
@@ -272,7 +282,7 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
     all = block_scan(x, sh);
     if (b0 >= nseq) return 0;  // the batch changed under the call
   }
-  c.b = found;
+  c.b = int(found);
   c.s = seq_of(p, c.b, false);
   int64_t rest = at - before;
   const int64_t head = steps_of(p, c.s);
@@ -357,8 +367,9 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // it one thread issues the scores' products of the next tile and the outputs'
 // of this one.  The barrier also tells whether some thread's score passed its
 // reference; then the references are raised and the probabilities made again.
-// Loads are two tiles (keys) and one (values) ahead in registers, the page
-// numbers one more; several CTAs on an SM fill each other's waits.
+// Each warp has its own 32 tokens of the next tile copied (the keys of the one
+// after) while it works on this one; several CTAs on an SM fill each other's
+// waits.
 namespace few {
 
 constexpr int NT = 128;
@@ -372,37 +383,40 @@ struct Cfg {
   static constexpr int OFF_V = 0;                              // [128 tokens][128 bytes], swizzled
   static constexpr int OFF_Q = OFF_V + TILE * 128;             // [NC][128 bytes], swizzled
   static constexpr int OFF_P = (OFF_Q + NC * 128 + 1023) / 1024 * 1024;  // [NC / 16][128 tokens][16 bytes]
-  static constexpr int OFF_ROW = OFF_P + NC * TILE;            // per row: factor, offset, end
-  static constexpr int OFF_M = OFF_ROW + RP * 12;              // reference m of each row
-  static constexpr int OFF_X = OFF_M + RP * 4;                 // float [4][2 RP] exchange
-  static constexpr int OFF_BAR = (OFF_X + 4 * 2 * RP * 4 + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_BAR + 32 + 1024;             // + alignment slack
+  static constexpr int OFF_ROW = OFF_P + NC * TILE;            // four numbers a row
+  static constexpr int OFF_X = OFF_ROW + RP * 16;              // float [4][2 RP] exchange; at first 10 words of find_start
+  static constexpr int GROUP = 16 * D / 2;                     // bytes of 16 packed tokens
+  static constexpr int RAW = 4 * GROUP + 128;                  // a warp's keys, values, key scales and value scales
+  static constexpr int OFF_RAW = (OFF_X + 4 * 2 * RP * 4 + 127) / 128 * 128;
+  static constexpr int OFF_BAR = OFF_RAW + 4 * RAW;
+  static constexpr int SMEM = OFF_BAR + 96;
 };
 
 template <typename T, int RP, int D>
 __global__ void __launch_bounds__(NT, RP == 4 ? 5 : RP == 8 ? 4 : 3)
 few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s,
-           const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int behind) {
+           const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int behind, Masks masks) {
   using C = Cfg<RP, D>;
   constexpr int NC = C::NC, WPT = C::WPT;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t sma = smem_u32(sm);
-  float* rowf = reinterpret_cast<float*>(sm + C::OFF_ROW);
-  float* rowo = rowf + RP;
-  int* rowe = reinterpret_cast<int*>(rowo + RP);
-  float* mref = reinterpret_cast<float*>(sm + C::OFF_M);
+  // of the rows, two at a time: factor and offset of the scores, the tokens they see, reference m + 8
+  float2* rowf = reinterpret_cast<float2*>(sm + C::OFF_ROW);
+  float2* rowo = rowf + RP / 2;
+  int2* rowe = reinterpret_cast<int2*>(rowo + RP / 2);
+  float2* mtop = reinterpret_cast<float2*>(rowe + RP / 2);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint64_t* bar_o = bar_s + 1;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(bar_s + 2);
-  volatile int* gave_up = reinterpret_cast<volatile int*>(bar_s + 3);
-  __shared__ int64_t sums[NT / 32];
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(bar_s + 10);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(bar_s + 11);
+  int64_t* sums = reinterpret_cast<int64_t*>(xch);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
+    for (int w = 0; w < 8; ++w) mbar_init(bar_o + 1 + w, 1);
     *gave_up = 0;
     fence_barrier_init();
   }
@@ -427,6 +441,16 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   Cursor cur;
   int64_t left = find_start(part, cur, sums);
   uint32_t ph_s = 0, ph_o = 0;  // phases that were waited for
+  // Copies are waited for even after another wait gave up: none is in flight when the CTA ends.
+  auto wait_copy = [&](uint64_t* bar, uint32_t& phase) {
+    bool ok = mbar_try_wait(bar, phase);
+    for (int n = 0; !ok && n < kTries; ++n) ok = mbar_try_wait(bar, phase);
+    if (!ok) {
+      *gave_up = 1;
+      record_error(QUAROT_ERR_TIMEOUT);
+    }
+    phase ^= 1;
+  };
   // A wait ends after about a second (each try sleeps some microseconds), is
   // recorded, and all later ones end at once.
   auto wait = [&](uint64_t* bar, uint32_t& phase) {
@@ -441,13 +465,19 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 
   const int r4 = lane >> 2, c4 = lane & 3;
   const int shift = (bt.ps & (bt.ps - 1)) == 0 ? __ffs(bt.ps) - 1 : -1;
-  // Registers of the tiles to come: packed words of tokens 16 gi + r4 (+ 8) of
-  // the warp's 32, scales of token `lane`; whether the token is there.
-  uint32_t kw[4][WPT], vw[4][WPT];
+  // A warp copies its own 32 tokens of a tile, two groups of 16, which lie in
+  // one page each: the keys' codes, and the values' with both scales.
+  const uint32_t raw = sma + C::OFF_RAW + warp * C::RAW;
+  const uint32_t k_raw = raw, v_raw = raw + C::GROUP * 2, s_raw = v_raw + C::GROUP * 2;
+  uint64_t* bar_k = bar_o + 1 + warp;
+  uint64_t* bar_v = bar_o + 5 + warp;
+  uint32_t ph_k = 0, ph_v = 0;
+  const uint32_t frag = r4 * (D / 2) + c4 * (4 * WPT);  // this lane's words of a token
+  uint32_t v_dst[2];  // this thread's 16-byte chunks of token 32 warp + r4 in shared memory
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < WPT; ++j) kw[i][j] = vw[i][j] = 0u;
+  for (int h = 0; h < 2; ++h)
+    v_dst[h] = sma + C::OFF_V + (32 * warp + r4) * 128 + ((((WPT / 2) * c4 + h % (WPT / 2)) ^ r4) << 4);
+  const uint32_t p_dst = sma + C::OFF_P + tid * 16;
   while (left > 0) {
     // ---------------------------------------------------------------- a unit's tiles
     const int t_lo = cur.s.tile0 + cur.tile;
@@ -455,62 +485,67 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
     const int lo = part.prefix ? 0 : part.shared, hi = cur.s.len;  // tokens of this part
     const int32_t* table = bt.table + int64_t(part.prefix ? 0 : cur.b) * bt.max_pages;
 
-    // Rows of the pages that groups of 16 tokens lie in: in [gi], the first
-    // token's row of [n_pages, Hkv, ps], or -1 (out of this part, or no page).
-    auto pages = [&](int tile, int* page) {
-#pragma unroll
-      for (int gi = 0; gi < 2; ++gi) {
-        const int tb = tile * TILE + 32 * warp + 16 * gi;
-        const int index = shift >= 0 ? tb >> shift : tb / bt.ps;
-        page[gi] = tb < hi && tb + 16 > lo && tile < t_lo + nt ? (index < bt.max_pages ? __ldcg(table + index) : -1) : -2;
+    // A lane looks after its token's group of 16 tokens: the group's page, then
+    // its first row in the cache in units of 16 rows, -1 where the part has no
+    // token in it (or the table no page).
+    const int last = t_lo + nt;
+    auto page_of = [&](int tile) -> int {
+      const int tb = tile * TILE + (tid & ~15);
+      const int index = shift >= 0 ? tb >> shift : tb / bt.ps;
+      return tb < hi && tb + 16 > lo && tile < last ? (index < bt.max_pages ? __ldcg(table + index) : -1) : -2;
+    };
+    auto row_of_page = [&](int tile, int page) -> int {
+      const int tb = tile * TILE + (tid & ~15);
+      const int off = (shift >= 0 ? tb & (bt.ps - 1) : tb % bt.ps) >> 4;
+      if (unsigned(page) < unsigned(bt.n_pages)) return (page * part.Hkv + cur.g) * (bt.ps >> 4) + off;
+      if (page != -2) record_error(QUAROT_ERR_INVALID_ARG);
+      return -1;
+    };
+    auto copy_keys = [&](int row16) {
+      const int row = __shfl_sync(0xffffffffu, row16, 16 * (lane & 1));
+      const unsigned there = __ballot_sync(0xffffffffu, row16 >= 0);
+      if (lane == 0) {
+        to_async_proxy();
+        mbar_arrive_expect_tx(bar_k, ((there & 1) + (there >> 31)) * C::GROUP);
+      }
+      __syncwarp();
+      if (lane < 2 && row >= 0) bulk_copy(k_raw + lane * C::GROUP, k_q + int64_t(row) * C::GROUP, C::GROUP, bar_k);
+    };
+    auto copy_values = [&](int row16) {
+      const int row = __shfl_sync(0xffffffffu, row16, 16 * (lane & 1));
+      const unsigned there = __ballot_sync(0xffffffffu, row16 >= 0);
+      if (lane == 0) {
+        to_async_proxy();
+        mbar_arrive_expect_tx(bar_v, ((there & 1) + (there >> 31)) * (C::GROUP + 64));
+      }
+      __syncwarp();
+      if (row >= 0) {
+        if (lane < 2) bulk_copy(v_raw + lane * C::GROUP, v_q + int64_t(row) * C::GROUP, C::GROUP, bar_v);
+        else if (lane < 6) bulk_copy(s_raw + (lane - 2) * 32, (lane < 4 ? k_s : v_s) + int64_t(row) * 16, 32, bar_v);
       }
     };
-    auto rows = [&](int tile, const int* page, int64_t* at) {
+    auto words = [&](uint32_t from, uint32_t (*w)[WPT]) {
 #pragma unroll
-      for (int gi = 0; gi < 2; ++gi) {
-        const int tb = tile * TILE + 32 * warp + 16 * gi;
-        const int off = shift >= 0 ? tb & (bt.ps - 1) : tb % bt.ps;
-        const bool ok = unsigned(page[gi]) < unsigned(bt.n_pages);
-        if (!ok && page[gi] != -2) record_error(QUAROT_ERR_INVALID_ARG);
-        at[gi] = ok ? (int64_t(page[gi]) * part.Hkv + cur.g) * bt.ps + off : -1;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = from + frag + 8 * (D / 2) * i;
+        if constexpr (WPT == 4)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "r"(at));
+        else
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at));
       }
-    };
-    auto load = [&](uint32_t (*w)[WPT], const uint8_t* src, const int64_t* at) {
-#pragma unroll
-      for (int gi = 0; gi < 2; ++gi)
-        if (at[gi] >= 0) {
-          const uint8_t* p = src + (at[gi] + r4) * (D / 2) + c4 * (4 * WPT);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if constexpr (WPT == 4) {
-              const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p + 8 * h * (D / 2)));
-              w[2 * gi + h][0] = a.x, w[2 * gi + h][1] = a.y, w[2 * gi + h][2] = a.z, w[2 * gi + h][3] = a.w;
-            } else {
-              const uint2 a = __ldcg(reinterpret_cast<const uint2*>(p + 8 * h * (D / 2)));
-              w[2 * gi + h][0] = a.x, w[2 * gi + h][1] = a.y;
-            }
-          }
-        }
-    };
-    // Scales of this thread's token, both 0 where it is not one of this part.
-    auto load_scales = [&](int tile, const int64_t* at) -> uint32_t {
-      const int tok = tile * TILE + tid;
-      const int64_t row = lane < 16 ? at[0] : at[1];
-      uint32_t v = 0xFFFF0000u;  // no token: the value scale's place holds a NaN, which no token's does
-      if (row >= 0 && tok >= lo && tok < hi)
-        v = __ldcg(reinterpret_cast<const unsigned short*>(k_s) + row + (lane & 15)) |
-            uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(v_s) + row + (lane & 15))) << 16;
-      return v;
     };
     // the keys of a tile, from registers to tensor memory
     auto put_keys = [&]() {
+      uint32_t kw[4][WPT];
+      wait_copy(bar_k, ph_k);
+      words(k_raw, kw);
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
         uint32_t a[4 * WPT];
 #pragma unroll
         for (int j = 0; j < WPT; ++j) {
-          bytes_of(kw[2 * gi][j], a[4 * j], a[4 * j + 1]);
-          bytes_of(kw[2 * gi + 1][j], a[4 * j + 2], a[4 * j + 3]);
+          bytes_of(kw[2 * gi][j], masks, a[4 * j], a[4 * j + 1]);
+          bytes_of(kw[2 * gi + 1][j], masks, a[4 * j + 2], a[4 * j + 3]);
         }
         if constexpr (WPT == 4) tmem_st_rows4(tm_k + quad + (uint32_t(16 * gi) << 16), a);
         else tmem_st_rows2(tm_k + quad + (uint32_t(16 * gi) << 16), a);
@@ -523,15 +558,11 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
       mma_commit(bar_s);
     };
 
-    // tile t_lo: keys and values; pages of the next
-    int64_t at[2], at_n[2];
-    int pg[2];
-    pages(t_lo, pg);
-    rows(t_lo, pg, at);
-    load(kw, k_q, at);
-    load(vw, v_q, at);
-    uint32_t sc = load_scales(t_lo, at), sc_n = 0;
-    pages(t_lo + 1, pg);
+    // tile t_lo: keys and values; the next one's page
+    int row = row_of_page(t_lo, page_of(t_lo)), row_n, row_k = -1;  // of the tile, the next, the one after
+    copy_keys(row);
+    copy_values(row);
+    int page = page_of(t_lo + 1);
     // ---- the rows' queries: a warp takes rows warp, warp + 4, ...; lane l
     // holds dims E l .. E l + E - 1, E = d / 32
     {
@@ -611,10 +642,10 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
           }
         }
         if (lane == 0) {
-          rowf[r] = 2.0f * amax * qscale;       // 2^9 of the codes, 1 / 256 of the pieces
-          rowo[r] = sum * (8.0f / 512.0f);
-          rowe[r] = row.end;
-          mref[r] = kNone;
+          reinterpret_cast<float*>(rowf)[r] = 2.0f * amax * qscale;  // 2^9 of the codes, 1 / 256 of the pieces
+          reinterpret_cast<float*>(rowo)[r] = sum * (-8.0f / 512.0f);
+          reinterpret_cast<int*>(rowe)[r] = row.end;
+          reinterpret_cast<float*>(mtop)[r] = kNone;
         }
       }
     }
@@ -624,98 +655,103 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
     put_keys();
     tc_wait_st();
     tc_before();
-    rows(t_lo + 1, pg, at_n);
-    load(kw, k_q, at_n);
-    sc_n = load_scales(t_lo + 1, at_n);
-    pages(t_lo + 2, pg);
+    row_n = row_of_page(t_lo + 1, page);
+    if (nt > 1) copy_keys(row_n);
+    page = page_of(t_lo + 2);
     __syncthreads();
     if (tid == 0) {
       tc_after();
       issue_scores();
     }
 
-    float l[RP], z[RP];
+    float2 l[RP / 2], z[RP / 2];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) l[r] = z[r] = 0.f;
+    for (int r = 0; r < RP / 2; ++r) l[r] = z[r] = make_float2(0.f, 0.f);
 
     for (int it = 0; it < nt; ++it) {
       // ---- the next tile's keys to tensor memory, once this one's scores are there
       wait(bar_s, ph_s);
       tc_after();
-      uint32_t v[NC];
-#pragma unroll
-      for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
-      if (it + 1 < nt) put_keys();
+      if (it + 1 < nt) {
+        put_keys();
+        if (it + 2 < nt) {
+          row_k = row_of_page(t_lo + it + 2, page);
+          copy_keys(row_k);
+          page = page_of(t_lo + it + 3);
+        }
+      }
       // ---- values to shared memory, once the products of the tile before have read theirs
+      uint32_t vw[4][WPT];
+      wait_copy(bar_v, ph_v);
+      words(v_raw, vw);
+      uint32_t k_half, v_half;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(k_half) : "r"(s_raw + 2 * lane));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v_half) : "r"(s_raw + 64 + 2 * lane));
+      const bool absent = row < 0 || (t_lo + it) * TILE + tid < lo || (t_lo + it) * TILE + tid >= hi;
+      if (it + 1 < nt) {
+        copy_values(row_n);
+        row = row_n;
+        row_n = row_k;
+      }
       if (it > 0) wait(bar_o, ph_o);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 32 * warp + 8 * i + r4;
         uint32_t b[2 * WPT];
 #pragma unroll
-        for (int j = 0; j < WPT; ++j) bytes_of(vw[i][j], b[2 * j], b[2 * j + 1]);
+        for (int j = 0; j < WPT; ++j) bytes_of(vw[i][j], masks, b[2 * j], b[2 * j + 1]);
 #pragma unroll
-        for (int h = 0; h < WPT / 2; ++h) {
-          const uint32_t chunk = uint32_t(WPT / 2 * c4 + h);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_V + t * 128 + ((chunk ^ (t & 7)) << 4)),
-                       "r"(b[4 * h]), "r"(b[4 * h + 1]), "r"(b[4 * h + 2]), "r"(b[4 * h + 3])
+        for (int h = 0; h < WPT / 2; ++h)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v_dst[h] + 1024u * i), "r"(b[4 * h]), "r"(b[4 * h + 1]),
+                       "r"(b[4 * h + 2]), "r"(b[4 * h + 3])
                        : "memory");
-        }
       }
-      // ---- loads ahead: values of the next tile, keys and scales of the one after
-      const uint32_t sc0 = sc;
-      if (it + 1 < nt) {
-        load(vw, v_q, at_n);
-        sc = sc_n;
-        if (it + 2 < nt) {
-          rows(t_lo + it + 2, pg, at_n);
-          load(kw, k_q, at_n);
-          sc_n = load_scales(t_lo + it + 2, at_n);
-          pages(t_lo + it + 3, pg);
-        }
-      }
-
-      // ---- scores of this thread's token
-      const float2 scales = h2_to_f2(sc0);
-      const float ksf = scales.x, vsf = sc0 == 0xFFFF0000u ? 0.f : scales.y;
-      const int tok = sc0 == 0xFFFF0000u ? 0x7fffffff : (t_lo + it) * TILE + tid;
-      const float lv = lg2(fmaxf(vsf, 5.9604645e-8f));
+      // ---- scores of this thread's token, two rows at a time
+      uint32_t v[NC];
+#pragma unroll
+      for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
+      const float2 scales = make_float2(__half2float(__ushort_as_half(uint16_t(k_half))),
+                                        absent ? 0.f : __half2float(__ushort_as_half(uint16_t(v_half))));
+      const float lv = lg2(fmaxf(scales.y, 5.9604645e-8f));
+      const int tok = absent ? 0x7fffffff : (t_lo + it) * TILE + tid;
       tc_wait_ld();
-      float s[RP];
+      float2 s[RP / 2];
       bool above = false;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float x = fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])) +
-                        fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f, -rowo[r]);
-        s[r] = tok < rowe[r] ? x * (rowf[r] * ksf) : -INFINITY;
-        above |= s[r] + lv > mref[r] + 8.0f;
+      for (int r = 0; r < RP / 2; ++r) {
+        auto two = [&](int c) { return make_float2(__uint_as_float(v[c + 2 * r]), __uint_as_float(v[c + 2 * r + 1])); };
+        const float2 f = rowf[r], o = rowo[r];
+        const float2 x = __fadd2_rn(__ffma2_rn(two(RP), make_float2(0.0625f, 0.0625f), two(0)),
+                                    __ffma2_rn(two(2 * RP), make_float2(0.00390625f, 0.00390625f), o));
+        s[r] = __fmul2_rn(x, __fmul2_rn(f, make_float2(scales.x, scales.x)));
+        const int2 end = rowe[r];
+        if (tok >= end.x) s[r].x = -INFINITY;
+        if (tok >= end.y) s[r].y = -INFINITY;
+        const float2 y = __fadd2_rn(s[r], make_float2(lv, lv)), m = mtop[r];  // mtop = mref + 8
+        above |= y.x > m.x || y.y > m.y;
       }
-      float p[RP], w[RP];
+      float2 p[RP / 2], w[RP / 2];
       auto probabilities = [&]() {
         uint32_t pw[3][RP / 4];
 #pragma unroll
-        for (int r = 0; r < RP; r += 4) {
+        for (int r = 0; r < RP / 2; r += 2) {
           uint32_t c[2][3];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int rr = r + 2 * h + e;
-              w[rr] = ex2(s[rr] - mref[rr]);
-              p[rr] = w[rr] * vsf;
-            }
-            pieces_of(h2_of_f2(p[r + 2 * h], p[r + 2 * h + 1]), c[h]);
+            const float2 m = mtop[r + h], y = __fadd2_rn(s[r + h], make_float2(8.0f - m.x, 8.0f - m.y));
+            w[r + h] = make_float2(ex2(y.x), ex2(y.y));
+            p[r + h] = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
+            pieces_of(h2_of_f2(p[r + h].x, p[r + h].y), c[h]);
           }
 #pragma unroll
-          for (int k = 0; k < 3; ++k) pw[k][r / 4] = c[0][k] | (c[1][k] << 16);
+          for (int k = 0; k < 3; ++k) pw[k][r / 2] = c[0][k] | (c[1][k] << 16);
         }
         uint32_t words[NC / 4];
 #pragma unroll
         for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
 #pragma unroll
         for (int i = 0; i < NC / 16; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sma + C::OFF_P + i * (16 * TILE) + tid * 16),
-                       "r"(words[4 * i]), "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_dst + 16u * TILE * i), "r"(words[4 * i]),
+                       "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
                        : "memory");
         to_async_proxy();
       };
@@ -724,9 +760,10 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
       tc_before();
       if (__syncthreads_or(above)) {
         // ---- raise the references that some score exceeds; sums and outputs so far follow
+        float* mt = reinterpret_cast<float*>(mtop);
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          float x = s[r] + lv;
+          float x = (r & 1 ? s[r / 2].y : s[r / 2].x) + lv;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
           if (lane == 0) xch[warp * RP + r] = x;
@@ -735,10 +772,10 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
         float al[RP];
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          const float mo = mref[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
-          al[r] = x > mo + 8.0f ? ex2(mo - x) : 1.0f;
-          l[r] *= al[r];
-          z[r] *= al[r];
+          const float mo = mt[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
+          al[r] = x > mo ? ex2(mo - 8.0f - x) : 1.0f;
+          (r & 1 ? l[r / 2].y : l[r / 2].x) *= al[r];
+          (r & 1 ? z[r / 2].y : z[r / 2].x) *= al[r];
         }
         if (it > 0) {
           uint32_t o[NC];
@@ -756,8 +793,8 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
         }
         __syncthreads();
         if (tid < RP) {
-          const float mo = mref[tid], x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
-          if (x > mo + 8.0f) mref[tid] = x;
+          const float x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
+          if (x > mt[tid]) mt[tid] = x + 8.0f;
         }
         __syncthreads();
         probabilities();
@@ -774,23 +811,24 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
         mma_commit(bar_o);
       }
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        l[r] += w[r];
-        z[r] += p[r];
+      for (int r = 0; r < RP / 2; ++r) {
+        l[r] = __fadd2_rn(l[r], w[r]);
+        z[r] = __fadd2_rn(z[r], p[r]);
       }
     }
 
     // ---------------------------------------------------------------- the unit's state
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
+      float lr = r & 1 ? l[r / 2].y : l[r / 2].x, zr = r & 1 ? z[r / 2].y : z[r / 2].x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
+        lr += __shfl_xor_sync(0xffffffffu, lr, o);
+        zr += __shfl_xor_sync(0xffffffffu, zr, o);
       }
       if (lane == 0) {
-        xch[warp * 2 * RP + r] = l[r];
-        xch[warp * 2 * RP + RP + r] = z[r];
+        xch[warp * 2 * RP + r] = lr;
+        xch[warp * 2 * RP + RP + r] = zr;
       }
     }
     __syncthreads();
@@ -813,7 +851,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
     }
     if (tid < RP) {
       const float ll = (xch[tid] + xch[2 * RP + tid]) + (xch[4 * RP + tid] + xch[6 * RP + tid]);
-      *reinterpret_cast<float2*>(ws.ml + (dst + tid) * 2) = make_float2(mref[tid], ll);
+      *reinterpret_cast<float2*>(ws.ml + (dst + tid) * 2) = make_float2(reinterpret_cast<float*>(mtop)[tid] - 8.0f, ll);
     }
     if (tid == 0) {
       if (cur.tile == 0) ws.span[2 * unit] = blockIdx.x;
@@ -970,7 +1008,7 @@ static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half*
     auto go = [&](auto kern, size_t smem, AttrCache& attr) {
       if (!smem_attr_once(kern, int(smem), attr)) return int(QUAROT_ERR_LAUNCH);
       return fp8::launch_dependent(kern, dim3(unsigned(plan.ctas)), few::NT, smem, 1, st, q, ld_q, k_q, k_s, v_q, v_s, part,
-                                   qscale, ws, behind);
+                                   qscale, ws, behind, Masks{0x0F0F0F0Fu, 0x08080808u});
     };
     static AttrCache attr[3];
     if (plan.RP == 4) return go(few::few_kernel<T, 4, D>, few::Cfg<4, D>::SMEM, attr[0]);
