@@ -85,6 +85,12 @@ __device__ __forceinline__ void tmem_st_rows2(uint32_t t, const uint32_t* r) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// One lane of a converged warp, in the form in which the compiler sees that it is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // Bytes (a multiple of 16, like both addresses) from global to this CTA's shared memory.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -212,6 +218,7 @@ struct Space {
   int* span;  // [units, 2]
   float* ml;
   float* o;
+  int ctas;
 };
 constexpr size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 inline size_t space_bytes(int64_t units, int64_t ctas, int64_t RP, int64_t d) {
@@ -225,6 +232,7 @@ inline Space space_at(unsigned char* p, int64_t units, int64_t ctas, int64_t RP)
   s.ml = reinterpret_cast<float*>(p);
   p += round256(size_t(units + ctas) * RP * 8);
   s.o = reinterpret_cast<float*>(p);
+  s.ctas = int(ctas);
   return s;
 }
 
@@ -252,8 +260,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t& v, int64_t* sh) {
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // both positive
   return (a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
 }
+// A cursor from thread 0 to all, through 16 ints of shared memory: whatever the
+// batch's arrays do meanwhile, the threads of a CTA agree on its tiles.
+__device__ __forceinline__ void tell_cursor(const Cursor& c, int* sh) {
+  const int v[10] = {c.b, c.g, c.j, c.tile, c.tiles, c.s.tok0, c.s.rows, c.s.first, c.s.len, c.s.tile0};
+#pragma unroll
+  for (int i = 0; i < 10; ++i) sh[i] = v[i];
+}
+__device__ __forceinline__ Cursor told_cursor(const int* sh) {
+  return {sh[0], sh[1], sh[2], sh[3], sh[4], {sh[5], sh[6], sh[7], sh[8], sh[9]}};
+}
 // Sets the cursor to this CTA's first tile (the row of all tiles is cut into
-// equal parts, the last ones maybe none) and returns how many it has.  sh: 10 words of shared memory.
+// equal parts, the last ones maybe none) and returns how many it has.  sh: 18 words of shared memory.
 __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
   const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
   const bool tell = blockIdx.x == 0;
@@ -282,25 +300,35 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
     all = block_scan(x, sh);
     if (b0 >= nseq) return 0;  // the batch changed under the call
   }
-  c.b = int(found);
-  c.s = seq_of(p, c.b, false);
-  int64_t rest = at - before;
-  const int64_t head = steps_of(p, c.s);
-  c.g = int(quotient(rest, head));
-  rest -= c.g * head;
-  c.j = 0;
-  if (p.prefix) {
-    c.tiles = tiles_of(p, c.s, 0);
-    c.j = int(quotient(rest, c.tiles));
-    rest -= int64_t(c.j) * c.tiles;
-  } else {
-    while (rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
-      rest -= c.tiles;
-      ++c.j;
+  if (tid == 0) {
+    c.b = int(found);
+    c.s = seq_of(p, c.b, false);
+    int64_t rest = at - before;
+    const int64_t head = steps_of(p, c.s);
+    c.tile = c.tiles = c.j = c.g = 0;
+    if (head > 0) {  // as it was, unless the batch changes under the call
+      c.g = int(min(quotient(rest, head), int64_t(p.Hkv - 1)));
+      rest -= c.g * head;
+      const int J = (c.s.rows + p.RP - 1) / p.RP;
+      if (p.prefix) {
+        c.tiles = tiles_of(p, c.s, 0);
+        c.j = int(quotient(rest, c.tiles));
+        rest -= int64_t(c.j) * c.tiles;
+      } else {
+        while (c.j < J && rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
+          rest -= c.tiles;
+          ++c.j;
+        }
+      }
+      if (c.j >= J) c.j = J - 1;
+      c.tile = int(min(rest, int64_t(c.tiles > 0 ? c.tiles - 1 : 0)));
     }
+    tell_cursor(c, reinterpret_cast<int*>(sh + 10));
   }
-  c.tile = int(rest);
-  return min(per, total - at);
+  __syncthreads();
+  c = told_cursor(reinterpret_cast<int*>(sh + 10));
+  __syncthreads();
+  return c.tiles > 0 ? min(per, total - at) : 0;
 }
 // The next unit that has tiles; without one (the batch changed under the call) c.tiles is 0.
 __device__ __forceinline__ void next_unit(const Part& p, Cursor& c) {
@@ -363,16 +391,18 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // exceeds it by 8, so p' <= 2^8 and the largest is at least 1 (fp16, then its
 // pieces, hold it to 2^-12).  Sums of 2^(s - m) and of p' stay in fp32.
 //
-// A CTA is four warps that do it all in turn, with one barrier a tile: behind
-// it one thread issues the scores' products of the next tile and the outputs'
-// of this one.  The barrier also tells whether some thread's score passed its
+// A CTA is four warps that unpack and do the softmax, and a fifth that feeds
+// them: it looks up the pages, has the packed tiles copied to shared memory two
+// ahead (contiguous pages, or parts of one, in one copy), and issues the MMAs.
+// There is one barrier a tile: behind it the fifth warp issues the scores'
+// products of the next tile and the outputs' of this one, and copies over what
+// was read.  The barrier also tells whether some thread's score passed its
 // reference; then the references are raised and the probabilities made again.
-// Each warp has its own 32 tokens of the next tile copied (the keys of the one
-// after) while it works on this one; several CTAs on an SM fill each other's
-// waits.
+// Several CTAs on an SM fill each other's waits.
 namespace few {
 
-constexpr int NT = 128;
+constexpr int NT = 160;
+constexpr int FEED = 4;  // the feeding warp
 
 template <int RP, int D>
 struct Cfg {
@@ -380,22 +410,29 @@ struct Cfg {
   static constexpr int KC = D / 4;                             // tensor-memory columns of a key
   static constexpr uint32_t COLS = KC + 2 * NC <= 64 ? 64 : 128;
   static constexpr int WPT = D / 32;                           // packed words a thread has of a token
+  static constexpr int CODES = TILE * D / 2;                   // packed codes of a tile
+  static constexpr int STAGE_V = CODES + 2 * TILE * 2;         // with key scales and value scales
   static constexpr int OFF_V = 0;                              // [128 tokens][128 bytes], swizzled
   static constexpr int OFF_Q = OFF_V + TILE * 128;             // [NC][128 bytes], swizzled
   static constexpr int OFF_P = (OFF_Q + NC * 128 + 1023) / 1024 * 1024;  // [NC / 16][128 tokens][16 bytes]
-  static constexpr int OFF_ROW = OFF_P + NC * TILE;            // four numbers a row
-  static constexpr int OFF_X = OFF_ROW + RP * 16;              // float [4][2 RP] exchange; at first 10 words of find_start
-  static constexpr int GROUP = 16 * D / 2;                     // bytes of 16 packed tokens
-  static constexpr int RAW = 4 * GROUP + 128;                  // a warp's keys, values, key scales and value scales
-  static constexpr int OFF_RAW = (OFF_X + 4 * 2 * RP * 4 + 127) / 128 * 128;
-  static constexpr int OFF_BAR = OFF_RAW + 4 * RAW;
-  static constexpr int SMEM = OFF_BAR + 96;
+  static constexpr int OFF_RK = OFF_P + NC * TILE;             // packed keys, two tiles
+  static constexpr int OFF_RV = OFF_RK + 2 * CODES;            // packed values and scales, two tiles
+  static constexpr int OFF_ROW = OFF_RV + 2 * STAGE_V;         // four numbers a row
+  static constexpr int OFF_X = OFF_ROW + RP * 16;              // float [4][2 RP] exchange
+  static constexpr int OFF_CUR = OFF_X + 4 * 2 * RP * 4;       // the next cursor; find_start's words begin 80 bytes before
+  static constexpr int OFF_BAR = OFF_CUR + 64;
+  static constexpr int SMEM = OFF_BAR + 80;
 };
+template <int RP>
+constexpr int ctas_per_sm() {
+  return RP == 4 ? 4 : RP == 8 ? 3 : 2;
+}
 
 template <typename T, int RP, int D>
-__global__ void __launch_bounds__(NT, RP == 4 ? 5 : RP == 8 ? 4 : 3)
+__global__ void __launch_bounds__(NT, ctas_per_sm<RP>())
 few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s,
-           const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int behind, Masks masks) {
+           const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int behind,
+           Masks masks) {
   using C = Cfg<RP, D>;
   constexpr int NC = C::NC, WPT = C::WPT;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -406,21 +443,22 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   int2* rowe = reinterpret_cast<int2*>(rowo + RP / 2);
   float2* mtop = reinterpret_cast<float2*>(rowe + RP / 2);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
+  int* next = reinterpret_cast<int*>(sm + C::OFF_CUR);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint64_t* bar_o = bar_s + 1;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(bar_s + 10);
-  volatile int* gave_up = reinterpret_cast<volatile int*>(bar_s + 11);
-  int64_t* sums = reinterpret_cast<int64_t*>(xch);
+  uint64_t* bar_k = bar_s + 2;  // [2]
+  uint64_t* bar_v = bar_s + 4;  // [2]
+  volatile int* there = reinterpret_cast<volatile int*>(bar_s + 6);  // [2]: which groups of 16 tokens a tile has
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(bar_s + 7);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(bar_s + 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    mbar_init(bar_s, 1);
-    mbar_init(bar_o, 1);
-    for (int w = 0; w < 8; ++w) mbar_init(bar_o + 1 + w, 1);
+    for (int i = 0; i < 6; ++i) mbar_init(bar_s + i, 1);
     *gave_up = 0;
     fence_barrier_init();
   }
-  if (warp == 0) {
+  if (warp == FEED) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(const_cast<uint32_t*>(slot))),
                  "r"(C::COLS)
                  : "memory");
@@ -436,95 +474,153 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   fp8::next_may_start();
 
   const uint32_t tm_k = tmem, tm_s = tmem + C::KC, tm_o = tm_s + NC;
-  const uint32_t quad = uint32_t(32 * warp) << 16;
   const Batch& bt = part.t;
   Cursor cur;
-  int64_t left = find_start(part, cur, sums);
-  uint32_t ph_s = 0, ph_o = 0;  // phases that were waited for
-  // Copies are waited for even after another wait gave up: none is in flight when the CTA ends.
-  auto wait_copy = [&](uint64_t* bar, uint32_t& phase) {
+  int64_t left = find_start(part, cur, reinterpret_cast<int64_t*>(sm + C::OFF_CUR - 80));
+  // A wait ends after about a second (each try sleeps some microseconds) and is
+  // recorded.  Once one gave up, waits for MMAs end at once; copies are waited
+  // for all the same, so that none is in flight when the CTA ends.
+  auto wait = [&](uint64_t* bar, uint32_t phase, bool copy) {
     bool ok = mbar_try_wait(bar, phase);
-    for (int n = 0; !ok && n < kTries; ++n) ok = mbar_try_wait(bar, phase);
+    for (int n = 0; !ok && n < kTries && (copy || !*gave_up); ++n) ok = mbar_try_wait(bar, phase);
     if (!ok) {
       *gave_up = 1;
       record_error(QUAROT_ERR_TIMEOUT);
     }
-    phase ^= 1;
-  };
-  // A wait ends after about a second (each try sleeps some microseconds), is
-  // recorded, and all later ones end at once.
-  auto wait = [&](uint64_t* bar, uint32_t& phase) {
-    bool ok = mbar_try_wait(bar, phase);
-    for (int n = 0; !ok && n < kTries && !*gave_up; ++n) ok = mbar_try_wait(bar, phase);
-    if (!ok) {
-      *gave_up = 1;
-      record_error(QUAROT_ERR_TIMEOUT);
-    }
-    phase ^= 1;
   };
 
-  const int r4 = lane >> 2, c4 = lane & 3;
-  const int shift = (bt.ps & (bt.ps - 1)) == 0 ? __ffs(bt.ps) - 1 : -1;
-  // A warp copies its own 32 tokens of a tile, two groups of 16, which lie in
-  // one page each: the keys' codes, and the values' with both scales.
-  const uint32_t raw = sma + C::OFF_RAW + warp * C::RAW;
-  const uint32_t k_raw = raw, v_raw = raw + C::GROUP * 2, s_raw = v_raw + C::GROUP * 2;
-  uint64_t* bar_k = bar_o + 1 + warp;
-  uint64_t* bar_v = bar_o + 5 + warp;
-  uint32_t ph_k = 0, ph_v = 0;
-  const uint32_t frag = r4 * (D / 2) + c4 * (4 * WPT);  // this lane's words of a token
-  uint32_t v_dst[2];  // this thread's 16-byte chunks of token 32 warp + r4 in shared memory
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    v_dst[h] = sma + C::OFF_V + (32 * warp + r4) * 128 + ((((WPT / 2) * c4 + h % (WPT / 2)) ^ r4) << 4);
-  const uint32_t p_dst = sma + C::OFF_P + tid * 16;
-  while (left > 0) {
-    // ---------------------------------------------------------------- a unit's tiles
-    const int t_lo = cur.s.tile0 + cur.tile;
-    const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
-    const int lo = part.prefix ? 0 : part.shared, hi = cur.s.len;  // tokens of this part
-    const int32_t* table = bt.table + int64_t(part.prefix ? 0 : cur.b) * bt.max_pages;
-
-    // A lane looks after its token's group of 16 tokens: the group's page, then
-    // its first row in the cache in units of 16 rows, -1 where the part has no
-    // token in it (or the table no page).
-    const int last = t_lo + nt;
-    auto page_of = [&](int tile) -> int {
-      const int tb = tile * TILE + (tid & ~15);
+  if (warp == FEED) {
+    // ================================================================ feeder
+    const int shift = (bt.ps & (bt.ps - 1)) == 0 ? __ffs(bt.ps) - 1 : -1;
+    const int lo = part.prefix ? 0 : part.shared;
+    const int rows_of_page = part.Hkv * (bt.ps >> 4);
+    Cursor f = cur;
+    int64_t ahead = left;  // tiles not looked up yet
+    int page = -2, off = 0;
+    // lane l < 8: page of the next tile's group l of 16 tokens, and the group's place in it in units of 16 rows
+    auto look = [&]() {
+      page = -2;
+      if (ahead <= 0) return;
+      --ahead;
+      if (f.tiles == 0) return;
+      const int tb = (f.s.tile0 + f.tile) * TILE + 16 * (lane & 7);
       const int index = shift >= 0 ? tb >> shift : tb / bt.ps;
-      return tb < hi && tb + 16 > lo && tile < last ? (index < bt.max_pages ? __ldcg(table + index) : -1) : -2;
+      off = f.g * (bt.ps >> 4) + ((tb - index * bt.ps) >> 4);
+      if (lane < 8 && tb < f.s.len && tb + 16 > lo)
+        page = index < bt.max_pages ? __ldcg(bt.table + int64_t(part.prefix ? 0 : f.b) * bt.max_pages + index) : -1;
+      if (++f.tile == f.tiles && ahead > 0) next_unit(part, f);
     };
-    auto row_of_page = [&](int tile, int page) -> int {
-      const int tb = tile * TILE + (tid & ~15);
-      const int off = (shift >= 0 ? tb & (bt.ps - 1) : tb % bt.ps) >> 4;
-      if (unsigned(page) < unsigned(bt.n_pages)) return (page * part.Hkv + cur.g) * (bt.ps >> 4) + off;
-      if (page != -2) record_error(QUAROT_ERR_INVALID_ARG);
-      return -1;
+    auto take = [&]() -> int {  // that group's first row, -1: none
+      int row = -1;
+      if (unsigned(page) < unsigned(bt.n_pages)) row = page * rows_of_page + off;
+      else if (page != -2) record_error(QUAROT_ERR_INVALID_ARG);
+      look();
+      return row;
     };
-    auto copy_keys = [&](int row16) {
-      const int row = __shfl_sync(0xffffffffu, row16, 16 * (lane & 1));
-      const unsigned there = __ballot_sync(0xffffffffu, row16 >= 0);
-      if (lane == 0) {
-        to_async_proxy();
-        mbar_arrive_expect_tx(bar_k, ((there & 1) + (there >> 31)) * C::GROUP);
+    int rows[2] = {-1, -1};  // of the latest two tiles
+    uint32_t nk = 0, nv = 0;
+    const int64_t total = left;
+    auto copy = [&](bool keys, int row) {
+      const uint32_t n = keys ? nk : nv, st = n & 1;
+      const unsigned valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFF;
+      const int before = __shfl_up_sync(0xffffffffu, row, 1);
+      unsigned starts = __ballot_sync(0xffffffffu, row >= 0 && (lane == 0 || before < 0 || row != before + 1)) & 0xFF;
+      const unsigned ends = (starts | ~valid) & 0x1FF;
+      uint64_t* bar = (keys ? bar_k : bar_v) + st;
+      const uint32_t to = sma + (keys ? C::OFF_RK + st * C::CODES : C::OFF_RV + st * C::STAGE_V);
+      constexpr uint32_t GROUP = 16 * D / 2;
+      if (elect_one()) {
+        if (!keys) there[st] = int(valid);
+        mbar_arrive_expect_tx(bar, __popc(valid) * (GROUP + (keys ? 0 : 64)));
+      }
+      while (starts) {
+        const int a = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const int len = __ffs(ends >> (a + 1));
+        const int64_t r = __shfl_sync(0xffffffffu, row, a);
+        if (elect_one()) {
+          bulk_copy(to + a * GROUP, (keys ? k_q : v_q) + r * GROUP, len * GROUP, bar);
+          if (!keys) {
+            bulk_copy(to + C::CODES + a * 32, k_s + r * 16, len * 32, bar);
+            bulk_copy(to + C::CODES + 2 * TILE + a * 32, v_s + r * 16, len * 32, bar);
+          }
+        }
       }
       __syncwarp();
-      if (lane < 2 && row >= 0) bulk_copy(k_raw + lane * C::GROUP, k_q + int64_t(row) * C::GROUP, C::GROUP, bar_k);
     };
-    auto copy_values = [&](int row16) {
-      const int row = __shfl_sync(0xffffffffu, row16, 16 * (lane & 1));
-      const unsigned there = __ballot_sync(0xffffffffu, row16 >= 0);
-      if (lane == 0) {
-        to_async_proxy();
-        mbar_arrive_expect_tx(bar_v, ((there & 1) + (there >> 31)) * (C::GROUP + 64));
-      }
+    auto feed_keys = [&]() {
+      if (nk >= total) return;
+      const int row = take();
+      rows[0] = rows[1];
+      rows[1] = row;
+      copy(true, row);
+      ++nk;
+    };
+    auto feed_values = [&]() {
+      if (nv >= total) return;
+      copy(false, nk == nv + 1 ? rows[1] : rows[0]);
+      ++nv;
+    };
+    auto issue_scores = [&]() {
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk)
+        mma8_ts(tm_s, tm_k + 8 * kk, desc_sw128(sma + C::OFF_Q + 32 * kk, 1024), idesc8(NC, false, false), kk > 0);
+      mma_commit(bar_s);
+    };
+    look();
+    feed_keys();
+    feed_values();
+    feed_keys();
+    feed_values();
+    while (left > 0) {
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      __syncthreads();  // the queries and the first keys are there
+      tc_after();
+      if (elect_one()) issue_scores();
       __syncwarp();
-      if (row >= 0) {
-        if (lane < 2) bulk_copy(v_raw + lane * C::GROUP, v_q + int64_t(row) * C::GROUP, C::GROUP, bar_v);
-        else if (lane < 6) bulk_copy(s_raw + (lane - 2) * 32, (lane < 4 ? k_s : v_s) + int64_t(row) * 16, 32, bar_v);
+      to_async_proxy();
+      feed_keys();
+      for (int it = 0; it < nt; ++it) {
+        if (__syncthreads_or(0))
+          for (int i = 0; i < 4; ++i) __syncthreads();
+        tc_after();
+        if (elect_one()) {
+          if (it + 1 < nt) issue_scores();
+#pragma unroll
+          for (int kk = 0; kk < TILE / 32; ++kk)
+            mma8_ss(tm_o, desc_sw128(sma + C::OFF_V + 4096 * kk, 1024), desc_plain(sma + C::OFF_P + 512 * kk, 128, 16 * TILE),
+                    idesc8(NC, true, true), it > 0 || kk > 0);
+          mma_commit(bar_o);
+        }
+        __syncwarp();
+        to_async_proxy();
+        if (it + 1 < nt) feed_keys();
+        feed_values();
       }
-    };
-    auto words = [&](uint32_t from, uint32_t (*w)[WPT]) {
+      left -= nt;
+      cur.tile += nt;
+      if (left > 0) {
+        next_unit(part, cur);
+        if (lane == 0) tell_cursor(cur, next);
+      }
+      __syncthreads();
+      if (left > 0) cur = told_cursor(next);
+      __syncthreads();
+      if (cur.tiles == 0) break;
+    }
+    for (uint32_t n = nk < 2 ? 0 : nk - 2; n < nk; ++n) wait(bar_k + (n & 1), (n >> 1) & 1, true);
+    for (uint32_t n = nv < 2 ? 0 : nv - 2; n < nv; ++n) wait(bar_v + (n & 1), (n >> 1) & 1, true);
+  } else {
+    // ================================================================ unpacking and softmax
+    const uint32_t quad = uint32_t(32 * warp) << 16;
+    const int r4 = lane >> 2, c4 = lane & 3;
+    const uint32_t frag = (32 * warp + r4) * (D / 2) + c4 * (4 * WPT);  // this lane's words of token 32 warp + r4
+    uint32_t v_dst[2];  // and its 16-byte chunks of that token's row of values
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v_dst[h] = sma + C::OFF_V + (32 * warp + r4) * 128 + ((((WPT / 2) * c4 + h % (WPT / 2)) ^ r4) << 4);
+    const uint32_t p_dst = sma + C::OFF_P + tid * 16;
+    auto words = [&](uint32_t from, uint32_t (*w)[WPT]) {  // of tokens 32 warp + r4 + 8 i
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t at = from + frag + 8 * (D / 2) * i;
@@ -534,11 +630,11 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
           asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at));
       }
     };
-    // the keys of a tile, from registers to tensor memory
-    auto put_keys = [&]() {
+    // keys of the CTA's tile n, unpacked, to tensor memory
+    auto put_keys = [&](uint32_t n) {
       uint32_t kw[4][WPT];
-      wait_copy(bar_k, ph_k);
-      words(k_raw, kw);
+      wait(bar_k + (n & 1), (n >> 1) & 1, true);
+      words(sma + C::OFF_RK + (n & 1) * C::CODES, kw);
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
         uint32_t a[4 * WPT];
@@ -551,324 +647,288 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
         else tmem_st_rows2(tm_k + quad + (uint32_t(16 * gi) << 16), a);
       }
     };
-    auto issue_scores = [&]() {
+    uint32_t n = 0;  // tiles done
+    while (left > 0) {
+      // -------------------------------------------------------------- a unit's tiles
+      const int t_lo = cur.s.tile0 + cur.tile;
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      const int lo = part.prefix ? 0 : part.shared, hi = cur.s.len;  // tokens of this part
+      // ---- the rows' queries: a warp takes rows warp, warp + 4, ...; lane l
+      // holds dims E l .. E l + E - 1, E = d / 32
+      {
+        constexpr int E = D / 32;
+        for (int r = warp; r < RP; r += 4) {
+          const Row row = row_of(part, cur.s, cur.j * RP + r);
+          float x[E];
+          if (row.tok >= 0) {
+            const T* src = q + row.tok * ld_q + int64_t(cur.g * part.G + row.hh) * D + E * lane;
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk)
-        mma8_ts(tm_s, tm_k + 8 * kk, desc_sw128(sma + C::OFF_Q + 32 * kk, 1024), idesc8(NC, false, false), kk > 0);
-      mma_commit(bar_s);
-    };
-
-    // tile t_lo: keys and values; the next one's page
-    int row = row_of_page(t_lo, page_of(t_lo)), row_n, row_k = -1;  // of the tile, the next, the one after
-    copy_keys(row);
-    copy_values(row);
-    int page = page_of(t_lo + 1);
-    // ---- the rows' queries: a warp takes rows warp, warp + 4, ...; lane l
-    // holds dims E l .. E l + E - 1, E = d / 32
-    {
-      constexpr int E = D / 32;
-      for (int r = warp; r < RP; r += 4) {
-        const Row row = row_of(part, cur.s, cur.j * RP + r);
-        float x[E];
-        if (row.tok >= 0) {
-          const T* src = q + row.tok * ld_q + int64_t(cur.g * part.G + row.hh) * D + E * lane;
+            for (int e = 0; e < E; e += 2) {
+              const float2 f = fp8::to_f2<T>(__ldcg(reinterpret_cast<const unsigned int*>(src + e)));
+              x[e] = f.x;
+              x[e + 1] = f.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.f;
+          }
+#pragma unroll
+          for (int s = 1; s < E; s <<= 1)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if ((e & s) == 0) {
+                const float a = x[e], b = x[e + s];
+                x[e] = a + b;
+                x[e + s] = a - b;
+              }
+          float amax = 0.f;
+#pragma unroll
+          for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float other = __shfl_xor_sync(0xffffffffu, x[e], s);
+              x[e] = (lane & s) ? other - x[e] : x[e] + other;
+            }
+#pragma unroll
+          for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+          // pieces of x * 256 / amax: the first of up to 256, the others' sixteenths
+          const float up = amax > 0.f ? 256.0f / amax : 0.f;
+          uint32_t c[E / 2][3];
+          float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
-            const float2 f = fp8::to_f2<T>(__ldcg(reinterpret_cast<const unsigned int*>(src + e)));
-            x[e] = f.x;
-            x[e + 1] = f.y;
-          }
-        } else {
+            float a = x[e] * up, b = x[e + 1] * up;
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = 0.f;
-        }
-#pragma unroll
-        for (int s = 1; s < E; s <<= 1)
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if ((e & s) == 0) {
-              const float a = x[e], b = x[e + s];
-              x[e] = a + b;
-              x[e + s] = a - b;
+            for (int k = 0; k < 3; ++k) {
+              c[e / 2][k] = fp8::cvt_e4m3x2(make_float2(a, b));
+              const float2 f = h2_to_f2(h2_of_e4m3x2(c[e / 2][k]));
+              const float w = k == 0 ? 1.f : k == 1 ? 0.0625f : 0.00390625f;
+              sum += (f.x + f.y) * w;
+              a = (a - f.x) * 16.f;
+              b = (b - f.y) * 16.f;
             }
-        float amax = 0.f;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float other = __shfl_xor_sync(0xffffffffu, x[e], s);
-            x[e] = (lane & s) ? other - x[e] : x[e] + other;
           }
 #pragma unroll
-        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-        // pieces of x * 256 / amax: the first of up to 256, the others' sixteenths
-        const float up = amax > 0.f ? 256.0f / amax : 0.f;
-        uint32_t c[E / 2][3];
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          float a = x[e] * up, b = x[e + 1] * up;
+          for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+          // dim 8 w + 2 byte + h lies in byte 4 (8 (w % WPT) + 2 (w / WPT) + h) + byte
+          const int w = E * lane / 8;
+          const uint32_t col = 8u * (w % WPT) + 2u * (w / WPT);
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            c[e / 2][k] = fp8::cvt_e4m3x2(make_float2(a, b));
-            const float2 f = h2_to_f2(h2_of_e4m3x2(c[e / 2][k]));
-            const float w = k == 0 ? 1.f : k == 1 ? 0.0625f : 0.00390625f;
-            sum += (f.x + f.y) * w;
-            a = (a - f.x) * 16.f;
-            b = (b - f.y) * 16.f;
+            const uint32_t n = k * RP + r;
+            auto put = [&](uint32_t pos) { return sma + C::OFF_Q + n * 128 + ((((pos >> 4) ^ n) & 7) << 4) + (pos & 15); };
+            if constexpr (E == 4) {
+              const uint32_t v = c[0][k] | (c[1][k] << 16);  // dims 0 1 2 3 of this lane
+              const uint32_t ev = (v & 0xFF) | ((v >> 8) & 0xFF00), od = ((v >> 8) & 0xFF) | ((v >> 16) & 0xFF00);
+              const uint32_t pos = 4 * col + 2 * (lane & 1);
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos)), "h"(uint16_t(ev)) : "memory");
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos + 4)), "h"(uint16_t(od)) : "memory");
+            } else {
+              const uint32_t pos = 4 * col + (lane & 3);
+              asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos)), "r"(c[0][k] & 0xFF) : "memory");
+              asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos + 4)), "r"(c[0][k] >> 8) : "memory");
+            }
+          }
+          if (lane == 0) {
+            reinterpret_cast<float*>(rowf)[r] = 2.0f * amax * qscale;  // 2^9 of the codes, 1 / 256 of the pieces
+            reinterpret_cast<float*>(rowo)[r] = sum * (-8.0f / 512.0f);
+            reinterpret_cast<int*>(rowe)[r] = row.end;
+            reinterpret_cast<float*>(mtop)[r] = kNone;
           }
         }
+      }
+      to_async_proxy();
+      put_keys(n);
+      tc_wait_st();
+      tc_before();
+      __syncthreads();  // the fifth warp issues the products of the first scores
+
+      float2 l[RP / 2], z[RP / 2];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        // dim 8 w + 2 byte + h lies in byte 4 (8 (w % WPT) + 2 (w / WPT) + h) + byte
-        const int w = E * lane / 8;
-        const uint32_t col = 8u * (w % WPT) + 2u * (w / WPT);
+      for (int r = 0; r < RP / 2; ++r) l[r] = z[r] = make_float2(0.f, 0.f);
+
+      for (int it = 0; it < nt; ++it, ++n) {
+        // ---- the next tile's keys, once this one's scores are there
+        wait(bar_s, n & 1, false);
+        tc_after();
+        if (it + 1 < nt) put_keys(n + 1);
+        // ---- values, once the products of the tile before have read theirs
+        uint32_t vw[4][WPT];
+        const uint32_t raw = sma + C::OFF_RV + (n & 1) * C::STAGE_V;
+        wait(bar_v + (n & 1), (n >> 1) & 1, true);
+        words(raw, vw);
+        uint32_t k_half, v_half;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(k_half) : "r"(raw + C::CODES + 2 * tid));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v_half) : "r"(raw + C::CODES + 2 * TILE + 2 * tid));
+        int tok = (t_lo + it) * TILE + tid;
+        const bool absent = !((there[n & 1] >> (tid >> 4)) & 1) || tok < lo || tok >= hi;
+        if (it > 0) wait(bar_o, (n - 1) & 1, false);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t n = k * RP + r;
-          auto put = [&](uint32_t pos) { return sma + C::OFF_Q + n * 128 + ((((pos >> 4) ^ n) & 7) << 4) + (pos & 15); };
-          if constexpr (E == 4) {
-            const uint32_t v = c[0][k] | (c[1][k] << 16);  // dims 0 1 2 3 of this lane
-            const uint32_t ev = (v & 0xFF) | ((v >> 8) & 0xFF00), od = ((v >> 8) & 0xFF) | ((v >> 16) & 0xFF00);
-            const uint32_t pos = 4 * col + 2 * (lane & 1);
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos)), "h"(uint16_t(ev)) : "memory");
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(put(pos + 4)), "h"(uint16_t(od)) : "memory");
-          } else {
-            const uint32_t pos = 4 * col + (lane & 3);
-            asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos)), "r"(c[0][k] & 0xFF) : "memory");
-            asm volatile("st.shared.b8 [%0], %1;" ::"r"(put(pos + 4)), "r"(c[0][k] >> 8) : "memory");
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b[2 * WPT];
+#pragma unroll
+          for (int j = 0; j < WPT; ++j) bytes_of(vw[i][j], masks, b[2 * j], b[2 * j + 1]);
+#pragma unroll
+          for (int h = 0; h < WPT / 2; ++h)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v_dst[h] + 1024u * i), "r"(b[4 * h]), "r"(b[4 * h + 1]),
+                         "r"(b[4 * h + 2]), "r"(b[4 * h + 3])
+                         : "memory");
+        }
+        // ---- scores of this thread's token, two rows at a time
+        uint32_t v[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
+        const float2 scales = make_float2(__half2float(__ushort_as_half(uint16_t(k_half))),
+                                          absent ? 0.f : __half2float(__ushort_as_half(uint16_t(v_half))));
+        const float lv = lg2(fmaxf(scales.y, 5.9604645e-8f));
+        if (absent) tok = 0x7fffffff;
+        tc_wait_ld();
+        float2 s[RP / 2];
+        bool above = false;
+#pragma unroll
+        for (int r = 0; r < RP / 2; ++r) {
+          auto two = [&](int c) { return make_float2(__uint_as_float(v[c + 2 * r]), __uint_as_float(v[c + 2 * r + 1])); };
+          const float2 f = rowf[r], o = rowo[r];
+          const float2 x = __fadd2_rn(__ffma2_rn(two(RP), make_float2(0.0625f, 0.0625f), two(0)),
+                                      __ffma2_rn(two(2 * RP), make_float2(0.00390625f, 0.00390625f), o));
+          s[r] = __fmul2_rn(x, __fmul2_rn(f, make_float2(scales.x, scales.x)));
+          const int2 end = rowe[r];
+          if (tok >= end.x) s[r].x = -INFINITY;
+          if (tok >= end.y) s[r].y = -INFINITY;
+          const float2 y = __fadd2_rn(s[r], make_float2(lv, lv)), m = mtop[r];  // mtop = mref + 8
+          above |= y.x > m.x || y.y > m.y;
+        }
+        float2 p[RP / 2], w[RP / 2];
+        auto probabilities = [&]() {
+          uint32_t pw[3][RP / 4];
+#pragma unroll
+          for (int r = 0; r < RP / 2; r += 2) {
+            uint32_t c[2][3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 m = mtop[r + h], y = __fadd2_rn(s[r + h], make_float2(8.0f - m.x, 8.0f - m.y));
+              w[r + h] = make_float2(ex2(y.x), ex2(y.y));
+              p[r + h] = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
+              pieces_of(h2_of_f2(p[r + h].x, p[r + h].y), c[h]);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) pw[k][r / 2] = c[0][k] | (c[1][k] << 16);
           }
+          uint32_t words[NC / 4];
+#pragma unroll
+          for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
+#pragma unroll
+          for (int i = 0; i < NC / 16; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_dst + 16u * TILE * i), "r"(words[4 * i]),
+                         "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
+                         : "memory");
+          to_async_proxy();
+        };
+        probabilities();
+        if (it + 1 < nt) tc_wait_st();
+        tc_before();
+        if (__syncthreads_or(above)) {
+          // ---- raise the references that some score exceeds; sums and outputs so far follow
+          float* mt = reinterpret_cast<float*>(mtop);
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            float x = (r & 1 ? s[r / 2].y : s[r / 2].x) + lv;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) xch[warp * RP + r] = x;
+          }
+          __syncthreads();
+          float al[RP];
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            const float mo = mt[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
+            al[r] = x > mo ? ex2(mo - 8.0f - x) : 1.0f;
+            (r & 1 ? l[r / 2].y : l[r / 2].x) *= al[r];
+            (r & 1 ? z[r / 2].y : z[r / 2].x) *= al[r];
+          }
+          if (it > 0) {
+            uint32_t o[NC];
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, o + c);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+              for (int r = 0; r < RP; ++r) o[k * RP + r] = __float_as_uint(__uint_as_float(o[k * RP + r]) * al[r]);
+#pragma unroll
+            for (int c = 0; c < NC; c += 16) tmem_st16(tm_o + quad + c, o + c);
+            tc_wait_st();
+          }
+          __syncthreads();
+          if (tid < RP) {
+            const float x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
+            if (x > mt[tid]) mt[tid] = x + 8.0f;
+          }
+          __syncthreads();
+          probabilities();
+          tc_before();
+          __syncthreads();
+        }
+#pragma unroll
+        for (int r = 0; r < RP / 2; ++r) {
+          l[r] = __fadd2_rn(l[r], w[r]);
+          z[r] = __fadd2_rn(z[r], p[r]);
+        }
+      }
+
+      // ---------------------------------------------------------------- the unit's state
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        float lr = r & 1 ? l[r / 2].y : l[r / 2].x, zr = r & 1 ? z[r / 2].y : z[r / 2].x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          lr += __shfl_xor_sync(0xffffffffu, lr, o);
+          zr += __shfl_xor_sync(0xffffffffu, zr, o);
         }
         if (lane == 0) {
-          reinterpret_cast<float*>(rowf)[r] = 2.0f * amax * qscale;  // 2^9 of the codes, 1 / 256 of the pieces
-          reinterpret_cast<float*>(rowo)[r] = sum * (-8.0f / 512.0f);
-          reinterpret_cast<int*>(rowe)[r] = row.end;
-          reinterpret_cast<float*>(mtop)[r] = kNone;
+          xch[warp * 2 * RP + r] = lr;
+          xch[warp * 2 * RP + RP + r] = zr;
         }
       }
-    }
-    to_async_proxy();
-
-    // scores of the first tile; keys and scales of the second
-    put_keys();
-    tc_wait_st();
-    tc_before();
-    row_n = row_of_page(t_lo + 1, page);
-    if (nt > 1) copy_keys(row_n);
-    page = page_of(t_lo + 2);
-    __syncthreads();
-    if (tid == 0) {
+      __syncthreads();
+      wait(bar_o, (n - 1) & 1, false);
       tc_after();
-      issue_scores();
-    }
-
-    float2 l[RP / 2], z[RP / 2];
-#pragma unroll
-    for (int r = 0; r < RP / 2; ++r) l[r] = z[r] = make_float2(0.f, 0.f);
-
-    for (int it = 0; it < nt; ++it) {
-      // ---- the next tile's keys to tensor memory, once this one's scores are there
-      wait(bar_s, ph_s);
-      tc_after();
-      if (it + 1 < nt) {
-        put_keys();
-        if (it + 2 < nt) {
-          row_k = row_of_page(t_lo + it + 2, page);
-          copy_keys(row_k);
-          page = page_of(t_lo + it + 3);
-        }
-      }
-      // ---- values to shared memory, once the products of the tile before have read theirs
-      uint32_t vw[4][WPT];
-      wait_copy(bar_v, ph_v);
-      words(v_raw, vw);
-      uint32_t k_half, v_half;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(k_half) : "r"(s_raw + 2 * lane));
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v_half) : "r"(s_raw + 64 + 2 * lane));
-      const bool absent = row < 0 || (t_lo + it) * TILE + tid < lo || (t_lo + it) * TILE + tid >= hi;
-      if (it + 1 < nt) {
-        copy_values(row_n);
-        row = row_n;
-        row_n = row_k;
-      }
-      if (it > 0) wait(bar_o, ph_o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t b[2 * WPT];
-#pragma unroll
-        for (int j = 0; j < WPT; ++j) bytes_of(vw[i][j], masks, b[2 * j], b[2 * j + 1]);
-#pragma unroll
-        for (int h = 0; h < WPT / 2; ++h)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v_dst[h] + 1024u * i), "r"(b[4 * h]), "r"(b[4 * h + 1]),
-                       "r"(b[4 * h + 2]), "r"(b[4 * h + 3])
-                       : "memory");
-      }
-      // ---- scores of this thread's token, two rows at a time
       uint32_t v[NC];
 #pragma unroll
-      for (int c = 0; c < NC; c += 16) tmem_ld16(tm_s + quad + c, v + c);
-      const float2 scales = make_float2(__half2float(__ushort_as_half(uint16_t(k_half))),
-                                        absent ? 0.f : __half2float(__ushort_as_half(uint16_t(v_half))));
-      const float lv = lg2(fmaxf(scales.y, 5.9604645e-8f));
-      const int tok = absent ? 0x7fffffff : (t_lo + it) * TILE + tid;
+      for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, v + c);
       tc_wait_ld();
-      float2 s[RP / 2];
-      bool above = false;
+      const int J = (cur.s.rows + RP - 1) / RP;
+      const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, RP) + int64_t(cur.g) * J + cur.j;
+      const int64_t dst = (unit + blockIdx.x) * RP;
+      const int dim = (tid & ~7) + 2 * (tid & 3) + ((tid >> 2) & 1);  // of byte tid of a token's row
 #pragma unroll
-      for (int r = 0; r < RP / 2; ++r) {
-        auto two = [&](int c) { return make_float2(__uint_as_float(v[c + 2 * r]), __uint_as_float(v[c + 2 * r + 1])); };
-        const float2 f = rowf[r], o = rowo[r];
-        const float2 x = __fadd2_rn(__ffma2_rn(two(RP), make_float2(0.0625f, 0.0625f), two(0)),
-                                    __ffma2_rn(two(2 * RP), make_float2(0.00390625f, 0.00390625f), o));
-        s[r] = __fmul2_rn(x, __fmul2_rn(f, make_float2(scales.x, scales.x)));
-        const int2 end = rowe[r];
-        if (tok >= end.x) s[r].x = -INFINITY;
-        if (tok >= end.y) s[r].y = -INFINITY;
-        const float2 y = __fadd2_rn(s[r], make_float2(lv, lv)), m = mtop[r];  // mtop = mref + 8
-        above |= y.x > m.x || y.y > m.y;
+      for (int r = 0; r < RP; ++r) {
+        const float zz = (xch[RP + r] + xch[3 * RP + r]) + (xch[5 * RP + r] + xch[7 * RP + r]);
+        const float o = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
+                             fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])));
+        if (tid < D) ws.o[(dst + r) * D + dim] = fmaf(o, 512.0f, -8.0f * zz);
       }
-      float2 p[RP / 2], w[RP / 2];
-      auto probabilities = [&]() {
-        uint32_t pw[3][RP / 4];
-#pragma unroll
-        for (int r = 0; r < RP / 2; r += 2) {
-          uint32_t c[2][3];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 m = mtop[r + h], y = __fadd2_rn(s[r + h], make_float2(8.0f - m.x, 8.0f - m.y));
-            w[r + h] = make_float2(ex2(y.x), ex2(y.y));
-            p[r + h] = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
-            pieces_of(h2_of_f2(p[r + h].x, p[r + h].y), c[h]);
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) pw[k][r / 2] = c[0][k] | (c[1][k] << 16);
-        }
-        uint32_t words[NC / 4];
-#pragma unroll
-        for (int i = 0; i < NC / 4; ++i) words[i] = i < 3 * RP / 4 ? pw[i / (RP / 4)][i % (RP / 4)] : 0u;
-#pragma unroll
-        for (int i = 0; i < NC / 16; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_dst + 16u * TILE * i), "r"(words[4 * i]),
-                       "r"(words[4 * i + 1]), "r"(words[4 * i + 2]), "r"(words[4 * i + 3])
-                       : "memory");
-        to_async_proxy();
-      };
-      probabilities();
-      if (it + 1 < nt) tc_wait_st();
-      tc_before();
-      if (__syncthreads_or(above)) {
-        // ---- raise the references that some score exceeds; sums and outputs so far follow
-        float* mt = reinterpret_cast<float*>(mtop);
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float x = (r & 1 ? s[r / 2].y : s[r / 2].x) + lv;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          if (lane == 0) xch[warp * RP + r] = x;
-        }
-        __syncthreads();
-        float al[RP];
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float mo = mt[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
-          al[r] = x > mo ? ex2(mo - 8.0f - x) : 1.0f;
-          (r & 1 ? l[r / 2].y : l[r / 2].x) *= al[r];
-          (r & 1 ? z[r / 2].y : z[r / 2].x) *= al[r];
-        }
-        if (it > 0) {
-          uint32_t o[NC];
-          tc_after();
-#pragma unroll
-          for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, o + c);
-          tc_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int r = 0; r < RP; ++r) o[k * RP + r] = __float_as_uint(__uint_as_float(o[k * RP + r]) * al[r]);
-#pragma unroll
-          for (int c = 0; c < NC; c += 16) tmem_st16(tm_o + quad + c, o + c);
-          tc_wait_st();
-        }
-        __syncthreads();
-        if (tid < RP) {
-          const float x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
-          if (x > mt[tid]) mt[tid] = x + 8.0f;
-        }
-        __syncthreads();
-        probabilities();
-        tc_before();
-        __syncthreads();
+      if (tid < RP) {
+        const float ll = (xch[tid] + xch[2 * RP + tid]) + (xch[4 * RP + tid] + xch[6 * RP + tid]);
+        *reinterpret_cast<float2*>(ws.ml + (dst + tid) * 2) = make_float2(reinterpret_cast<float*>(mtop)[tid] - 8.0f, ll);
       }
       if (tid == 0) {
-        tc_after();
-        if (it + 1 < nt) issue_scores();
-#pragma unroll
-        for (int kk = 0; kk < TILE / 32; ++kk)
-          mma8_ss(tm_o, desc_sw128(sma + C::OFF_V + 4096 * kk, 1024), desc_plain(sma + C::OFF_P + 512 * kk, 128, 16 * TILE),
-                  idesc8(NC, true, true), it > 0 || kk > 0);
-        mma_commit(bar_o);
+        if (cur.tile == 0) ws.span[2 * unit] = blockIdx.x;
+        if (cur.tile + nt == cur.tiles) ws.span[2 * unit + 1] = blockIdx.x;
       }
-#pragma unroll
-      for (int r = 0; r < RP / 2; ++r) {
-        l[r] = __fadd2_rn(l[r], w[r]);
-        z[r] = __fadd2_rn(z[r], p[r]);
-      }
-    }
-
-    // ---------------------------------------------------------------- the unit's state
-#pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      float lr = r & 1 ? l[r / 2].y : l[r / 2].x, zr = r & 1 ? z[r / 2].y : z[r / 2].x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        lr += __shfl_xor_sync(0xffffffffu, lr, o);
-        zr += __shfl_xor_sync(0xffffffffu, zr, o);
-      }
-      if (lane == 0) {
-        xch[warp * 2 * RP + r] = lr;
-        xch[warp * 2 * RP + RP + r] = zr;
-      }
-    }
-    __syncthreads();
-    wait(bar_o, ph_o);
-    tc_after();
-    uint32_t v[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c += 16) tmem_ld16(tm_o + quad + c, v + c);
-    tc_wait_ld();
-    const int J = (cur.s.rows + RP - 1) / RP;
-    const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, RP) + int64_t(cur.g) * J + cur.j;
-    const int64_t dst = (unit + blockIdx.x) * RP;
-    const int dim = (tid & ~7) + 2 * (tid & 3) + ((tid >> 2) & 1);  // of byte tid of a token's row
-#pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      const float zz = (xch[RP + r] + xch[3 * RP + r]) + (xch[5 * RP + r] + xch[7 * RP + r]);
-      const float o = fmaf(__uint_as_float(v[2 * RP + r]), 0.00390625f,
-                           fmaf(__uint_as_float(v[RP + r]), 0.0625f, __uint_as_float(v[r])));
-      if (tid < D) ws.o[(dst + r) * D + dim] = fmaf(o, 512.0f, -8.0f * zz);
-    }
-    if (tid < RP) {
-      const float ll = (xch[tid] + xch[2 * RP + tid]) + (xch[4 * RP + tid] + xch[6 * RP + tid]);
-      *reinterpret_cast<float2*>(ws.ml + (dst + tid) * 2) = make_float2(reinterpret_cast<float*>(mtop)[tid] - 8.0f, ll);
-    }
-    if (tid == 0) {
-      if (cur.tile == 0) ws.span[2 * unit] = blockIdx.x;
-      if (cur.tile + nt == cur.tiles) ws.span[2 * unit + 1] = blockIdx.x;
-    }
-    tc_before();
-    __syncthreads();  // the exchange, the rows and the references are read
-    left -= nt;
-    cur.tile += nt;
-    if (left > 0) {
-      next_unit(part, cur);
-      if (cur.tiles == 0) break;
+      tc_before();
+      left -= nt;
+      __syncthreads();  // the exchange, the rows and the references are read
+      if (left > 0) cur = told_cursor(next);
+      if (left > 0 && cur.tiles == 0) break;
     }
   }
   if (behind) fp8::wait_for_previous();  // the prefix part is over before this part is
   __syncthreads();
-  if (warp == 0) {
+  if (warp == FEED) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
   }
@@ -905,8 +965,10 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
     const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
     if (tiles_of(p, q, j) == 0) continue;
     const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
-    const int2 span = __ldcg(reinterpret_cast<const int2*>(s.span + 2 * unit));
-    cnt[k] = span.y - span.x + 1;
+    int2 span = __ldcg(reinterpret_cast<const int2*>(s.span + 2 * unit));
+    span.x = min(max(span.x, 0), s.ctas - 1);  // as they are, unless the batch changed under the call
+    span.y = min(span.y, s.ctas - 1);
+    cnt[k] = max(span.y - span.x + 1, 0);
     const int64_t at = (unit + span.x) * p.RP + rr - j * p.RP;
     ml[k] += at * 2;
     o[k] += at * D;
@@ -965,7 +1027,7 @@ struct Plan {
   int64_t units;
 };
 inline int rows_of_unit(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
-inline int ctas_per_sm(int RP) { return RP == 4 ? 5 : RP == 8 ? 4 : 3; }
+inline int ctas_per_sm(int RP) { return RP == 4 ? few::ctas_per_sm<4>() : RP == 8 ? few::ctas_per_sm<8>() : few::ctas_per_sm<16>(); }
 inline Plan plan_own(int64_t N, int64_t B, int64_t G, int64_t Hkv, int64_t max_q, int sms) {
   Plan p;
   p.RP = rows_of_unit(max_q * G);
