@@ -275,12 +275,17 @@ __device__ __forceinline__ Cursor told_cursor(const int* sh) {
 __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
   const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
   const bool tell = blockIdx.x == 0;
-  int64_t &before = sh[8], &found = sh[9];
   // sequences in blocks of n, this thread's within the first one kept
-  int64_t first = tid < nseq ? steps_of(p, seq_of(p, tid, tell)) * p.Hkv : 0, sum = first;
+  Seq mine = {0, 0, 0, 0, 0};
+  int64_t head = 0;  // its tiles of one KV head
+  if (tid < nseq) {
+    mine = seq_of(p, tid, tell);
+    head = steps_of(p, mine);
+  }
+  const int64_t own = head * p.Hkv;
+  int64_t first = own, sum = own;
   for (int b = tid + n; b < nseq; b += n) sum += steps_of(p, seq_of(p, b, tell)) * p.Hkv;
-  if (tid == 0) found = -1;
-  const int64_t own = first;
+  if (tid == 0) sh[8] = 0;  // whether some thread found the tile
   int64_t all = block_scan(first, sh), total = all;
   if (nseq > n) total = block_scan(sum, sh);
   if (total == 0) return 0;
@@ -289,46 +294,43 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
   int64_t v = own, x = first, done = 0;
   for (int b0 = 0;;) {
     if (v > 0 && at >= done + x - v && at < done + x) {
-      found = b0 + tid;
-      before = done + x - v;
-    }
-    __syncthreads();
-    if (found >= 0) break;
-    done += all;
-    b0 += n;
-    x = v = b0 + tid < nseq ? steps_of(p, seq_of(p, b0 + tid, false)) * p.Hkv : 0;
-    all = block_scan(x, sh);
-    if (b0 >= nseq) return 0;  // the batch changed under the call
-  }
-  if (tid == 0) {
-    c.b = int(found);
-    c.s = seq_of(p, c.b, false);
-    int64_t rest = at - before;
-    const int64_t head = steps_of(p, c.s);
-    c.tile = c.tiles = c.j = c.g = 0;
-    if (head > 0) {  // as it was, unless the batch changes under the call
-      c.g = int(min(quotient(rest, head), int64_t(p.Hkv - 1)));
+      int64_t rest = at - (done + x - v);
+      c.b = b0 + tid;
+      c.s = mine;
+      c.g = int(quotient(rest, head));
       rest -= c.g * head;
-      const int J = (c.s.rows + p.RP - 1) / p.RP;
+      c.j = 0;
       if (p.prefix) {
         c.tiles = tiles_of(p, c.s, 0);
         c.j = int(quotient(rest, c.tiles));
         rest -= int64_t(c.j) * c.tiles;
       } else {
-        while (c.j < J && rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
+        while (rest >= (c.tiles = tiles_of(p, c.s, c.j))) {
           rest -= c.tiles;
           ++c.j;
         }
       }
-      if (c.j >= J) c.j = J - 1;
-      c.tile = int(min(rest, int64_t(c.tiles > 0 ? c.tiles - 1 : 0)));
+      c.tile = int(rest);
+      tell_cursor(c, reinterpret_cast<int*>(sh + 10));
+      sh[8] = 1;
     }
-    tell_cursor(c, reinterpret_cast<int*>(sh + 10));
+    __syncthreads();
+    if (sh[8] != 0) break;
+    done += all;
+    b0 += n;
+    if (b0 >= nseq) return 0;  // the batch changed under the call
+    head = v = 0;
+    if (b0 + tid < nseq) {
+      mine = seq_of(p, b0 + tid, false);
+      head = steps_of(p, mine);
+      v = head * p.Hkv;
+    }
+    x = v;
+    all = block_scan(x, sh);
   }
-  __syncthreads();
   c = told_cursor(reinterpret_cast<int*>(sh + 10));
   __syncthreads();
-  return c.tiles > 0 ? min(per, total - at) : 0;
+  return min(per, total - at);
 }
 // The next unit that has tiles; without one (the batch changed under the call) c.tiles is 0.
 __device__ __forceinline__ void next_unit(const Part& p, Cursor& c) {
@@ -937,50 +939,62 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 }  // namespace few
 
 // ------------------------------------------------------------------ join
-// One CTA per (token, query head), a thread a dim: the states of the row's
-// unit of each part, o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, d of them
-// at a time.
+// One CTA per (token, query head): o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i
+// over the states of the row's unit of each part, d of them at a time.  A thread
+// adds 4 dims of every fourth state, eight loads at once: with one tile a CTA
+// (33 states of a row, 1 x 4097 tokens) the round trips to L2 are what counts.
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
 join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __restrict__ out, int64_t ld_out) {
   __shared__ float x[D], top[D / 32], low[D / 32];
-  fp8::wait_for_previous();
+  __shared__ float4 part4[4][D / 4];
   const int n = blockIdx.x / Hq, h = blockIdx.x % Hq, e = threadIdx.x;
   const int g = h / own.G;
+  // the batch was there before the parts' CTAs let this kernel start
   const Place pl = place_of(own.t, n);
-  if (pl.b < 0) return;
-  // slots of either part that hold a state of this row
+  // slots of either part that may hold a state of this row
   const float *ml[2], *o[2];
-  int cnt[2] = {0, 0};
+  const int* span[2] = {nullptr, nullptr};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const Part& p = k == 0 ? pre : own;
     const Space& s = k == 0 ? sp : so;
     ml[k] = s.ml;
     o[k] = s.o;
-    if (k == 0 && p.shared == 0) continue;
+    if (pl.b < 0 || (k == 0 && p.shared == 0)) continue;
     const Seq q = seq_of(p, pl.b, false);
     const int rr = (n - q.tok0) * p.G + h - g * p.G;
     if (pl.pos < 0 || rr < 0 || rr >= q.rows) continue;
     const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
     if (tiles_of(p, q, j) == 0) continue;
     const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
-    int2 span = __ldcg(reinterpret_cast<const int2*>(s.span + 2 * unit));
-    span.x = min(max(span.x, 0), s.ctas - 1);  // as they are, unless the batch changed under the call
-    span.y = min(span.y, s.ctas - 1);
-    cnt[k] = max(span.y - span.x + 1, 0);
-    const int64_t at = (unit + span.x) * p.RP + rr - j * p.RP;
+    span[k] = s.span + 2 * unit;
+    const int64_t at = unit * p.RP + rr - j * p.RP;
     ml[k] += at * 2;
     o[k] += at * D;
   }
-  float m = kNone, num = 0.f, den = 0.f;
+  fp8::wait_for_previous();
+  if (pl.b < 0) return;
+  float m = kNone, den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d4 = e % (D / 4), grp = e / (D / 4);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
+    if (span[k] == nullptr) continue;
+    const int ctas = k == 0 ? sp.ctas : so.ctas;
     const int64_t step = k == 0 ? pre.RP : own.RP;
-    for (int i0 = 0; i0 < cnt[k]; i0 += D) {
-      const int c = min(cnt[k] - i0, D);
+    int2 w = __ldcg(reinterpret_cast<const int2*>(span[k]));
+    w.x = min(max(w.x, 0), ctas - 1);  // as they are, unless the batch changed under the call
+    w.y = min(w.y, ctas - 1);
+    for (int i0 = w.x; i0 <= w.y; i0 += D) {
+      const int c = min(w.y - i0 + 1, D);
       float2 s = make_float2(kNone, 0.f);
       if (e < c) s = __ldcg(reinterpret_cast<const float2*>(ml[k] + (i0 + e) * step * 2));
+      const float* src = o[k] + (i0 + grp) * step * D + 4 * d4;
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (grp + 4 * i < c) v[i] = __ldcg(reinterpret_cast<const float4*>(src + 4 * i * step * D));
       float mx = s.x;
 #pragma unroll
       for (int b = 16; b > 0; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
@@ -989,7 +1003,7 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
       __syncthreads();
       mx = m;
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) mx = fmaxf(mx, top[w]);
+      for (int b = 0; b < D / 32; ++b) mx = fmaxf(mx, top[b]);
       const float a = ex2(m - mx), f = ex2(s.x - mx);
       m = mx;
       x[e] = f;
@@ -1000,21 +1014,36 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
       __syncthreads();
       den *= a;
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) den += low[w];
-      num *= a;
-      const float* src = o[k] + i0 * step * D + e;
-#pragma unroll 8
-      for (int i = 0; i < c; ++i) num = fmaf(x[i], __ldcg(src + i * step * D), num);
+      for (int b = 0; b < D / 32; ++b) den += low[b];
+      num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+      for (int i1 = 0; i1 < c; i1 += 32) {
+        if (i1 > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i1 + grp + 4 * i < c) v[i] = __ldcg(reinterpret_cast<const float4*>(src + (i1 + 4 * i) * step * D));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i1 + grp + 4 * i < c) {
+            const float b = x[i1 + grp + 4 * i];
+            num = make_float4(fmaf(b, v[i].x, num.x), fmaf(b, v[i].y, num.y), fmaf(b, v[i].z, num.z), fmaf(b, v[i].w, num.w));
+          }
+      }
     }
   }
-  float y = den > 0.f ? num / den : 0.f;
+  __syncthreads();
+  part4[grp][d4] = num;
+  __syncthreads();
+  const float* pf = reinterpret_cast<const float*>(part4);
+  const float all = (pf[e] + pf[D + e]) + (pf[2 * D + e] + pf[3 * D + e]);
+  float y = den > 0.f ? all / den : 0.f;
   if (unrotate) {
-    for (int span = 1; span < D; span <<= 1) {
+    for (int span2 = 1; span2 < D; span2 <<= 1) {
       __syncthreads();
       x[e] = y;
       __syncthreads();
-      const float other = x[e ^ span];
-      y = (e & span) ? other - y : y + other;
+      const float other = x[e ^ span2];
+      y = (e & span2) ? other - y : y + other;
     }
     y *= 1.0f / sqrtf(float(D));
   }
