@@ -155,10 +155,11 @@ constexpr int kTries = 1 << 18;
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing: 2^(kNone - s) is 0
 
 // One part of a call: the shared prefix (rows of all N tokens as one list,
-// tokens [0, shared)) or the sequences' own tokens [shared, length).
+// tokens [0, shared)), the sequences' own tokens [shared, length), or (whole)
+// all tokens of each sequence, the shared ones from the first one's pages.
 struct Part {
   Batch t;
-  int N, G, Hkv, shared, prefix;
+  int N, G, Hkv, shared, prefix, whole;
   int RP;  // rows of a unit
 };
 
@@ -192,7 +193,10 @@ __device__ __forceinline__ int tiles_of(const Part& p, const Seq& s, int j) {
     const int last = min(p.RP * (j + 1), s.rows) - 1;
     end = min(end, s.first + last / p.G + 1);
   }
-  return end <= 0 ? 0 : max((end + TILE - 1) / TILE - s.tile0, 0);
+  if (end <= 0) return 0;
+  const int own = (end + TILE - 1) / TILE - s.tile0;
+  if (!p.whole) return max(own, 0);
+  return (min(end, p.shared) + TILE - 1) / TILE + (end > p.shared ? own : 0);
 }
 // Tiles of one KV head of a sequence.
 __device__ __forceinline__ int64_t steps_of(const Part& p, const Seq& s) {
@@ -241,7 +245,7 @@ struct Cursor {
   int b, g, j, tile, tiles;  // unit (b, g, j), next of its tiles, all of them
   Seq s;
 };
-// Sums over the block: of the threads up to this one, and (returned) of all.  sh: a word a warp, at most 8.
+// Sums over the block: of the threads up to this one, and (returned) of all.  sh: a word a warp, at most 16.
 __device__ __forceinline__ int64_t block_scan(int64_t& v, int64_t* sh) {
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
@@ -271,8 +275,9 @@ __device__ __forceinline__ Cursor told_cursor(const int* sh) {
   return {sh[0], sh[1], sh[2], sh[3], sh[4], {sh[5], sh[6], sh[7], sh[8], sh[9]}};
 }
 // Sets the cursor to this CTA's first tile (the row of all tiles is cut into
-// equal parts, the last ones maybe none) and returns how many it has.  sh: 18 words of shared memory.
-__device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t* sh) {
+// equal parts, the last ones maybe none) and returns how many it has.  sh: 26 words of shared memory.
+// per: the tiles of each but the last CTAs.
+__device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t& per, int64_t* sh) {
   const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
   const bool tell = blockIdx.x == 0;
   // sequences in blocks of n, this thread's within the first one kept
@@ -285,11 +290,12 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
   const int64_t own = head * p.Hkv;
   int64_t first = own, sum = own;
   for (int b = tid + n; b < nseq; b += n) sum += steps_of(p, seq_of(p, b, tell)) * p.Hkv;
-  if (tid == 0) sh[8] = 0;  // whether some thread found the tile
+  if (tid == 0) sh[16] = 0;  // whether some thread found the tile
   int64_t all = block_scan(first, sh), total = all;
   if (nseq > n) total = block_scan(sum, sh);
   if (total == 0) return 0;
-  const int64_t per = quotient(total + gridDim.x - 1, gridDim.x), at = per * blockIdx.x;
+  per = quotient(total + gridDim.x - 1, gridDim.x);
+  const int64_t at = per * blockIdx.x;
   if (at >= total) return 0;
   int64_t v = own, x = first, done = 0;
   for (int b0 = 0;;) {
@@ -311,11 +317,11 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
         }
       }
       c.tile = int(rest);
-      tell_cursor(c, reinterpret_cast<int*>(sh + 10));
-      sh[8] = 1;
+      tell_cursor(c, reinterpret_cast<int*>(sh + 18));
+      sh[16] = 1;
     }
     __syncthreads();
-    if (sh[8] != 0) break;
+    if (sh[16] != 0) break;
     done += all;
     b0 += n;
     if (b0 >= nseq) return 0;  // the batch changed under the call
@@ -328,7 +334,7 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t*
     x = v;
     all = block_scan(x, sh);
   }
-  c = told_cursor(reinterpret_cast<int*>(sh + 10));
+  c = told_cursor(reinterpret_cast<int*>(sh + 18));
   __syncthreads();
   return min(per, total - at);
 }
@@ -421,7 +427,7 @@ struct Cfg {
   static constexpr int OFF_RV = OFF_RK + 2 * CODES;            // packed values and scales, two tiles
   static constexpr int OFF_ROW = OFF_RV + 2 * STAGE_V;         // four numbers a row
   static constexpr int OFF_X = OFF_ROW + RP * 16;              // float [4][2 RP] exchange
-  static constexpr int OFF_CUR = OFF_X + 4 * 2 * RP * 4;       // the next cursor; find_start's words begin 80 bytes before
+  static constexpr int OFF_CUR = OFF_X + 4 * 2 * RP * 4;       // the next cursor; find_start's words begin 144 bytes before
   static constexpr int OFF_BAR = OFF_CUR + 64;
   static constexpr int SMEM = OFF_BAR + 80;
 };
@@ -478,7 +484,8 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   const uint32_t tm_k = tmem, tm_s = tmem + C::KC, tm_o = tm_s + NC;
   const Batch& bt = part.t;
   Cursor cur;
-  int64_t left = find_start(part, cur, reinterpret_cast<int64_t*>(sm + C::OFF_CUR - 80));
+  int64_t per;
+  int64_t left = find_start(part, cur, per, reinterpret_cast<int64_t*>(sm + C::OFF_CUR - 144));
   // A wait ends after about a second (each try sleeps some microseconds) and is
   // recorded.  Once one gave up, waits for MMAs end at once; copies are waited
   // for all the same, so that none is in flight when the CTA ends.
@@ -489,6 +496,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
       *gave_up = 1;
       record_error(QUAROT_ERR_TIMEOUT);
     }
+    __syncwarp();
   };
 
   if (warp == FEED) {
@@ -938,6 +946,762 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 
 }  // namespace few
 
+// ===================================================================== many
+// Up to 128 rows of a unit, rows as the MMA's M: a row's scores are one
+// thread pair's, its probabilities go back to tensor memory as the A operand
+// of O += P V without a word between lanes.  The warps of a CTA (one on an SM):
+//   warp 0      feeder: pages, copies of packed tiles (three ahead), the next
+//               unit's queries
+//   warp 1      MMA issuer
+//   warps 2-5   converters: key codes to e4m3 bytes (bytes_of, rows of a
+//               swizzled K-major operand); values to fp16 code * scale, token
+//               after token (the B operand with N running fastest: no transpose)
+//   warps 6-13  softmax, two to a lane quadrant, each half a row: queries
+//               rotated and split into e4m3 pieces at a unit's start, scores to
+//               probabilities, outputs at its end
+// Tensor memory: the three pieces of the queries (A operand of S), two score
+// buffers, of which fp16 probabilities take the first half, and O.  S(n + 1)
+// runs while the softmax works on S(n).
+//
+// A score is (S - off) ks f with off = 8 sum q~ (the codes' offset) and f the
+// row's factor; the references are raised as in `few`, without the value
+// scales, which the values carry here.
+//
+// What bounds it: 12 MMAs of 128 x 128 x 32 for S and 8 of 128 x 128 x 16 for
+// P V a tile, some 90 clocks each.
+namespace many {
+
+constexpr int NT = 448, ROWS = 128, NCW = 4, NSW = 8, SP = 3, UNIT_READERS = 1 + NCW + NSW;
+constexpr uint32_t COL_Q = 0, COL_S = 128, COL_O = 384;  // S buffer b at COL_S + 128 b
+
+template <int D>
+struct Cfg {
+  static constexpr int WPT = D / 32;
+  static constexpr int CODES = TILE * D / 2;
+  static constexpr int STAGE = 2 * CODES + 4 * TILE;   // packed keys, values, key scales, value scales
+  static constexpr int ATOM = TILE * 128;              // 128 bytes of every token
+  static constexpr int VBYTES = ATOM * (D / 64);       // a converted value tile
+  static constexpr int OFF_K = 0;                      // converted keys, two tiles
+  static constexpr int OFF_V = OFF_K + 2 * ATOM;       // converted values, two tiles
+  static constexpr int OFF_Q = OFF_V + 2 * VBYTES;     // the unit's queries, 16-byte chunks swizzled
+  static constexpr int OFF_RAW = OFF_Q + ROWS * D * 2;
+  static constexpr int OFF_KS = OFF_RAW + SP * STAGE;  // float [2][TILE] key scales of the score buffers
+  static constexpr int OFF_X = OFF_KS + 2 * TILE * 4;  // float [2][ROWS] exchange of a row's halves, three times; at first find_start's words
+  static constexpr int OFF_CUR = OFF_X + 6 * ROWS * 4; // cursors of two units
+  static constexpr int OFF_BAR = OFF_CUR + 128;
+  static constexpr int NBAR = 2 * SP + 4 + 4 + 3 + 8 + 2;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 64;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// Instruction descriptor of kind::f16, fp16 x fp16 to fp32, M = 128, B with N running fastest.
+__host__ __device__ constexpr uint32_t idesc16(int n) { return (1u << 4) | (1u << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24); }
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
+}
+// 128-byte swizzle, N (or M) running fastest: 64 fp16 of 8 tokens are 1024
+// bytes, further tokens `sbo`, further columns `lbo` bytes on.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* r) {
+  tmem_ld16(t, r);
+  tmem_ld16(t + 16, r + 16);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Sequence-row, tokens and range of a unit's k-th tile: the tiles of the
+// prefix come first where a part has both.
+struct Span {
+  int row, t0, lo, hi;
+};
+__device__ __forceinline__ Span tile_at(const Part& p, const Cursor& c, int k) {
+  if (p.prefix) return {0, k * TILE, 0, c.s.len};
+  if (p.whole) {
+    const int np = (min(c.s.len, p.shared) + TILE - 1) / TILE;
+    if (k < np) return {0, k * TILE, 0, min(c.s.len, p.shared)};
+    k -= np;
+  }
+  return {c.b, (c.s.tile0 + k) * TILE, p.shared, c.s.len};
+}
+// Sums and differences over spans 1 .. N / 2 of N registers.
+template <int N>
+__device__ __forceinline__ void hadamard_regs(float2* x) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) x[i] = make_float2(x[i].x + x[i].y, x[i].x - x[i].y);
+#pragma unroll
+  for (int s = 1; s < N / 2; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      if ((i & s) == 0) {
+        const float2 a = x[i], b = x[i + s];
+        x[i] = __fadd2_rn(a, b);
+        x[i + s] = __fadd2_rn(a, make_float2(-b.x, -b.y));
+      }
+}
+
+struct Values {  // constants of the values' conversion, like Masks
+  uint32_t mask, flip;  // 0x000F000F, 0x64086408
+};
+
+// direct: units that a CTA works on alone are written to out; of the others
+// (the start of one and the end of another, two a CTA) slot 2 w + 0 holds the
+// state of one that an earlier CTA began, 2 w + 1 of one that this CTA began,
+// and todo [w] names the unit of another CTA's that CTA w ended.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT, 1)
+many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s,
+            const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int4* todo,
+            int unrotate, T* __restrict__ out, int64_t ld_out, Masks masks, Values vals) {
+  using C = Cfg<D>;
+  constexpr int WPT = C::WPT, H = D / 2;  // H: elements of a thread's half row
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const uint32_t sma = smem_u32(sm);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  uint64_t* raw_empty = raw_full + SP;
+  uint64_t* k_full = raw_empty + SP;  // [2] each
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* unit_full = v_empty + 2;   // cursor and queries
+  uint64_t* unit_empty = unit_full + 1;
+  uint64_t* q_full = unit_empty + 1;
+  uint64_t* s_full = q_full + 1;  // [2] each
+  uint64_t* p_full = s_full + 2;
+  uint64_t* ks_full = p_full + 2;
+  uint64_t* ks_empty = ks_full + 2;
+  uint64_t* o_done = ks_empty + 2;     // one phase a tile
+  uint64_t* unit_done = o_done + 1;    // and a unit
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  volatile int* there = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);      // [SP] groups of 16 tokens that a packed tile has
+  volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers
+  float* ksf = reinterpret_cast<float*>(sm + C::OFF_KS);
+  float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
+  int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [2][16]
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    for (int i = 0; i < SP; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, NCW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, NCW);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, NCW);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, NSW);
+      mbar_init(ks_full + i, NCW);
+      mbar_init(ks_empty + i, NSW);
+    }
+    mbar_init(unit_full, 33);  // each lane's copies, and the cursor
+    mbar_init(unit_empty, UNIT_READERS);
+    mbar_init(q_full, NSW);
+    mbar_init(o_done, 1);
+    mbar_init(unit_done, 1);
+    *gave_up = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(const_cast<uint32_t*>(slot))),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  fp8::wait_for_previous();
+  fp8::next_may_start();
+  Cursor cur;
+  int64_t per;
+  int64_t left = find_start(part, cur, per, reinterpret_cast<int64_t*>(sm + C::OFF_X));
+  if (todo != nullptr && tid == 0) todo[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+  auto wait = [&](uint64_t* bar, uint32_t phase, bool copy = false) {
+    bool ok = mbar_try_wait(bar, phase);
+    for (int n = 0; !ok && n < kTries && (copy || !*gave_up); ++n) ok = mbar_try_wait(bar, phase);
+    if (!ok) {
+      *gave_up = 1;
+      record_error(QUAROT_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  // the unit that the feeder published: waits for it and reads its cursor
+  auto unit_at = [&](uint32_t u) {
+    wait(unit_full, u & 1, true);
+    return told_cursor(cursors + 16 * (u & 1));
+  };
+
+  if (warp == 0) {
+    // ================================================================ feeder
+    const int shift = (part.t.ps & (part.t.ps - 1)) == 0 ? __ffs(part.t.ps) - 1 : -1;
+    uint32_t n = 0;
+    for (uint32_t u = 0; left > 0; ++u) {
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      // ---- the unit: cursor, queries
+      if (u > 0) wait(unit_empty, (u - 1) & 1);
+      if (lane == 0) tell_cursor(cur, cursors + 16 * (u & 1));
+      for (int c = lane; c < ROWS * (D / 8); c += 32) {
+        const int r = c / (D / 8), ch = c % (D / 8), rr = cur.j * ROWS + r;
+        const int i = rr / part.G;
+        const bool in = rr < cur.s.rows;
+        const T* src = q + (in ? (cur.s.tok0 + i) * ld_q + int64_t(cur.g * part.G + rr - i * part.G) * D + 8 * ch : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sma + C::OFF_Q + r * (2 * D) + ((ch ^ (r & 7)) << 4)),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(unit_full)) : "memory");
+      if (lane == 0) mbar_arrive(unit_full);
+      // ---- its tiles
+      for (int k = 0; k < nt; ++k, ++n) {
+        const Span sp = tile_at(part, cur, cur.tile + k);
+        const int tb = sp.t0 + 16 * (lane & 7);
+        const int index = shift >= 0 ? tb >> shift : tb / part.t.ps;
+        int row = -1;
+        if (lane < 8 && tb < sp.hi && tb + 16 > sp.lo) {
+          const int page = index < part.t.max_pages ? __ldcg(part.t.table + int64_t(sp.row) * part.t.max_pages + index) : -1;
+          if (unsigned(page) < unsigned(part.t.n_pages))
+            row = (page * part.Hkv + cur.g) * (part.t.ps >> 4) + ((tb - index * part.t.ps) >> 4);
+          else
+            record_error(QUAROT_ERR_INVALID_ARG);
+        }
+        const uint32_t st = n % SP;
+        if (n >= SP) wait(raw_empty + st, (n / SP - 1) & 1);
+        const unsigned valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFF;
+        const int before = __shfl_up_sync(0xffffffffu, row, 1);
+        unsigned starts = __ballot_sync(0xffffffffu, row >= 0 && (lane == 0 || before < 0 || row != before + 1)) & 0xFF;
+        const unsigned ends = (starts | ~valid) & 0x1FF;
+        const uint32_t to = sma + C::OFF_RAW + st * C::STAGE;
+        constexpr uint32_t GROUP = 16 * D / 2;
+        if (elect_one()) {
+          to_async_proxy();
+          there[st] = int(valid);
+          mbar_arrive_expect_tx(raw_full + st, __popc(valid) * (2 * GROUP + 64));
+        }
+        while (starts) {
+          const int a = __ffs(starts) - 1;
+          starts &= starts - 1;
+          const int len = __ffs(ends >> (a + 1));
+          const int64_t r = __shfl_sync(0xffffffffu, row, a);
+          if (elect_one()) {
+            bulk_copy(to + a * GROUP, k_q + r * GROUP, len * GROUP, raw_full + st);
+            bulk_copy(to + C::CODES + a * GROUP, v_q + r * GROUP, len * GROUP, raw_full + st);
+            bulk_copy(to + 2 * C::CODES + a * 32, k_s + r * 16, len * 32, raw_full + st);
+            bulk_copy(to + 2 * C::CODES + 2 * TILE + a * 32, v_s + r * 16, len * 32, raw_full + st);
+          }
+        }
+        __syncwarp();
+      }
+      left -= nt;
+      cur.tile += nt;
+      if (left > 0) {
+        next_unit(part, cur);
+        if (cur.tiles == 0) {  // the batch changed under the call: an empty unit ends every role
+          wait(unit_empty, u & 1);
+          if (lane == 0) tell_cursor(cur, cursors + 16 * ((u + 1) & 1));
+          __syncwarp();
+          mbar_arrive(unit_full);
+          if (lane == 0) mbar_arrive(unit_full);
+          break;
+        }
+      }
+    }
+    for (uint32_t m = n < SP ? 0 : n - SP; m < n; ++m) wait(raw_full + m % SP, (m / SP) & 1, true);
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    uint32_t n = 0, units = 0;
+    for (uint32_t u = 0; left > 0; ++u) {
+      cur = unit_at(u);
+      arrive(unit_empty);
+      if (cur.tiles == 0) break;
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      left -= nt;
+      ++units;
+      auto issue_scores = [&](uint32_t m) {
+        const uint32_t d = tmem + COL_S + 128 * (m & 1);
+        const uint64_t kd = desc_sw128(sma + C::OFF_K + (m & 1) * C::ATOM, 1024);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma8_ts(d, tmem + COL_Q + p * (D / 4) + 8 * kk, kd + 2 * kk, idesc8(TILE, false, false), p + kk > 0);
+        mma_commit(s_full + (m & 1));
+        mma_commit(k_empty + (m & 1));
+      };
+      wait(q_full, u & 1);
+      wait(k_full + (n & 1), (n >> 1) & 1);
+      tc_after();
+      if (elect_one()) issue_scores(n);
+      __syncwarp();
+      for (int k = 0; k < nt; ++k, ++n) {
+        if (k + 1 < nt) {
+          // buffer (n + 1) % 2 holds P(n - 1), which O += P(n - 1) V has to have read
+          wait(k_full + ((n + 1) & 1), ((n + 1) >> 1) & 1);
+          if (n > 0) wait(o_done, (n - 1) & 1);
+          tc_after();
+          if (elect_one()) issue_scores(n + 1);
+          __syncwarp();
+        }
+        wait(v_full + (n & 1), (n >> 1) & 1);
+        wait(p_full + (n & 1), (n >> 1) & 1);
+        tc_after();
+        if (elect_one()) {
+          const uint64_t vd = desc_sw128_mn(sma + C::OFF_V + (n & 1) * C::VBYTES, C::ATOM, 1024);
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            mma16_ts(tmem + COL_O, tmem + COL_S + 128 * (n & 1) + 8 * kk, vd + 128 * kk, idesc16(D), k > 0 || kk > 0);
+          mma_commit(o_done);
+          mma_commit(v_empty + (n & 1));
+          if (k + 1 == nt) mma_commit(unit_done);
+        }
+        __syncwarp();
+      }
+    }
+    if (units > 0) wait(unit_done, (units - 1) & 1);
+  } else if (warp < 2 + NCW) {
+    // ================================================================ converters
+    const int cw = warp - 2, r4 = lane >> 2, c4 = lane & 3;
+    const int ctid = 32 * cw + lane;
+    uint32_t n = 0;
+    for (uint32_t u = 0; left > 0; ++u) {
+      cur = unit_at(u);
+      arrive(unit_empty);
+      if (cur.tiles == 0) break;
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      left -= nt;
+      for (int k = 0; k < nt; ++k, ++n) {
+        const Span sp = tile_at(part, cur, cur.tile + k);
+        const uint32_t st = n % SP, b = n & 1;
+        wait(raw_full + st, (n / SP) & 1, true);
+        const uint32_t raw = sma + C::OFF_RAW + st * C::STAGE + (32 * cw + r4) * (D / 2) + c4 * (4 * WPT);
+        const int have = there[st];
+        // words c4 WPT .. of tokens 32 cw + 8 i + r4
+        uint32_t w[4][WPT];
+        auto words = [&](uint32_t from) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t at = from + 8 * (D / 2) * i;
+            if constexpr (WPT == 4)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "r"(at));
+            else
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at));
+          }
+        };
+        // ---- keys
+        words(raw);
+        if (n > 1) wait(k_empty + b, ((n >> 1) - 1) & 1);
+        const uint32_t k_row = sma + C::OFF_K + b * C::ATOM + (32 * cw + r4) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[2 * WPT];
+#pragma unroll
+          for (int j = 0; j < WPT; ++j) bytes_of(w[i][j], masks, o[2 * j], o[2 * j + 1]);
+#pragma unroll
+          for (int h = 0; h < WPT / 2; ++h)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(k_row + 1024 * i + ((((WPT / 2) * c4 + h) ^ r4) << 4)),
+                         "r"(o[4 * h]), "r"(o[4 * h + 1]), "r"(o[4 * h + 2]), "r"(o[4 * h + 3])
+                         : "memory");
+        }
+        to_async_proxy();
+        arrive(k_full + b);
+        // ---- key scales, 0 where the part has no token
+        uint32_t half;
+        const uint32_t scales = sma + C::OFF_RAW + st * C::STAGE + 2 * C::CODES;
+        const int tok = sp.t0 + ctid;
+        const bool mine = tok >= sp.lo && tok < sp.hi && ((have >> (ctid >> 4)) & 1);
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * ctid));
+        if (n > 1) wait(ks_empty + b, ((n >> 1) - 1) & 1);
+        ksf[b * TILE + ctid] = mine ? __half2float(__ushort_as_half(uint16_t(half))) : 0.f;
+        if (ctid == 0) there_s[b] = have;
+        arrive(ks_full + b);
+        // ---- values: fp16 code * scale, pairs (k, k + 4) of a word's dims; 0 where the part has no token
+        words(raw + C::CODES);
+        uint32_t vs2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 32 * cw + 8 * i + r4;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * TILE + 2 * t));
+          const bool in = sp.t0 + t >= sp.lo && sp.t0 + t < sp.hi && ((have >> (t >> 4)) & 1);
+          vs2[i] = in ? half | (half << 16) : 0u;
+        }
+        arrive(raw_empty + st);
+        if (n > 1) wait(v_empty + b, ((n >> 1) - 1) & 1);
+        const uint32_t v_row = sma + C::OFF_V + b * C::VBYTES + (32 * cw + r4) * 128 + (WPT == 4 ? (c4 >> 1) * C::ATOM : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (WPT == 4) {  // lanes of the two halves of a token store different chunks at a time
+            if (c4 & 2) {
+              uint32_t x = w[i][0];
+              w[i][0] = w[i][2], w[i][2] = x;
+              x = w[i][1];
+              w[i][1] = w[i][3], w[i][3] = x;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < WPT; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = hmul2(hadd2(((w[i][j] >> (4 * e)) & vals.mask) ^ vals.flip, 0xE408E408u /* -1032 */), vs2[i]);
+            const uint32_t chunk = WPT == 4 ? uint32_t(4 * (c4 & 1) + (j ^ (c4 & 2))) : uint32_t(2 * c4 + j);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v_row + 1024 * i + ((chunk ^ r4) << 4)), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+          }
+        }
+        to_async_proxy();
+        arrive(v_full + b);
+      }
+    }
+  } else {
+    // ================================================================ softmax
+    const int qd = warp & 3, hh = (warp - 2 - NCW) >> 2;  // lane quadrant; half of the row's columns
+    const int r = 32 * qd + lane;                         // row
+    const uint32_t quad = tmem + (uint32_t(32 * qd) << 16);
+    const int pair = 1 + qd;  // named barrier of the two warps that share the rows
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
+    auto pair_any = [&](bool v) {
+      uint32_t o;
+      asm volatile(
+          "{\n\t.reg .pred p, o;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred o, %2, 64, p;\n\tselp.u32 %0, 1, 0, o;\n\t}"
+          : "=r"(o)
+          : "r"(uint32_t(v)), "r"(pair)
+          : "memory");
+      return o != 0;
+    };
+    // a value of each half of the row, to both
+    auto both = [&](float v, int which) {
+      xch[(2 * which + hh) * ROWS + r] = v;
+      pair_sync();
+      return xch[(2 * which + (hh ^ 1)) * ROWS + r];
+    };
+    uint32_t n = 0;
+    for (uint32_t u = 0; left > 0; ++u) {
+      cur = unit_at(u);
+      if (cur.tiles == 0) {
+        arrive(unit_empty);
+        break;
+      }
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      left -= nt;
+      const Row row = row_of(part, cur.s, cur.j * ROWS + r);
+      // ---- the query: span H over the whole row, then this half's own spans
+      float f, off;
+      {
+        float2 x[H / 2];
+        const uint32_t qr = sma + C::OFF_Q + r * (2 * D);
+#pragma unroll
+        for (int c = 0; c < H / 8; ++c) {
+          uint4 a, b;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(qr + ((c ^ (r & 7)) << 4)));
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(qr + (((c + H / 8) ^ (r & 7)) << 4)));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 lo = fp8::to_f2<T>(aw[k]), hi = fp8::to_f2<T>(bw[k]);
+            x[4 * c + k] = hh == 0 ? __fadd2_rn(lo, hi) : __fadd2_rn(lo, make_float2(-hi.x, -hi.y));
+          }
+        }
+        arrive(unit_empty);
+        hadamard_regs<H>(x);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < H / 2; ++i) amax = max3(amax, fabsf(x[i].x), fabsf(x[i].y));
+        amax = fmaxf(amax, both(amax, 0));
+        // pieces of x * 256 / amax that add up to it: each of 4 bits, off by 2^-15 of the largest in the end
+        const float up = amax > 0.f ? 256.0f / amax : 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          uint32_t o[H / 4];
+#pragma unroll
+          for (int w = 0; w < H / 8; ++w) {
+            // bytes of a word's dims: even ones, then odd ones
+            uint32_t e[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float2 &a = x[4 * w + 2 * k], &b = x[4 * w + 2 * k + 1];  // dims 4 k, 4 k + 1 and 4 k + 2, 4 k + 3
+              if (p == 0) {
+                a = make_float2(a.x * up, a.y * up);
+                b = make_float2(b.x * up, b.y * up);
+              }
+              e[k] = fp8::cvt_e4m3x2(make_float2(a.x, b.x));
+              e[2 + k] = fp8::cvt_e4m3x2(make_float2(a.y, b.y));
+              const float2 ev = h2_to_f2(h2_of_e4m3x2(e[k])), od = h2_to_f2(h2_of_e4m3x2(e[2 + k]));
+              sum += (ev.x + ev.y) + (od.x + od.y);
+              a = make_float2(a.x - ev.x, a.y - od.x);
+              b = make_float2(b.x - ev.y, b.y - od.y);
+            }
+            o[2 * w] = e[0] | (e[1] << 16);
+            o[2 * w + 1] = e[2] | (e[3] << 16);
+          }
+          const uint32_t to = quad + COL_Q + p * (D / 4) + hh * (D / 8);
+          if constexpr (H == 64) tmem_st16(to, o);
+          else tmem_st8(to, o);
+        }
+        tc_wait_st();
+        tc_before();
+        sum += both(sum, 1);
+        arrive(q_full);
+        // of 2^9 of the codes and 1 / 256 of the pieces; never 0, so that a hidden score stays -inf
+        f = fmaxf(2.0f * amax * qscale, 1e-37f);
+        off = sum * (-8.0f / 512.0f);
+      }
+      // ---- tiles
+      float m = kNone, l = 0.f;
+      for (int k = 0; k < nt; ++k, ++n) {
+        const uint32_t b = n & 1;
+        wait(s_full + b, (n >> 1) & 1);
+        wait(ks_full + b, (n >> 1) & 1);
+        tc_after();
+        const uint32_t s_t = quad + COL_S + 128 * b;
+        uint32_t v[64];
+        tmem_ld32(s_t + 64 * hh, v);
+        tmem_ld32(s_t + 64 * hh + 32, v + 32);
+        const Span sp = tile_at(part, cur, cur.tile + k);
+        const int have = there_s[b];
+        tc_wait_ld();
+        const uint32_t kf = smem_u32(ksf + b * TILE + 64 * hh);
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          float4 s4;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s4.x), "=f"(s4.y), "=f"(s4.z), "=f"(s4.w) : "r"(kf + 4 * e));
+          const float2 o2 = make_float2(off, off);
+          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), o2), make_float2(s4.x, s4.y));
+          const float2 c = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), o2), make_float2(s4.z, s4.w));
+          v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y), v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
+        }
+        arrive(ks_empty + b);
+        // columns that this row does not see
+        const int lo = sp.lo - sp.t0 - 64 * hh, hi = min(row.end, sp.hi) - sp.t0 - 64 * hh;
+        if (__any_sync(0xffffffffu, lo > 0 || hi < 64 || have != 0xFF)) {
+          const int h4 = have >> (4 * hh);
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < lo || e >= hi || !((h4 >> (e >> 4)) & 1)) v[e] = __float_as_uint(-INFINITY);
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(v[i]), __uint_as_float(v[4 + i]), __uint_as_float(v[8 + i]));
+#pragma unroll
+        for (int e = 12; e < 60; e += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(v[e + i]), __uint_as_float(v[e + 4 + i]));
+        float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], __uint_as_float(v[60])),
+                          max3(__uint_as_float(v[61]), __uint_as_float(v[62]), __uint_as_float(v[63]))) * f;
+        // behind this barrier both halves' scores are in registers: probabilities may take their columns
+        if (pair_any(top > m + 8.0f)) {
+          top = fmaxf(top, both(top, int(b)));
+          const bool raise = top > m + 8.0f;
+          const float al = raise ? ex2(m - top) : 1.0f;
+          if (raise) m = top;
+          l *= al;
+          if (k > 0) {  // outputs so far follow, once O += P(n - 1) V is over
+            wait(o_done, (n - 1) & 1);
+            tc_after();
+            const uint32_t o_t = quad + COL_O + (D / 2) * hh;
+#pragma unroll 1
+            for (int c = 0; c < H / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_t + 16 * c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tmem_st16(o_t + 16 * c, o);
+            }
+          }
+        }
+        const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, m2);
+          const float2 p = make_float2(ex2(d.x), ex2(d.y));
+          ls[(e >> 1) & 1] = __fadd2_rn(ls[(e >> 1) & 1], p);
+          v[e >> 1] = h2_of_f2(p.x, p.y);
+        }
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        tmem_st16(s_t + 32 * hh, v);
+        tmem_st16(s_t + 32 * hh + 16, v + 16);
+        tc_wait_st();
+        tc_before();
+        arrive(p_full + b);
+      }
+      // ---- the unit's outputs: a state, or, where this CTA had all of its tiles, the result
+      l += both(l, 2);
+      // (S of the last tile was issued before O += P V of the one before it, and a wait for a parity cannot tell a
+      // phase from the one two earlier: the unit's end has a barrier of its own)
+      wait(unit_done, u & 1);
+      tc_after();
+      const bool starts = cur.tile == 0, ends = cur.tile + nt == cur.tiles;
+      const bool direct = todo != nullptr && starts && ends;
+      const uint32_t o_t = quad + COL_O;
+      if (direct) {
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        // dims of columns 8 w + 2 k + e: 8 w + k + 4 e
+        float2 x[H / 2];
+#pragma unroll
+        for (int c = 0; c < H / 16; ++c) {
+          uint32_t a[16], b[16];
+          tmem_ld16(o_t + H * hh + 16 * c, a);
+          if (unrotate) tmem_ld16(o_t + H * (hh ^ 1) + 16 * c, b);
+          tc_wait_ld();
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int p = 8 * w + 2 * (i & 3) + (i >> 2);
+              float y = __uint_as_float(a[p]);
+              if (unrotate) y = hh == 0 ? y + __uint_as_float(b[p]) : __uint_as_float(b[p]) - y;
+              (i & 1 ? x[8 * c + 4 * w + i / 2].y : x[8 * c + 4 * w + i / 2].x) = y;
+            }
+        }
+        float sc = inv;
+        if (unrotate) {
+          hadamard_regs<H>(x);
+          sc *= 1.0f / sqrtf(float(D));
+        }
+        if (row.tok >= 0) {
+          T* dst = out + row.tok * ld_out + int64_t(cur.g * part.G + row.hh) * D + H * hh;
+#pragma unroll
+          for (int c = 0; c < H / 8; ++c) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = fp8::from_f2<T>(make_float2(x[4 * c + i].x * sc, x[4 * c + i].y * sc));
+            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      } else {
+        const int J = (cur.s.rows + ROWS - 1) / ROWS;
+        const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, ROWS) + int64_t(cur.g) * J + cur.j;
+        const int64_t at = ((todo != nullptr ? 2 * int64_t(blockIdx.x) + (starts ? 1 : 0) : unit + blockIdx.x) * ROWS + r);
+#pragma unroll 1
+        for (int c = 0; c < H / 16; ++c) {
+          uint32_t a[16];
+          tmem_ld16(o_t + H * hh + 16 * c, a);
+          tc_wait_ld();
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+              auto at_dim = [&](int d) { return __uint_as_float(a[8 * w + 2 * (d & 3) + (d >> 2)]); };
+              *reinterpret_cast<float4*>(ws.o + at * D + H * hh + 16 * c + 8 * w + i) =
+                  make_float4(at_dim(i), at_dim(i + 1), at_dim(i + 2), at_dim(i + 3));
+            }
+        }
+        if (hh == 0) *reinterpret_cast<float2*>(ws.ml + at * 2) = make_float2(m, l);
+        if (warp == 2 + NCW && lane == 0) {
+          if (todo == nullptr) {
+            if (starts) ws.span[2 * unit] = blockIdx.x;
+            if (ends) ws.span[2 * unit + 1] = blockIdx.x;
+          } else if (ends) {
+            todo[blockIdx.x] = make_int4(int((cur.tile + per - 1) / per), cur.b, cur.g, cur.j);  // CTAs before this one that had tiles of it
+          }
+        }
+      }
+      tc_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// The units that several CTAs had a part in, each joined by 16 CTAs of 8 rows:
+// todo [w] says how many CTAs before w had tiles of the unit that CTA w ended
+// (0: it ended none that it did not begin), and which unit.  Tokens that see
+// nothing, whose units may have had no tile at all, get their zeros here.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+join_units_kernel(Part part, Space ws, const int4* __restrict__ todo, int unrotate, T* __restrict__ out, int64_t ld_out) {
+  __shared__ float x[8][D];
+  fp8::wait_for_previous();
+  for (int n = 8 * (blockIdx.y * gridDim.x + blockIdx.x) + (threadIdx.x >> 5); n < part.N; n += 8 * gridDim.x * gridDim.y) {
+    const Place p = place_of(part.t, n);
+    if (p.b >= 0 && p.pos < 0)
+      for (int e = 8 * (threadIdx.x & 31); e < part.G * part.Hkv * D; e += 256)
+        *reinterpret_cast<uint4*>(out + n * ld_out + e) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int w = blockIdx.x;
+  const int4 t = __ldcg(todo + w);
+  if (t.x <= 0) return;
+  const int before = min(t.x, w);
+  const Seq s = seq_of(part, t.y, false);
+  const int r = 8 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const Row row = row_of(part, s, t.w * ROWS + r);
+  constexpr int E = D / 32;
+  float m = kNone, den = 0.f, num[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) num[e] = 0.f;
+  for (int c = w - before; c <= w; ++c) {
+    const int64_t at = (2 * int64_t(c) + (c == w - before ? 1 : 0)) * ROWS + r;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(ws.ml + at * 2));
+    const float mx = fmaxf(m, ml.x), a = ex2(m - mx), f = ex2(ml.x - mx);
+    m = mx;
+    den = den * a + ml.y * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) num[e] = num[e] * a + f * __ldcg(ws.o + at * D + lane + 32 * e);
+  }
+  const float inv = den > 0.f ? 1.0f / den : 0.f;
+  float* y = x[threadIdx.x >> 5];
+#pragma unroll
+  for (int e = 0; e < E; ++e) num[e] *= inv;
+  if (unrotate) {
+    for (int span = 1; span < D; span <<= 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[lane + 32 * e] = num[e];
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float other = y[(lane + 32 * e) ^ span];
+        num[e] = ((lane + 32 * e) & span) ? other - num[e] : num[e] + other;
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) num[e] *= 1.0f / sqrtf(float(D));
+  }
+  if (row.tok >= 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[row.tok * ld_out + int64_t(t.z * part.G + row.hh) * D + lane + 32 * e] = T(num[e]);
+  }
+}
+
+}  // namespace many
+
 // ------------------------------------------------------------------ join
 // One CTA per (token, query head): o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i
 // over the states of the row's unit of each part, d of them at a time.  A thread
@@ -1051,26 +1815,38 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
 }
 
 // ------------------------------------------------------------------ host
+// Which kernel a part gets, by the rows that see the same keys: up to 16, the
+// tokens as the MMA's M (each 4, 8 or 16 rows read the keys once); above, the
+// rows.  Sequences of more new rows than that are worked on whole, the shared
+// tokens with their own: the keys are read for every 128 rows anyway.
 struct Plan {
+  bool many;
   int RP, ctas;
   int64_t units;
 };
-inline int rows_of_unit(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
-inline int ctas_per_sm(int RP) { return RP == 4 ? few::ctas_per_sm<4>() : RP == 8 ? few::ctas_per_sm<8>() : few::ctas_per_sm<16>(); }
-inline Plan plan_own(int64_t N, int64_t B, int64_t G, int64_t Hkv, int64_t max_q, int sms) {
+inline Plan plan(int64_t rows, int64_t N, int64_t B, int64_t G, int64_t Hkv, int sms) {
   Plan p;
-  p.RP = rows_of_unit(max_q * G);
-  p.ctas = sms * ctas_per_sm(p.RP);
+  p.many = rows > 16;
+  p.RP = p.many ? many::ROWS : rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+  p.ctas = sms * (p.many ? 1 : p.RP == 4 ? few::ctas_per_sm<4>() : p.RP == 8 ? few::ctas_per_sm<8>() : few::ctas_per_sm<16>());
   p.units = unit_count(N, B, G, Hkv, p.RP);
   return p;
 }
-inline Plan plan_prefix(int64_t N, int64_t G, int64_t Hkv, int64_t shared, int sms) {
-  Plan p = {4, 0, 0};
-  if (shared == 0) return p;
-  p.RP = rows_of_unit(N * G);
-  p.ctas = sms * ctas_per_sm(p.RP);
-  p.units = unit_count(N, 1, G, Hkv, p.RP);
-  return p;
+struct Call {
+  Plan own, pre;
+  bool prefix;  // there is a part of its own for the shared tokens
+  size_t bytes;
+};
+inline size_t whole_bytes(int64_t ctas, int64_t d) { return round256(size_t(ctas) * 16) + space_bytes(0, 2 * ctas, many::ROWS, d); }
+inline bool plan_call(int64_t N, int64_t B, int64_t G, int64_t Hkv, int64_t d, int64_t max_q, int64_t shared, Call* c) {
+  int sms = 0;
+  if (!sm_count(&sms)) return false;
+  c->own = plan((max_q < N ? max_q : N) * G, N, B, G, Hkv, sms);
+  c->pre = plan(N * G, N, 1, G, Hkv, sms);
+  c->prefix = shared > 0 && !c->own.many;
+  c->bytes = c->own.many ? whole_bytes(c->own.ctas, d) : space_bytes(c->own.units, c->own.ctas, c->own.RP, d);
+  if (c->prefix) c->bytes += space_bytes(c->pre.units, c->pre.ctas, c->pre.RP, d);
+  return true;
 }
 
 }  // namespace paged
@@ -1084,31 +1860,51 @@ extern "C" size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq,
   if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_q <= 0 || shared_len < 0 ||
       N > kMaxTokens || B > kMaxTokens || Hq > kMaxHeads)
     return 0;
-  int sms = 0;
-  if (!sm_count(&sms)) return 0;
-  const int64_t mq = max_q < N ? max_q : N;
-  const Plan own = plan_own(N, B, Hq / Hkv, Hkv, mq, sms), pre = plan_prefix(N, Hq / Hkv, Hkv, shared_len, sms);
-  return space_bytes(own.units, own.ctas, own.RP, d) + space_bytes(pre.units, pre.ctas, pre.RP, d);
+  Call c;
+  return plan_call(N, B, Hq / Hkv, Hkv, d, max_q, shared_len, &c) ? c.bytes : 0;
 }
 
 template <typename T, int D>
 static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half* k_s, const uint8_t* v_q, const __half* v_s,
-                     const Part& own, const Plan& po, const Space& so, const Part& pre, const Plan& pp, const Space& sp, int Hq,
-                     float qscale, int unrotate, T* out, int64_t ld_out, cudaStream_t st) {
+                     Part own, const Call& call, unsigned char* work, int Hq, float qscale, int unrotate, T* out,
+                     int64_t ld_out, cudaStream_t st) {
+  const Masks masks = {0x0F0F0F0Fu, 0x08080808u};
   auto few_part = [&](const Part& part, const Plan& plan, const Space& ws, int behind) -> int {
     auto go = [&](auto kern, size_t smem, AttrCache& attr) {
       if (!smem_attr_once(kern, int(smem), attr)) return int(QUAROT_ERR_LAUNCH);
       return fp8::launch_dependent(kern, dim3(unsigned(plan.ctas)), few::NT, smem, 1, st, q, ld_q, k_q, k_s, v_q, v_s, part,
-                                   qscale, ws, behind, Masks{0x0F0F0F0Fu, 0x08080808u});
+                                   qscale, ws, behind, masks);
     };
     static AttrCache attr[3];
     if (plan.RP == 4) return go(few::few_kernel<T, 4, D>, few::Cfg<4, D>::SMEM, attr[0]);
     if (plan.RP == 8) return go(few::few_kernel<T, 8, D>, few::Cfg<8, D>::SMEM, attr[1]);
     return go(few::few_kernel<T, 16, D>, few::Cfg<16, D>::SMEM, attr[2]);
   };
+  auto many_part = [&](const Part& part, const Plan& plan, const Space& ws, int4* todo) -> int {
+    static AttrCache attr;
+    auto kern = many::many_kernel<T, D>;
+    if (!smem_attr_once(kern, many::Cfg<D>::SMEM, attr)) return QUAROT_ERR_LAUNCH;
+    return fp8::launch_dependent(kern, dim3(unsigned(plan.ctas)), many::NT, many::Cfg<D>::SMEM, 1, st, q, ld_q, k_q, k_s, v_q, v_s,
+                                 part, qscale, ws, todo, unrotate, out, ld_out, masks, many::Values{0x000F000Fu, 0x64086408u});
+  };
+  const Plan &po = call.own, &pp = call.pre;
+  own.RP = po.RP;
   int rc = QUAROT_OK;
-  if (pre.shared > 0 && (rc = few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
-  if ((rc = few_part(own, po, so, pre.shared > 0)) != QUAROT_OK) return rc;
+  if (po.many) {
+    own.whole = 1;
+    int4* todo = reinterpret_cast<int4*>(work);
+    const Space ws = space_at(work + round256(size_t(po.ctas) * 16), 0, 2 * po.ctas, po.RP);
+    if ((rc = many_part(own, po, ws, todo)) != QUAROT_OK) return rc;
+    return fp8::launch_dependent(many::join_units_kernel<T, D>, dim3(unsigned(po.ctas), 16), 256, 0, 1, st, own, ws,
+                                 static_cast<const int4*>(todo), unrotate, out, ld_out);
+  }
+  const Space so = space_at(work, po.units, po.ctas, po.RP);
+  const Space sp = space_at(work + space_bytes(po.units, po.ctas, po.RP, D), pp.units, pp.ctas, pp.RP);
+  Part pre = own;
+  pre.prefix = 1;
+  pre.RP = pp.RP;
+  if (call.prefix && (rc = pp.many ? many_part(pre, pp, sp, nullptr) : few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
+  if ((rc = few_part(own, po, so, call.prefix)) != QUAROT_OK) return rc;
   return fp8::launch_dependent(join_kernel<T, D>, dim3(unsigned(own.N) * unsigned(Hq)), D, 0, 1, st, own, so, pre, sp, Hq,
                                unrotate, out, ld_out);
 }
@@ -1130,24 +1926,21 @@ extern "C" int quarot_paged_attn(const void* q, int64_t ld_q, int dtype, int64_t
   if ((rc = check_cache(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_pages)) != QUAROT_OK) return rc;
   if (!workspace) return QUAROT_ERR_INVALID_ARG;
   if (misaligned(workspace, 256)) return QUAROT_ERR_ALIGNMENT;
-  if (ws_bytes < quarot_paged_workspace_bytes(N, B, Hq, Hkv, d, max_q, shared_len)) return QUAROT_ERR_INVALID_ARG;
-  int sms = 0;
-  if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
-  const int64_t G = Hq / Hkv, mq = max_q < N ? max_q : N;
-  const Plan po = plan_own(N, B, G, Hkv, mq, sms), pp = plan_prefix(N, G, Hkv, shared_len, sms);
+  Call call;
+  const int64_t G = Hq / Hkv;
+  if (!plan_call(N, B, G, Hkv, d, max_q, shared_len, &call)) return QUAROT_ERR_CUDA;
+  if (ws_bytes < call.bytes) return QUAROT_ERR_INVALID_ARG;
   const Batch t = {page_table, lengths, cu_q, int(B), int(max_pages), int(n_pages), int(page_size)};
-  const Part own = {t, int(N), int(G), int(Hkv), int(shared_len), 0, po.RP}, pre = {t, int(N), int(G), int(Hkv), int(shared_len), 1, pp.RP};
-  unsigned char* w = static_cast<unsigned char*>(workspace);
-  const Space so = space_at(w, po.units, po.ctas, po.RP);
-  const Space sp = space_at(w + space_bytes(po.units, po.ctas, po.RP, d), pp.units, pp.ctas, pp.RP);
+  const Part own = {t, int(N), int(G), int(Hkv), int(shared_len), 0, 0, 0};
   const float qscale = (sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(float(d))) * 1.4426950408889634f / sqrtf(float(d));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto* ksh = static_cast<const __half*>(k_s);
   auto* vsh = static_cast<const __half*>(v_s);
   auto typed = [&](auto* qp, auto* op) {
     using T = std::remove_pointer_t<decltype(op)>;
-    return d == 64 ? attn_impl<T, 64>(qp, ld_q, k_q, ksh, v_q, vsh, own, po, so, pre, pp, sp, int(Hq), qscale, unrotate_out, op, ld_out, st)
-                   : attn_impl<T, 128>(qp, ld_q, k_q, ksh, v_q, vsh, own, po, so, pre, pp, sp, int(Hq), qscale, unrotate_out, op, ld_out, st);
+    unsigned char* work = static_cast<unsigned char*>(workspace);
+    return d == 64 ? attn_impl<T, 64>(qp, ld_q, k_q, ksh, v_q, vsh, own, call, work, int(Hq), qscale, unrotate_out, op, ld_out, st)
+                   : attn_impl<T, 128>(qp, ld_q, k_q, ksh, v_q, vsh, own, call, work, int(Hq), qscale, unrotate_out, op, ld_out, st);
   };
   if (dtype == QUAROT_FP16) return typed(static_cast<const __half*>(q), static_cast<__half*>(out));
   return typed(static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out));
