@@ -950,8 +950,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // Up to 128 rows of a unit, rows as the MMA's M: a row's scores are one
 // thread pair's, its probabilities go back to tensor memory as the A operand
 // of O += P V without a word between lanes.  The warps of a CTA (one on an SM):
-//   warp 0      feeder: pages, copies of packed tiles (three ahead), the next
-//               unit's queries
+//   warp 0      feeder: pages, copies of packed tiles, three ahead
 //   warp 1      MMA issuer
 //   warps 2-5   converters: key codes to e4m3 bytes (bytes_of, rows of a
 //               swizzled K-major operand); values to fp16 code * scale, token
@@ -959,6 +958,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 //   warps 6-13  softmax, two to a lane quadrant, each half a row: queries
 //               rotated and split into e4m3 pieces at a unit's start, scores to
 //               probabilities, outputs at its end
+//   warp 14     the next unit: which it is, and its queries
 // Tensor memory: the three pieces of the queries (A operand of S), two score
 // buffers, of which fp16 probabilities take the first half, and O.  S(n + 1)
 // runs while the softmax works on S(n).
@@ -971,7 +971,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // P V a tile, some 90 clocks each.
 namespace many {
 
-constexpr int NT = 448, ROWS = 128, NCW = 4, NSW = 8, SP = 3, UNIT_READERS = 1 + NCW + NSW;
+constexpr int NT = 480, ROWS = 128, NCW = 4, NSW = 8, SP = 3, UNIT_READERS = 2 + NCW + NSW;
 constexpr uint32_t COL_Q = 0, COL_S = 128, COL_O = 384;  // S buffer b at COL_S + 128 b
 
 template <int D>
@@ -1168,22 +1168,11 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
     const int shift = (part.t.ps & (part.t.ps - 1)) == 0 ? __ffs(part.t.ps) - 1 : -1;
     uint32_t n = 0;
     for (uint32_t u = 0; left > 0; ++u) {
+      cur = unit_at(u);
+      arrive(unit_empty);
+      if (cur.tiles == 0) break;
       const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
-      // ---- the unit: cursor, queries
-      if (u > 0) wait(unit_empty, (u - 1) & 1);
-      if (lane == 0) tell_cursor(cur, cursors + 16 * (u & 1));
-      for (int c = lane; c < ROWS * (D / 8); c += 32) {
-        const int r = c / (D / 8), ch = c % (D / 8), rr = cur.j * ROWS + r;
-        const int i = rr / part.G;
-        const bool in = rr < cur.s.rows;
-        const T* src = q + (in ? (cur.s.tok0 + i) * ld_q + int64_t(cur.g * part.G + rr - i * part.G) * D + 8 * ch : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sma + C::OFF_Q + r * (2 * D) + ((ch ^ (r & 7)) << 4)),
-                     "l"(src), "r"(in ? 16 : 0)
-                     : "memory");
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(unit_full)) : "memory");
-      if (lane == 0) mbar_arrive(unit_full);
-      // ---- its tiles
+      left -= nt;
       for (int k = 0; k < nt; ++k, ++n) {
         const Span sp = tile_at(part, cur, cur.tile + k);
         const int tb = sp.t0 + 16 * (lane & 7);
@@ -1222,19 +1211,6 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           }
         }
         __syncwarp();
-      }
-      left -= nt;
-      cur.tile += nt;
-      if (left > 0) {
-        next_unit(part, cur);
-        if (cur.tiles == 0) {  // the batch changed under the call: an empty unit ends every role
-          wait(unit_empty, u & 1);
-          if (lane == 0) tell_cursor(cur, cursors + 16 * ((u + 1) & 1));
-          __syncwarp();
-          mbar_arrive(unit_full);
-          if (lane == 0) mbar_arrive(unit_full);
-          break;
-        }
       }
     }
     for (uint32_t m = n < SP ? 0 : n - SP; m < n; ++m) wait(raw_full + m % SP, (m / SP) & 1, true);
@@ -1384,6 +1360,32 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         arrive(v_full + b);
       }
     }
+  } else if (warp == 2 + NCW + NSW) {
+    // ================================================================ units
+    for (uint32_t u = 0; left > 0; ++u) {
+      if (u > 0) wait(unit_empty, (u - 1) & 1);
+      if (lane == 0) tell_cursor(cur, cursors + 16 * (u & 1));
+#pragma unroll 1
+      for (int r = lane; r < ROWS; r += 32) {
+        const int rr = cur.j * ROWS + r, i = rr / part.G;
+        const bool in = rr < cur.s.rows && cur.tiles > 0;
+        const T* src = q + (in ? (cur.s.tok0 + i) * ld_q + int64_t(cur.g * part.G + rr - i * part.G) * D : 0);
+        const uint32_t dst = sma + C::OFF_Q + r * (2 * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + ((c ^ (r & 7)) << 4)), "l"(src + 8 * c),
+                       "r"(in ? 16 : 0)
+                       : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(unit_full)) : "memory");
+      if (lane == 0) mbar_arrive(unit_full);
+      if (cur.tiles == 0) break;  // the batch changed under the call: an empty unit ends every role
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      left -= nt;
+      cur.tile += nt;
+      if (left > 0) next_unit(part, cur);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ================================================================ softmax
     const int qd = warp & 3, hh = (warp - 2 - NCW) >> 2;  // lane quadrant; half of the row's columns
