@@ -295,8 +295,8 @@ ATTN = [
     ([300], [300], 64, 2, 2, 128, 0),
     ([9, 3, 20], [2, 3, 1], 16, 2, 8, 128, 0),                    # drafts of a few tokens
     ([9, 3, 2000], [2, 5, 4], 16, 2, 8, 128, 0),                  # a sequence shorter than its new tokens
-    ([0, 300, 130], [150, 140, 200], 64, 2, 4, 128, 0),           # whole tiles of rows that see nothing
-    ([2000, 900], [1000, 3], 64, 4, 16, 64, 333),                 # units of several CTAs, a prefix among them
+    ([0, 200, 130], [70, 40, 140], 64, 2, 4, 128, 0),             # whole tiles of rows that see nothing
+    ([2000, 900], [150, 3], 64, 2, 4, 64, 333),                   # units of several CTAs, a prefix among them
 ]
 
 

@@ -245,7 +245,7 @@ struct Cursor {
   int b, g, j, tile, tiles;  // unit (b, g, j), next of its tiles, all of them
   Seq s;
 };
-// Sums over the block: of the threads up to this one, and (returned) of all.  sh: a word a warp, at most 16.
+// Sums over the block: of the threads up to this one, and (returned) of all.  sh: a word a warp, at most 24.
 __device__ __forceinline__ int64_t block_scan(int64_t& v, int64_t* sh) {
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
@@ -275,7 +275,7 @@ __device__ __forceinline__ Cursor told_cursor(const int* sh) {
   return {sh[0], sh[1], sh[2], sh[3], sh[4], {sh[5], sh[6], sh[7], sh[8], sh[9]}};
 }
 // Sets the cursor to this CTA's first tile (the row of all tiles is cut into
-// equal parts, the last ones maybe none) and returns how many it has.  sh: 26 words of shared memory.
+// equal parts, the last ones maybe none) and returns how many it has.  sh: 34 words of shared memory.
 // per: the tiles of each but the last CTAs.
 __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t& per, int64_t* sh) {
   const int n = blockDim.x, nseq = p.prefix ? 1 : p.t.B, tid = threadIdx.x;
@@ -290,7 +290,7 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t&
   const int64_t own = head * p.Hkv;
   int64_t first = own, sum = own;
   for (int b = tid + n; b < nseq; b += n) sum += steps_of(p, seq_of(p, b, tell)) * p.Hkv;
-  if (tid == 0) sh[16] = 0;  // whether some thread found the tile
+  if (tid == 0) sh[24] = 0;  // whether some thread found the tile
   int64_t all = block_scan(first, sh), total = all;
   if (nseq > n) total = block_scan(sum, sh);
   if (total == 0) return 0;
@@ -317,11 +317,11 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t&
         }
       }
       c.tile = int(rest);
-      tell_cursor(c, reinterpret_cast<int*>(sh + 18));
-      sh[16] = 1;
+      tell_cursor(c, reinterpret_cast<int*>(sh + 26));
+      sh[24] = 1;
     }
     __syncthreads();
-    if (sh[16] != 0) break;
+    if (sh[24] != 0) break;
     done += all;
     b0 += n;
     if (b0 >= nseq) return 0;  // the batch changed under the call
@@ -334,7 +334,7 @@ __device__ __forceinline__ int64_t find_start(const Part& p, Cursor& c, int64_t&
     x = v;
     all = block_scan(x, sh);
   }
-  c = told_cursor(reinterpret_cast<int*>(sh + 18));
+  c = told_cursor(reinterpret_cast<int*>(sh + 26));
   __syncthreads();
   return min(per, total - at);
 }
@@ -427,7 +427,7 @@ struct Cfg {
   static constexpr int OFF_RV = OFF_RK + 2 * CODES;            // packed values and scales, two tiles
   static constexpr int OFF_ROW = OFF_RV + 2 * STAGE_V;         // four numbers a row
   static constexpr int OFF_X = OFF_ROW + RP * 16;              // float [4][2 RP] exchange
-  static constexpr int OFF_CUR = OFF_X + 4 * 2 * RP * 4;       // the next cursor; find_start's words begin 144 bytes before
+  static constexpr int OFF_CUR = OFF_X + 4 * 2 * RP * 4;       // the next cursor; find_start's words begin 208 bytes before
   static constexpr int OFF_BAR = OFF_CUR + 64;
   static constexpr int SMEM = OFF_BAR + 80;
 };
@@ -485,7 +485,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
   const Batch& bt = part.t;
   Cursor cur;
   int64_t per;
-  int64_t left = find_start(part, cur, per, reinterpret_cast<int64_t*>(sm + C::OFF_CUR - 144));
+  int64_t left = find_start(part, cur, per, reinterpret_cast<int64_t*>(sm + C::OFF_CUR - 208));
   // A wait ends after about a second (each try sleeps some microseconds) and is
   // recorded.  Once one gave up, waits for MMAs end at once; copies are waited
   // for all the same, so that none is in flight when the CTA ends.
@@ -955,13 +955,13 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 //   warps 2-5   converters: key codes to e4m3 bytes (bytes_of, rows of a
 //               swizzled K-major operand); values to fp16 code * scale, token
 //               after token (the B operand with N running fastest: no transpose)
-//   warps 6-13  softmax, two to a lane quadrant, each half a row: queries
-//               rotated and split into e4m3 pieces at a unit's start, scores to
-//               probabilities, outputs at its end
-//   warp 14     the next unit: which it is, and its queries
+//   warps 6-21  softmax, four to a lane quadrant, each a quarter of its rows:
+//               queries rotated and split into e4m3 pieces at a unit's start,
+//               scores to probabilities, outputs at its end
+//   warp 22     the next unit: which it is, and its queries
 // Tensor memory: the three pieces of the queries (A operand of S), two score
-// buffers, of which fp16 probabilities take the first half, and O.  S(n + 1)
-// runs while the softmax works on S(n).
+// buffers, in which fp16 probabilities take the place of the scores that they
+// were made from, and O.  S(n + 1) runs while the softmax works on S(n).
 //
 // A score is (S - off) ks f with off = 8 sum q~ (the codes' offset) and f the
 // row's factor; the references are raised as in `few`, without the value
@@ -971,7 +971,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // P V a tile, some 90 clocks each.
 namespace many {
 
-constexpr int NT = 480, ROWS = 128, NCW = 4, NSW = 8, SP = 3, UNIT_READERS = 2 + NCW + NSW;
+constexpr int NT = 736, ROWS = 128, NCW = 4, NSW = 16, SP = 3, UNIT_READERS = 2 + NCW + NSW;
 constexpr uint32_t COL_Q = 0, COL_S = 128, COL_O = 384;  // S buffer b at COL_S + 128 b
 
 template <int D>
@@ -986,8 +986,8 @@ struct Cfg {
   static constexpr int OFF_Q = OFF_V + 2 * VBYTES;     // the unit's queries, 16-byte chunks swizzled
   static constexpr int OFF_RAW = OFF_Q + ROWS * D * 2;
   static constexpr int OFF_KS = OFF_RAW + SP * STAGE;  // float [2][TILE] key scales of the score buffers
-  static constexpr int OFF_X = OFF_KS + 2 * TILE * 4;  // float [2][ROWS] exchange of a row's halves, three times; at first find_start's words
-  static constexpr int OFF_CUR = OFF_X + 6 * ROWS * 4; // cursors of two units
+  static constexpr int OFF_X = OFF_KS + 2 * TILE * 4;  // float [4][ROWS] exchange of a row's quarters, three times; at first find_start's words
+  static constexpr int OFF_CUR = OFF_X + 12 * ROWS * 4; // cursors of two units
   static constexpr int OFF_BAR = OFF_CUR + 128;
   static constexpr int NBAR = 2 * SP + 4 + 4 + 3 + 8 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -1009,9 +1009,9 @@ __device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t addr, uint32_t lbo, u
   return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
          (uint64_t(2) << 61);
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* r) {
-  tmem_ld16(t, r);
-  tmem_ld16(t + 16, r + 16);
+__device__ __forceinline__ void tmem_st4(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -1077,7 +1077,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             const uint8_t* __restrict__ v_q, const __half* __restrict__ v_s, Part part, float qscale, Space ws, int4* todo,
             int unrotate, T* __restrict__ out, int64_t ld_out, Masks masks, Values vals) {
   using C = Cfg<D>;
-  constexpr int WPT = C::WPT, H = D / 2;  // H: elements of a thread's half row
+  constexpr int WPT = C::WPT, E = D / 4;  // E: elements of a thread's quarter of a row
   extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t sma = smem_u32(sm);
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
@@ -1098,7 +1098,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   volatile int* there = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);      // [SP] groups of 16 tokens that a packed tile has
-  volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers
+  volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers; 0x100: all tokens are there
   float* ksf = reinterpret_cast<float*>(sm + C::OFF_KS);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
   int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [2][16]
@@ -1256,7 +1256,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           const uint64_t vd = desc_sw128_mn(sma + C::OFF_V + (n & 1) * C::VBYTES, C::ATOM, 1024);
 #pragma unroll
           for (int kk = 0; kk < TILE / 16; ++kk)
-            mma16_ts(tmem + COL_O, tmem + COL_S + 128 * (n & 1) + 8 * kk, vd + 128 * kk, idesc16(D), k > 0 || kk > 0);
+            mma16_ts(tmem + COL_O, tmem + COL_S + 128 * (n & 1) + 32 * (kk >> 1) + 8 * (kk & 1), vd + 128 * kk, idesc16(D), k > 0 || kk > 0);
           mma_commit(o_done);
           mma_commit(v_empty + (n & 1));
           if (k + 1 == nt) mma_commit(unit_done);
@@ -1319,7 +1319,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * ctid));
         if (n > 1) wait(ks_empty + b, ((n >> 1) - 1) & 1);
         ksf[b * TILE + ctid] = mine ? __half2float(__ushort_as_half(uint16_t(half))) : 0.f;
-        if (ctid == 0) there_s[b] = have;
+        if (ctid == 0) there_s[b] = have | (have == 0xFF && sp.t0 >= sp.lo && sp.t0 + TILE <= sp.hi ? 0x100 : 0);
         arrive(ks_full + b);
         // ---- values: fp16 code * scale, pairs (k, k + 4) of a word's dims; 0 where the part has no token
         words(raw + C::CODES);
@@ -1388,25 +1388,30 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ================================================================ softmax
-    const int qd = warp & 3, hh = (warp - 2 - NCW) >> 2;  // lane quadrant; half of the row's columns
+    const int qd = warp & 3, qq = (warp - 2 - NCW) >> 2;  // lane quadrant; quarter of the row's columns
     const int r = 32 * qd + lane;                         // row
     const uint32_t quad = tmem + (uint32_t(32 * qd) << 16);
-    const int pair = 1 + qd;  // named barrier of the two warps that share the rows
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
-    auto pair_any = [&](bool v) {
+    const int group = 1 + qd;  // named barrier of the four warps that share the rows
+    auto group_any = [&](bool v) {
       uint32_t o;
       asm volatile(
-          "{\n\t.reg .pred p, o;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred o, %2, 64, p;\n\tselp.u32 %0, 1, 0, o;\n\t}"
+          "{\n\t.reg .pred p, o;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred o, %2, 128, p;\n\tselp.u32 %0, 1, 0, o;\n\t}"
           : "=r"(o)
-          : "r"(uint32_t(v)), "r"(pair)
+          : "r"(uint32_t(v)), "r"(group)
           : "memory");
       return o != 0;
     };
-    // a value of each half of the row, to both
-    auto both = [&](float v, int which) {
-      xch[(2 * which + hh) * ROWS + r] = v;
-      pair_sync();
-      return xch[(2 * which + (hh ^ 1)) * ROWS + r];
+    // the values of the row's quarters, to all of them
+    auto all_four = [&](float v, int which) {
+      float* x = xch + 4 * ROWS * which + r;
+      x[ROWS * qq] = v;
+      asm volatile("bar.sync %0, 128;" ::"r"(group) : "memory");
+      return make_float4(x[0], x[ROWS], x[2 * ROWS], x[3 * ROWS]);
+    };
+    // of the row's quarters a .. d what spans E and 2 E leave in this one
+    auto spans = [&](float2 a, float2 b, float2 c, float2 d) {
+      const float2 s1 = make_float2(qq & 1 ? -1.f : 1.f, qq & 1 ? -1.f : 1.f), s2 = make_float2(qq & 2 ? -1.f : 1.f, qq & 2 ? -1.f : 1.f);
+      return __ffma2_rn(__ffma2_rn(d, s1, c), s2, __ffma2_rn(b, s1, a));
     };
     uint32_t n = 0;
     for (uint32_t u = 0; left > 0; ++u) {
@@ -1418,46 +1423,49 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
       left -= nt;
       const Row row = row_of(part, cur.s, cur.j * ROWS + r);
-      // ---- the query: span H over the whole row, then this half's own spans
+      // tiles of the unit that every row of the warp sees all tokens of (where the part has them all)
+      const int all_see = __reduce_min_sync(0xffffffffu, row.end);
+      int clear = cur.tile;
+      while (clear < cur.tile + nt && tile_at(part, cur, clear).t0 + TILE <= all_see) ++clear;
+      // ---- the query: spans over the whole row, then this quarter's own
       float f, off;
       {
-        float2 x[H / 2];
+        float2 x[E / 2];
         const uint32_t qr = sma + C::OFF_Q + r * (2 * D);
 #pragma unroll
-        for (int c = 0; c < H / 8; ++c) {
-          uint4 a, b;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(qr + ((c ^ (r & 7)) << 4)));
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(qr + (((c + H / 8) ^ (r & 7)) << 4)));
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        for (int c = 0; c < E / 8; ++c) {
+          uint32_t w[4][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 lo = fp8::to_f2<T>(aw[k]), hi = fp8::to_f2<T>(bw[k]);
-            x[4 * c + k] = hh == 0 ? __fadd2_rn(lo, hi) : __fadd2_rn(lo, make_float2(-hi.x, -hi.y));
-          }
+          for (int k = 0; k < 4; ++k)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
+                         : "r"(qr + (((c + k * (E / 8)) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[4 * c + i] = spans(fp8::to_f2<T>(w[0][i]), fp8::to_f2<T>(w[1][i]), fp8::to_f2<T>(w[2][i]), fp8::to_f2<T>(w[3][i]));
         }
         arrive(unit_empty);
-        hadamard_regs<H>(x);
+        hadamard_regs<E>(x);
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < H / 2; ++i) amax = max3(amax, fabsf(x[i].x), fabsf(x[i].y));
-        amax = fmaxf(amax, both(amax, 0));
+        for (int i = 0; i < E / 2; ++i) amax = max3(amax, fabsf(x[i].x), fabsf(x[i].y));
+        float4 all = all_four(amax, 0);
+        amax = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
         // pieces of x * 256 / amax that add up to it: each of 4 bits, off by 2^-15 of the largest in the end
         const float up = amax > 0.f ? 256.0f / amax : 0.f;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) x[i] = __fmul2_rn(x[i], make_float2(up, up));
         float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < 3; ++p) {
-          uint32_t o[H / 4];
+          uint32_t o[E / 4];
 #pragma unroll
-          for (int w = 0; w < H / 8; ++w) {
+          for (int w = 0; w < E / 8; ++w) {
             // bytes of a word's dims: even ones, then odd ones
             uint32_t e[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float2 &a = x[4 * w + 2 * k], &b = x[4 * w + 2 * k + 1];  // dims 4 k, 4 k + 1 and 4 k + 2, 4 k + 3
-              if (p == 0) {
-                a = make_float2(a.x * up, a.y * up);
-                b = make_float2(b.x * up, b.y * up);
-              }
               e[k] = fp8::cvt_e4m3x2(make_float2(a.x, b.x));
               e[2 + k] = fp8::cvt_e4m3x2(make_float2(a.y, b.y));
               const float2 ev = h2_to_f2(h2_of_e4m3x2(e[k])), od = h2_to_f2(h2_of_e4m3x2(e[2 + k]));
@@ -1468,13 +1476,14 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             o[2 * w] = e[0] | (e[1] << 16);
             o[2 * w + 1] = e[2] | (e[3] << 16);
           }
-          const uint32_t to = quad + COL_Q + p * (D / 4) + hh * (D / 8);
-          if constexpr (H == 64) tmem_st16(to, o);
-          else tmem_st8(to, o);
+          const uint32_t to = quad + COL_Q + p * (D / 4) + qq * (D / 16);
+          if constexpr (E == 32) tmem_st8(to, o);
+          else tmem_st4(to, o);
         }
         tc_wait_st();
         tc_before();
-        sum += both(sum, 1);
+        all = all_four(sum, 1);
+        sum = (all.x + all.y) + (all.z + all.w);
         arrive(q_full);
         // of 2^9 of the codes and 1 / 256 of the pieces; never 0, so that a hidden score stays -inf
         f = fmaxf(2.0f * amax * qscale, 1e-37f);
@@ -1487,44 +1496,44 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         wait(s_full + b, (n >> 1) & 1);
         wait(ks_full + b, (n >> 1) & 1);
         tc_after();
-        const uint32_t s_t = quad + COL_S + 128 * b;
-        uint32_t v[64];
-        tmem_ld32(s_t + 64 * hh, v);
-        tmem_ld32(s_t + 64 * hh + 32, v + 32);
-        const Span sp = tile_at(part, cur, cur.tile + k);
+        const uint32_t s_t = quad + COL_S + 128 * b + 32 * qq;
+        uint32_t v[32];
+        tmem_ld16(s_t, v);
+        tmem_ld16(s_t + 16, v + 16);
         const int have = there_s[b];
-        tc_wait_ld();
-        const uint32_t kf = smem_u32(ksf + b * TILE + 64 * hh);
+        const uint32_t kf = smem_u32(ksf + b * TILE + 32 * qq);
+        float4 s4[8];
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          float4 s4;
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s4.x), "=f"(s4.y), "=f"(s4.z), "=f"(s4.w) : "r"(kf + 4 * e));
-          const float2 o2 = make_float2(off, off);
-          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), o2), make_float2(s4.x, s4.y));
-          const float2 c = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), o2), make_float2(s4.z, s4.w));
+        for (int e = 0; e < 8; ++e)
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s4[e].x), "=f"(s4[e].y), "=f"(s4[e].z), "=f"(s4[e].w) : "r"(kf + 16 * e));
+        tc_wait_ld();
+        const float2 o2 = make_float2(off, off);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), o2), make_float2(s4[e / 4].x, s4[e / 4].y));
+          const float2 c = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), o2), make_float2(s4[e / 4].z, s4[e / 4].w));
           v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y), v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
         }
         arrive(ks_empty + b);
-        // columns that this row does not see
-        const int lo = sp.lo - sp.t0 - 64 * hh, hi = min(row.end, sp.hi) - sp.t0 - 64 * hh;
-        if (__any_sync(0xffffffffu, lo > 0 || hi < 64 || have != 0xFF)) {
-          const int h4 = have >> (4 * hh);
+        if (!(have & 0x100) || cur.tile + k >= clear) {  // columns that this row does not see
+          const Span sp = tile_at(part, cur, cur.tile + k);
+          const int lo = sp.lo - sp.t0 - 32 * qq, hi = min(row.end, sp.hi) - sp.t0 - 32 * qq, h2 = have >> (2 * qq);
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < lo || e >= hi || !((h4 >> (e >> 4)) & 1)) v[e] = __float_as_uint(-INFINITY);
+          for (int e = 0; e < 32; ++e)
+            if (e < lo || e >= hi || !((h2 >> (e >> 4)) & 1)) v[e] = __float_as_uint(-INFINITY);
         }
         float mx[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(v[i]), __uint_as_float(v[4 + i]), __uint_as_float(v[8 + i]));
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(v[i]);
 #pragma unroll
-        for (int e = 12; e < 60; e += 8)
+        for (int e = 4; e < 28; e += 8)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(v[e + i]), __uint_as_float(v[e + 4 + i]));
-        float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], __uint_as_float(v[60])),
-                          max3(__uint_as_float(v[61]), __uint_as_float(v[62]), __uint_as_float(v[63]))) * f;
-        // behind this barrier both halves' scores are in registers: probabilities may take their columns
-        if (pair_any(top > m + 8.0f)) {
-          top = fmaxf(top, both(top, int(b)));
+        float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], __uint_as_float(v[28])),
+                          max3(__uint_as_float(v[29]), __uint_as_float(v[30]), __uint_as_float(v[31]))) * f;
+        if (group_any(top > m + 8.0f)) {
+          const float4 all = all_four(top, int(b));
+          top = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
           const bool raise = top > m + 8.0f;
           const float al = raise ? ex2(m - top) : 1.0f;
           if (raise) m = top;
@@ -1532,9 +1541,9 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           if (k > 0) {  // outputs so far follow, once O += P(n - 1) V is over
             wait(o_done, (n - 1) & 1);
             tc_after();
-            const uint32_t o_t = quad + COL_O + (D / 2) * hh;
+            const uint32_t o_t = quad + COL_O + E * qq;
 #pragma unroll 1
-            for (int c = 0; c < H / 16; ++c) {
+            for (int c = 0; c < E / 16; ++c) {
               uint32_t o[16];
               tmem_ld16(o_t + 16 * c, o);
               tc_wait_ld();
@@ -1547,21 +1556,23 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
+        for (int e = 0; e < 32; e += 2) {
           const float2 d = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, m2);
           const float2 p = make_float2(ex2(d.x), ex2(d.y));
           ls[(e >> 1) & 1] = __fadd2_rn(ls[(e >> 1) & 1], p);
           v[e >> 1] = h2_of_f2(p.x, p.y);
         }
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-        tmem_st16(s_t + 32 * hh, v);
-        tmem_st16(s_t + 32 * hh + 16, v + 16);
+        tmem_st16(s_t, v);
         tc_wait_st();
         tc_before();
         arrive(p_full + b);
       }
       // ---- the unit's outputs: a state, or, where this CTA had all of its tiles, the result
-      l += both(l, 2);
+      {
+        const float4 all = all_four(l, 2);
+        l = (all.x + all.y) + (all.z + all.w);
+      }
       // (S of the last tile was issued before O += P V of the one before it, and a wait for a parity cannot tell a
       // phase from the one two earlier: the unit's end has a barrier of its own)
       wait(unit_done, u & 1);
@@ -1569,35 +1580,41 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       const bool starts = cur.tile == 0, ends = cur.tile + nt == cur.tiles;
       const bool direct = todo != nullptr && starts && ends;
       const uint32_t o_t = quad + COL_O;
-      if (direct) {
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        // dims of columns 8 w + 2 k + e: 8 w + k + 4 e
-        float2 x[H / 2];
+      float2 x[E / 2];
+      // 16 columns are two words' dims: column 8 w + 2 k + e is dim 8 w + k + 4 e
+      auto in_order = [&](const uint32_t* a, int i) {
+        auto dim = [&](int d) { return __uint_as_float(a[(d & 8) + 2 * (d & 3) + ((d >> 2) & 1)]); };
+        return make_float2(dim(2 * i), dim(2 * i + 1));
+      };
 #pragma unroll
-        for (int c = 0; c < H / 16; ++c) {
-          uint32_t a[16], b[16];
-          tmem_ld16(o_t + H * hh + 16 * c, a);
-          if (unrotate) tmem_ld16(o_t + H * (hh ^ 1) + 16 * c, b);
+      for (int c = 0; c < E / 16; ++c) {
+        if (direct && unrotate) {
+          uint32_t a[2][16], bq[2][16];
+          tmem_ld16(o_t + 16 * c, a[0]);
+          tmem_ld16(o_t + E + 16 * c, a[1]);
+          tmem_ld16(o_t + 2 * E + 16 * c, bq[0]);
+          tmem_ld16(o_t + 3 * E + 16 * c, bq[1]);
           tc_wait_ld();
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+          for (int i = 0; i < 8; ++i) x[8 * c + i] = spans(in_order(a[0], i), in_order(a[1], i), in_order(bq[0], i), in_order(bq[1], i));
+        } else {
+          uint32_t a[16];
+          tmem_ld16(o_t + E * qq + 16 * c, a);
+          tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int p = 8 * w + 2 * (i & 3) + (i >> 2);
-              float y = __uint_as_float(a[p]);
-              if (unrotate) y = hh == 0 ? y + __uint_as_float(b[p]) : __uint_as_float(b[p]) - y;
-              (i & 1 ? x[8 * c + 4 * w + i / 2].y : x[8 * c + 4 * w + i / 2].x) = y;
-            }
+          for (int i = 0; i < 8; ++i) x[8 * c + i] = in_order(a, i);
         }
-        float sc = inv;
+      }
+      if (direct) {
+        float sc = l > 0.f ? 1.0f / l : 0.f;
         if (unrotate) {
-          hadamard_regs<H>(x);
+          hadamard_regs<E>(x);
           sc *= 1.0f / sqrtf(float(D));
         }
         if (row.tok >= 0) {
-          T* dst = out + row.tok * ld_out + int64_t(cur.g * part.G + row.hh) * D + H * hh;
+          T* dst = out + row.tok * ld_out + int64_t(cur.g * part.G + row.hh) * D + E * qq;
 #pragma unroll
-          for (int c = 0; c < H / 8; ++c) {
+          for (int c = 0; c < E / 8; ++c) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = fp8::from_f2<T>(make_float2(x[4 * c + i].x * sc, x[4 * c + i].y * sc));
@@ -1608,21 +1625,10 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         const int J = (cur.s.rows + ROWS - 1) / ROWS;
         const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, ROWS) + int64_t(cur.g) * J + cur.j;
         const int64_t at = ((todo != nullptr ? 2 * int64_t(blockIdx.x) + (starts ? 1 : 0) : unit + blockIdx.x) * ROWS + r);
-#pragma unroll 1
-        for (int c = 0; c < H / 16; ++c) {
-          uint32_t a[16];
-          tmem_ld16(o_t + H * hh + 16 * c, a);
-          tc_wait_ld();
+        float4* dst = reinterpret_cast<float4*>(ws.o + at * D + E * qq);
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-              auto at_dim = [&](int d) { return __uint_as_float(a[8 * w + 2 * (d & 3) + (d >> 2)]); };
-              *reinterpret_cast<float4*>(ws.o + at * D + H * hh + 16 * c + 8 * w + i) =
-                  make_float4(at_dim(i), at_dim(i + 1), at_dim(i + 2), at_dim(i + 3));
-            }
-        }
-        if (hh == 0) *reinterpret_cast<float2*>(ws.ml + at * 2) = make_float2(m, l);
+        for (int i = 0; i < E / 4; ++i) dst[i] = make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
+        if (qq == 0) *reinterpret_cast<float2*>(ws.ml + at * 2) = make_float2(m, l);
         if (warp == 2 + NCW && lane == 0) {
           if (todo == nullptr) {
             if (starts) ws.span[2 * unit] = blockIdx.x;
