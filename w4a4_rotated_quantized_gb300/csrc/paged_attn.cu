@@ -405,8 +405,8 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // There is one barrier a tile: behind it the fifth warp issues the scores'
 // products of the next tile and the outputs' of this one, and copies over what
 // was read.  The barrier also tells whether some thread's score passed its
-// reference; then the references are raised and the probabilities made again.
-// Several CTAs on an SM fill each other's waits.
+// reference; then the references are raised and the probabilities made again
+// (a unit's first tile sets them before).  Several CTAs on an SM fill each other's waits.
 namespace few {
 
 constexpr int NT = 160;
@@ -591,7 +591,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
       to_async_proxy();
       feed_keys();
       for (int it = 0; it < nt; ++it) {
-        if (__syncthreads_or(0))
+        if (it == 0 || __syncthreads_or(0))
           for (int i = 0; i < 4; ++i) __syncthreads();
         tc_after();
         if (elect_one()) {
@@ -836,10 +836,14 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
                          : "memory");
           to_async_proxy();
         };
-        probabilities();
-        if (it + 1 < nt) tc_wait_st();
-        tc_before();
-        if (__syncthreads_or(above)) {
+        bool raise = it == 0;  // a unit's first tile always raises
+        if (!raise) {
+          probabilities();
+          if (it + 1 < nt) tc_wait_st();
+          tc_before();
+          raise = __syncthreads_or(above);
+        }
+        if (raise) {
           // ---- raise the references that some score exceeds; sums and outputs so far follow
           float* mt = reinterpret_cast<float*>(mtop);
 #pragma unroll
@@ -879,6 +883,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
           }
           __syncthreads();
           probabilities();
+          if (it + 1 < nt) tc_wait_st();
           tc_before();
           __syncthreads();
         }
@@ -1711,58 +1716,141 @@ join_units_kernel(Part part, Space ws, const int4* __restrict__ todo, int unrota
 }  // namespace many
 
 // ------------------------------------------------------------------ join
-// One CTA per (token, query head): o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i
-// over the states of the row's unit of each part, d of them at a time.  A thread
-// adds 4 dims of every fourth state, eight loads at once: with one tile a CTA
-// (33 states of a row, 1 x 4097 tokens) the round trips to L2 are what counts.
+// o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i over the states of a row's unit
+// of each part.
+struct States {
+  const float *ml[2], *o[2];  // of slot 0, prefix and own part
+  const int* span[2];         // null: no state
+  bool none;                  // the token is behind the last sequence
+  __device__ __forceinline__ States(const Part& own, const Space& so, const Part& pre, const Space& sp, int n, int h, int D) {
+    const Place pl = place_of(own.t, n);
+    none = pl.b < 0;
+    const int g = h / own.G;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Part& p = k == 0 ? pre : own;
+      const Space& s = k == 0 ? sp : so;
+      span[k] = nullptr;
+      if (none || pl.pos < 0 || (k == 0 && p.shared == 0)) continue;
+      const Seq q = seq_of(p, pl.b, false);
+      const int rr = (n - q.tok0) * p.G + h - g * p.G;
+      if (rr < 0 || rr >= q.rows) continue;
+      const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
+      if (tiles_of(p, q, j) == 0) continue;
+      const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
+      span[k] = s.span + 2 * unit;
+      const int64_t at = unit * p.RP + rr - j * p.RP;
+      ml[k] = s.ml + at * 2;
+      o[k] = s.o + at * D;
+    }
+  }
+  // first and last slot; as they are, unless the batch changed under the call
+  __device__ __forceinline__ int2 slots(int k, const Space& s) const {
+    const int2 w = __ldcg(reinterpret_cast<const int2*>(span[k]));
+    return make_int2(min(max(w.x, 0), s.ctas - 1), min(w.y, s.ctas - 1));
+  }
+};
+
+// Many rows, few states each: a warp a (token, query head), E = d / 32 dims a lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+join_rows_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __restrict__ out, int64_t ld_out) {
+  constexpr int E = D / 32;
+  const int64_t row = 8 * int64_t(blockIdx.x) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int n = int(row / Hq), h = int(row - int64_t(n) * Hq);
+  // the batch was there before the parts' CTAs let this kernel start
+  const States t(own, so, pre, sp, n, h, D);
+  fp8::wait_for_previous();
+  if (t.none || n >= own.N) return;
+  float m = kNone, den = 0.f, num[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) num[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (t.span[k] == nullptr) continue;
+    const int64_t step = k == 0 ? pre.RP : own.RP;
+    const int2 w = t.slots(k, k == 0 ? sp : so);
+    for (int i0 = w.x; i0 <= w.y; i0 += 32) {
+      const int c = min(w.y - i0 + 1, 32);
+      float2 s = make_float2(kNone, 0.f);
+      if (lane < c) s = __ldcg(reinterpret_cast<const float2*>(t.ml[k] + (i0 + lane) * step * 2));
+      float mx = fmaxf(m, s.x);
+#pragma unroll
+      for (int b = 16; b > 0; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
+      const float a = ex2(m - mx), f = ex2(s.x - mx);
+      m = mx;
+      float lw = f * s.y;
+#pragma unroll
+      for (int b = 16; b > 0; b >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, b);
+      den = den * a + lw;
+#pragma unroll
+      for (int e = 0; e < E; ++e) num[e] *= a;
+      const float* src = t.o[k] + i0 * step * D + E * lane;
+#pragma unroll 4
+      for (int i = 0; i < c; ++i) {
+        const float b = __shfl_sync(0xffffffffu, f, i);
+        if constexpr (E == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i * step * D));
+          num[0] = fmaf(b, v.x, num[0]), num[1] = fmaf(b, v.y, num[1]), num[2] = fmaf(b, v.z, num[2]), num[3] = fmaf(b, v.w, num[3]);
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src + i * step * D));
+          num[0] = fmaf(b, v.x, num[0]), num[1] = fmaf(b, v.y, num[1]);
+        }
+      }
+    }
+  }
+  float sc = den > 0.f ? 1.0f / den : 0.f;
+  if (unrotate) {
+#pragma unroll
+    for (int s = 1; s < E; s <<= 1)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((e & s) == 0) {
+          const float a = num[e], b = num[e + s];
+          num[e] = a + b;
+          num[e + s] = a - b;
+        }
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float other = __shfl_xor_sync(0xffffffffu, num[e], s);
+        num[e] = (lane & s) ? other - num[e] : num[e] + other;
+      }
+    sc *= 1.0f / sqrtf(float(D));
+  }
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + n * ld_out + int64_t(h) * D + E * lane);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = fp8::from_f2<T>(make_float2(num[e] * sc, num[e + 1] * sc));
+}
+
+// Few rows, many states each: a CTA a (token, query head).  A thread adds 4
+// dims of every fourth state, eight loads at once: with one tile a CTA (33
+// states of a row, 1 x 4097 tokens) the round trips to L2 are what counts.
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
 join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __restrict__ out, int64_t ld_out) {
   __shared__ float x[D], top[D / 32], low[D / 32];
   __shared__ float4 part4[4][D / 4];
   const int n = blockIdx.x / Hq, h = blockIdx.x % Hq, e = threadIdx.x;
-  const int g = h / own.G;
   // the batch was there before the parts' CTAs let this kernel start
-  const Place pl = place_of(own.t, n);
-  // slots of either part that may hold a state of this row
-  const float *ml[2], *o[2];
-  const int* span[2] = {nullptr, nullptr};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const Part& p = k == 0 ? pre : own;
-    const Space& s = k == 0 ? sp : so;
-    ml[k] = s.ml;
-    o[k] = s.o;
-    if (pl.b < 0 || (k == 0 && p.shared == 0)) continue;
-    const Seq q = seq_of(p, pl.b, false);
-    const int rr = (n - q.tok0) * p.G + h - g * p.G;
-    if (pl.pos < 0 || rr < 0 || rr >= q.rows) continue;
-    const int j = rr / p.RP, J = (q.rows + p.RP - 1) / p.RP;
-    if (tiles_of(p, q, j) == 0) continue;
-    const int64_t unit = unit_base(q.tok0, p.prefix ? 0 : pl.b, p.G, p.Hkv, p.RP) + int64_t(g) * J + j;
-    span[k] = s.span + 2 * unit;
-    const int64_t at = unit * p.RP + rr - j * p.RP;
-    ml[k] += at * 2;
-    o[k] += at * D;
-  }
+  const States t(own, so, pre, sp, n, h, D);
   fp8::wait_for_previous();
-  if (pl.b < 0) return;
+  if (t.none) return;
   float m = kNone, den = 0.f;
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
   const int d4 = e % (D / 4), grp = e / (D / 4);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (span[k] == nullptr) continue;
-    const int ctas = k == 0 ? sp.ctas : so.ctas;
+    if (t.span[k] == nullptr) continue;
     const int64_t step = k == 0 ? pre.RP : own.RP;
-    int2 w = __ldcg(reinterpret_cast<const int2*>(span[k]));
-    w.x = min(max(w.x, 0), ctas - 1);  // as they are, unless the batch changed under the call
-    w.y = min(w.y, ctas - 1);
+    const int2 w = t.slots(k, k == 0 ? sp : so);
     for (int i0 = w.x; i0 <= w.y; i0 += D) {
       const int c = min(w.y - i0 + 1, D);
       float2 s = make_float2(kNone, 0.f);
-      if (e < c) s = __ldcg(reinterpret_cast<const float2*>(ml[k] + (i0 + e) * step * 2));
-      const float* src = o[k] + (i0 + grp) * step * D + 4 * d4;
+      if (e < c) s = __ldcg(reinterpret_cast<const float2*>(t.ml[k] + (i0 + e) * step * 2));
+      const float* src = t.o[k] + (i0 + grp) * step * D + 4 * d4;
       float4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -1913,8 +2001,12 @@ static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half*
   pre.RP = pp.RP;
   if (call.prefix && (rc = pp.many ? many_part(pre, pp, sp, nullptr) : few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
   if ((rc = few_part(own, po, so, call.prefix)) != QUAROT_OK) return rc;
-  return fp8::launch_dependent(join_kernel<T, D>, dim3(unsigned(own.N) * unsigned(Hq)), D, 0, 1, st, own, so, pre, sp, Hq,
-                               unrotate, out, ld_out);
+  // 256 sequences sharing 32768 tokens, 32 heads: a warp a row 8 us, a CTA a row 45 us; 1 x 4097: 5 us and 3 us
+  const unsigned rows = unsigned(own.N) * unsigned(Hq);
+  if (rows > 1024)
+    return fp8::launch_dependent(join_rows_kernel<T, D>, dim3((rows + 7) / 8), 256, 0, 1, st, own, so, pre, sp, Hq, unrotate, out,
+                                 ld_out);
+  return fp8::launch_dependent(join_kernel<T, D>, dim3(rows), D, 0, 1, st, own, so, pre, sp, Hq, unrotate, out, ld_out);
 }
 
 extern "C" int quarot_paged_attn(const void* q, int64_t ld_q, int dtype, int64_t N, int64_t Hq, int64_t Hkv, int64_t d,
