@@ -44,7 +44,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported size", 3: "misaligned 
           4: "kernel launch failed", 5: "device-side wait timed out", 6: "CUDA error"}
 
 _lib = None
-_calls = None  # compiled form of the 8-bit calls
+_calls = None  # compiled form of the 8-bit and paged calls
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -108,12 +108,12 @@ class QuarotError(RuntimeError):
 
 
 class _GeneralOnly:
-    """In the place of the compiled form of the 8-bit calls where there is none: takes nothing."""
+    """In the place of the compiled form of the 8-bit and paged calls where there is none: takes nothing."""
 
     def quant(self, *args):
         return None
 
-    norm = gemm = gated = quant
+    norm = gemm = gated = rope = append = read = attn = quant
 
 
 def _load_calls(lib):
@@ -135,6 +135,8 @@ def _load_calls(lib):
     calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
         "quarot_quant_fp8", "quarot_quant_fp8_block", "quarot_add_rmsnorm_quant_fp8", "quarot_fp8_gemm",
         "quarot_fp8_gated_gemm")))
+    calls.bind_paged(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "quarot_rope", "quarot_paged_append", "quarot_paged_read", "quarot_paged_workspace_bytes", "quarot_paged_attn")))
     calls.error = QuarotError
     return calls
 
@@ -929,6 +931,9 @@ def quarot_rope(q, k, positions, inv_freq, interleaved: bool = False, scale: flo
     if stream is not None:
         with _on(stream, q):
             return quarot_rope(q, k, positions, inv_freq, interleaved, scale, q_out, k_out)
+    done = (_calls or _loaded()).rope(q, k, positions, inv_freq, interleaved, scale, q_out, k_out)
+    if done is not None:
+        return done
     ld = _heads(q, "q")
     (N, Hq, d), dt, dev = q.shape, q.dtype, q.get_device()
     q_out, ld_o = _heads_out(q_out, q.shape, "q_out", dev, dt)
@@ -964,6 +969,9 @@ def quarot_paged_append(k, v, k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None
         with _on(stream, k):
             return quarot_paged_append(k, v, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, q, inv_freq, interleaved, scale,
                                        q_out)
+    done = (_calls or _loaded()).append(k, v, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, q, inv_freq, interleaved, scale, q_out)
+    if done is not None:
+        return done[0]
     cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
     ld_k = _heads(k, "k", dev)
     dt, N = k.dtype, k.shape[0]
@@ -996,6 +1004,10 @@ def quarot_paged_read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, n=None
     if stream is not None:
         with _on(stream, k_q):
             return quarot_paged_read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, n, unrotate, out_dtype, k_out, v_out)
+    done = (_calls or _loaded()).read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, n, unrotate, _DTYPES.get(out_dtype, -1), k_out,
+                                      v_out)
+    if done is not None:
+        return done
     cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
     tab, lens, cu, B, mp = _batch(page_table, lengths, cu_q, dev)
     if n is None:
@@ -1033,6 +1045,10 @@ def quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, max
         with _on(stream, q):
             return quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_q, shared_len, sm_scale,
                                      unrotate_out, out, workspace)
+    done = (_calls or _loaded()).attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_q, shared_len, sm_scale, unrotate_out,
+                                      out, workspace)
+    if done is not None:
+        return done[0]
     cache, P, ps, H, d, dev = _pages(k_q, k_s, v_q, v_s)
     ld = _heads(q, "q", dev)
     N, Hq, dq = q.shape

@@ -1,5 +1,5 @@
 """Builds libquarot.so in-tree for sm_103a with nvcc (no CMake, no torch), and
-beside it the Python module of the 8-bit calls (host code against torch), which
+beside it the Python module of the 8-bit and the paged calls (host code against torch), which
 the package can do without: where it cannot be built, a warning says so.
 
 Each translation unit under csrc/ is compiled in parallel, as relocatable
@@ -23,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libquarot.so")
 CALLS_SRC = os.path.join(CSRC, "fp8_calls.cpp")
+CALLS_HEADER = os.path.join(CSRC, "paged_calls.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 WHOLE_PROGRAM = {"fp8_gemm.cu"}  # ptxas honours setmaxnreg only there
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
@@ -59,7 +60,7 @@ def _lib_up_to_date() -> bool:
 
 def _calls_up_to_date() -> bool:
     try:
-        return _newer(calls_path(), [CALLS_SRC])
+        return _newer(calls_path(), [CALLS_SRC, CALLS_HEADER])
     except ImportError:  # no torch: nothing to build it against
         return False
 

@@ -1,4 +1,4 @@
-// The 8-bit calls from Python without the interpreter: each function checks
+// The 8-bit calls (and, in paged_calls.h, the paged ones) from Python without the interpreter: each function checks
 // the tensors, allocates the outputs that were not given and calls the C ABI on
 // the current stream.  A decode step makes a handful of these calls with
 // microseconds of GPU work each; through ctypes a call costs the host 9 to 14
@@ -228,9 +228,13 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+#include "paged_calls.h"
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef g_methods[] = {{"bind", FAST(bind)}, {"quant", FAST(quant)}, {"norm", FAST(norm)},
-                           {"gemm", FAST(gemm)}, {"gated", FAST(gated)}, {nullptr, nullptr, 0, nullptr}};
+                           {"gemm", FAST(gemm)}, {"gated", FAST(gated)}, {"bind_paged", FAST(bind_paged)},
+                           {"rope", FAST(rope)}, {"append", FAST(append)}, {"read", FAST(read)},
+                           {"attn", FAST(attn)}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fp8_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
