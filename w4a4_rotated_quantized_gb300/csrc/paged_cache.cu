@@ -14,139 +14,180 @@ namespace paged {
 // ------------------------------------------------------------------ rotary positions
 // A head is d / 16 units of 16 elements: 8 pairs that are turned (elements
 // 16 u .. 16 u + 15 of interleaved pairs, 8 u .. 8 u + 7 with their partners
-// rot / 2 further of the half layout), or 16 elements that stay.  A thread owns
-// a unit of every HSth head of a token: it makes the 8 angles once for them.
+// rot / 2 further of the half layout), or 16 elements that stay: either way two
+// 16-byte loads and stores that no other unit touches, so the outputs may be
+// the inputs.  A CTA makes the cosines and sines of its few tokens once, in
+// shared memory, one or a few a thread; its threads then walk over the units of
+// all their heads, three loaded ahead of the arithmetic.
 struct Heads {
   const void* in;
   void* out;
   int64_t ld_in, ld_out;
   int H;
 };
+constexpr int RT = 256;  // threads
 
+// Units of `nt` tokens from n0 on.  A thread has unit u = tid % U of every
+// (RT / U * parts)-th head; cs [token][pair].  skip: for each token 0 to turn
+// it, 1 to write zeros, 2 to leave its output.
 template <typename T>
-__device__ __forceinline__ void rope_unit(const T* src, T* dst, int u, int rot, bool inter, const float2* cs) {
-  const int units = rot >> 4;
-  int e0, e1;
-  if (u >= units || inter) {
-    e0 = 16 * u;
-    e1 = e0 + 8;
-  } else {
-    e0 = 8 * u;
-    e1 = e0 + (rot >> 1);
-  }
-  uint4 r0 = *reinterpret_cast<const uint4*>(src + e0), r1 = *reinterpret_cast<const uint4*>(src + e1);
-  if (u < units) {
-    float a[8], b[8];
-    unpack8<T>(r0, a);
-    unpack8<T>(r1, b);
-    if (inter) {
+__device__ __forceinline__ void turn_heads(const Heads& x, int64_t n0, int nt, int d, int rot, bool inter, const float2* cs,
+                                           const int* skip, int part, int parts) {
+  constexpr int AHEAD = 3;
+  const int U = d >> 4, u = int(threadIdx.x) % U, per = RT / U * parts;
+  if (int(threadIdx.x) >= RT / U * U) return;
+  const bool turned = 16 * u < rot;
+  const int e0 = turned && !inter ? 8 * u : 16 * u, e1 = turned && !inter ? e0 + (rot >> 1) : e0 + 8;
+  const float2* c = cs + 8 * u;
+  const int half = rot >> 1;
+  int v = int(threadIdx.x) / U + RT / U * part;  // (token, head)
+  int ti = v / x.H, h = v - ti * x.H;
+  while (ti < nt) {
+    uint4 r[AHEAD][2];
+    int tk[AHEAD], hk[AHEAD], cnt = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        turn(a[2 * i], a[2 * i + 1], cs[i]);
-        turn(b[2 * i], b[2 * i + 1], cs[4 + i]);
+    for (int i = 0; i < AHEAD; ++i) {
+      tk[i] = ti;
+      hk[i] = h;
+      if (ti < nt) {
+        const T* src = static_cast<const T*>(x.in) + (n0 + ti) * x.ld_in + int64_t(h) * d;
+        r[i][0] = *reinterpret_cast<const uint4*>(src + e0);
+        r[i][1] = *reinterpret_cast<const uint4*>(src + e1);
+        cnt = i + 1;
+        h += per;
+        if (h >= x.H) {
+          const int k = h / x.H;
+          ti += k;
+          h -= k * x.H;
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) turn(a[i], b[i], cs[i]);
     }
-    r0 = pack8<T>(a);
-    r1 = pack8<T>(b);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i >= cnt) continue;
+      const int what = skip == nullptr ? 0 : skip[tk[i]];
+      if (what == 2) continue;
+      if (turned) {
+        float a[8], b[8];
+        unpack8<T>(r[i][0], a);
+        unpack8<T>(r[i][1], b);
+        float2 t[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 f = *reinterpret_cast<const float4*>(c + tk[i] * half + 2 * k);
+          t[2 * k] = make_float2(f.x, f.y);
+          t[2 * k + 1] = make_float2(f.z, f.w);
+        }
+        if (inter) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            turn(a[2 * k], a[2 * k + 1], t[k]);
+            turn(b[2 * k], b[2 * k + 1], t[4 + k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) turn(a[k], b[k], t[k]);
+        }
+        r[i][0] = pack8<T>(a);
+        r[i][1] = pack8<T>(b);
+      }
+      if (what == 1) r[i][0] = r[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      T* dst = static_cast<T*>(x.out) + (n0 + tk[i]) * x.ld_out + int64_t(hk[i]) * d;
+      *reinterpret_cast<uint4*>(dst + e0) = r[i][0];
+      *reinterpret_cast<uint4*>(dst + e1) = r[i][1];
+    }
   }
-  *reinterpret_cast<uint4*>(dst + e0) = r0;
-  *reinterpret_cast<uint4*>(dst + e1) = r1;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(RT)
 rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ positions,
-            const double* __restrict__ inv_freq, int rot, int inter, float scale, int HS) {
-  const int U = d >> 4;
-  const int64_t gt = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int lane_unit = int(gt % U);
-  const int64_t slot = gt / U;  // (token, first head)
-  const int64_t n = slot / HS;
-  if (n >= N) return;
-  float2 cs[8];
-  if (16 * lane_unit < rot) {
-    const int pos = positions[n];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = turn_of(pos, turn_step(inv_freq[8 * lane_unit + i]), scale);
-  }
-  for (int h = int(slot % HS); h < q.H + k.H; h += HS) {
-    const bool isq = h < q.H;
-    const Heads& x = isq ? q : k;
-    const int hh = isq ? h : h - q.H;
-    rope_unit<T>(static_cast<const T*>(x.in) + n * x.ld_in + int64_t(hh) * d,
-                 static_cast<T*>(x.out) + n * x.ld_out + int64_t(hh) * d, lane_unit, rot, inter != 0, cs);
-  }
+            const double* __restrict__ inv_freq, int rot, int inter, float scale, int tokens) {
+  extern __shared__ __align__(16) unsigned char rsm[];
+  float2* cs = reinterpret_cast<float2*>(rsm);  // [tokens][half]
+  const int half = rot >> 1;
+  const int64_t n0 = int64_t(blockIdx.x) * tokens;
+  const int nt = int(min(int64_t(tokens), N - n0));
+  // a thread's pair is the same for every token that it makes an angle of, where half is a power of two
+  for (int i = threadIdx.x; i < nt * half; i += RT)
+    cs[i] = turn_of(positions[n0 + i / half], turn_step(inv_freq[i % half]), scale);
+  __syncthreads();
+  turn_heads<T>(q, n0, nt, d, rot, inter != 0, cs, nullptr, blockIdx.y, gridDim.y);
+  if (k.H > 0) turn_heads<T>(k, n0, nt, d, rot, inter != 0, cs, nullptr, blockIdx.y, gridDim.y);
 }
 
 // ------------------------------------------------------------------ append
 // As in quarot_kv_write, d / 32 lanes own one (token, head) vector, 32
-// elements each.  A CTA takes 64 (d = 128) or 128 neighbouring vectors of the
-// keys, the values or the queries, heads fastest, so that the angles of its
-// few tokens are made once, in shared memory.
-constexpr int AT = 256;       // threads
-constexpr int ATOK = 64;      // most tokens of a CTA
+// elements each.  A CTA takes some neighbouring tokens' keys, values or
+// queries, so that places are looked up and angles made once for all heads.
+constexpr int ATOK = 32;      // most tokens of a CTA
 constexpr int AHALF = 64;     // most pairs of a head
 
 template <typename T, int D>
-__global__ void __launch_bounds__(AT)
+__global__ void __launch_bounds__(RT)
 append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ inv_freq, int rot, int inter, float scale,
               uint8_t* __restrict__ k_q, __half* __restrict__ k_s, uint8_t* __restrict__ v_q, __half* __restrict__ v_s,
-              Batch t, int blocks_kv) {
+              Batch t, int kv_tokens, int kv_blocks, int q_tokens, int q_parts) {
   constexpr int TPV = D / 32;
-  __shared__ float2 cs[ATOK][AHALF];
+  __shared__ __align__(16) float2 cs[ATOK * AHALF];
   __shared__ uint64_t step[AHALF];
-  __shared__ int row[ATOK], posn[ATOK];
-  const int which = int(blockIdx.x) < blocks_kv ? 0 : int(blockIdx.x) < 2 * blocks_kv ? 1 : 2;
+  __shared__ int row[ATOK], posn[ATOK], skip[ATOK];
+  // the queries' CTAs first: theirs is most of the memory's work
+  const int which = int(blockIdx.x) >= int(gridDim.x) - kv_blocks ? 1 : int(blockIdx.x) >= int(gridDim.x) - 2 * kv_blocks ? 0 : 2;
   const Heads x = which == 0 ? k : which == 1 ? v : q;
-  const int64_t blk = int64_t(blockIdx.x) - which * int64_t(blocks_kv);
-  // tokens [n0, n0 + nt): whole tokens, as many as fit
-  const int per = AT / TPV;                              // vectors at a time
-  const int nt_max = min(ATOK, max(1, per / x.H));
+  const int64_t blk = which == 2 ? blockIdx.x / q_parts : which == 0 ? blockIdx.x - (gridDim.x - 2 * kv_blocks) : blockIdx.x - (gridDim.x - kv_blocks);
+  const int nt_max = which == 2 ? q_tokens : kv_tokens;
   const int64_t n0 = blk * nt_max;
   const int nt = int(min(int64_t(nt_max), N - n0));
-  const bool turned = which != 1 && rot > 0;
   const int half = rot >> 1;
+  const bool turned = which != 1 && half > 0;
   if (int(threadIdx.x) < nt) {
     const Place p = place_of(t, int(n0) + threadIdx.x);
-    int r = -2;  // nothing to store, and nothing wrong
-    if (p.b >= 0 && p.pos >= 0) {
-      const int page = page_at(t, p.b, p.pos / t.ps);
-      r = page < 0 ? -1 : p.pos % t.ps;
-      posn[threadIdx.x] = p.pos;
-      row[threadIdx.x] = page < 0 ? -1 : page;
-    } else {
-      posn[threadIdx.x] = p.b < 0 ? -2 : -1;
-      row[threadIdx.x] = r;
-    }
+    posn[threadIdx.x] = p.pos;
+    skip[threadIdx.x] = p.b < 0 ? 2 : p.pos < 0 ? 1 : 0;
+    if (which != 2) row[threadIdx.x] = p.b >= 0 && p.pos >= 0 ? page_at(t, p.b, p.pos / t.ps) : -1;
   }
   if (turned && int(threadIdx.x) < half) step[threadIdx.x] = turn_step(inv_freq[threadIdx.x]);
   __syncthreads();
   if (turned) {
-    for (int i = threadIdx.x; i < nt * half; i += AT) cs[i / half][i % half] = turn_of(posn[i / half], step[i % half], scale);
+    for (int i = threadIdx.x; i < nt * half; i += RT) cs[i] = turn_of(posn[i / half], step[i % half], scale);
     __syncthreads();
   }
-  const int total = nt * x.H;
+  if (which == 2) {
+    turn_heads<T>(x, n0, nt, D, rot, inter != 0, cs, skip, int(blockIdx.x) % q_parts, q_parts);
+    return;
+  }
+  constexpr int per = RT / TPV;  // vectors at a time
+  const int total = nt * x.H, part = int(threadIdx.x) % TPV;
+  // The next vector's 64 bytes are loaded before this one is worked on.
+  auto source = [&](int vi) {
+    const int ti = vi / x.H;
+    return static_cast<const T*>(x.in) + (n0 + ti) * x.ld_in + int64_t(vi - ti * x.H) * D;
+  };
+  const int first = int(threadIdx.x) / TPV;
+  uint4 nx[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    nx[i] = first < total ? __ldcs(reinterpret_cast<const uint4*>(source(first) + 32 * part) + i) : make_uint4(0u, 0u, 0u, 0u);
   for (int base = 0; base < total; base += per) {
-    const int vi = base + int(threadIdx.x) / TPV, part = int(threadIdx.x) % TPV;
+    const int vi = base + first;
     const bool valid = vi < total;
-    const int ti = valid ? vi / x.H : 0, h = valid ? vi % x.H : 0;
+    const int ti = valid ? vi / x.H : 0, h = valid ? vi - ti * x.H : 0;
     const T* src = static_cast<const T*>(x.in) + (n0 + ti) * x.ld_in + int64_t(h) * D;
     float e[32];
-    if (valid) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) unpack8<T>(*reinterpret_cast<const uint4*>(src + 32 * part + 8 * i), e + 8 * i);
-    } else {
+    for (int i = 0; i < 4; ++i) unpack8<T>(nx[i], e + 8 * i);
+    if (vi + per < total) {
+      const uint4* p = reinterpret_cast<const uint4*>(source(vi + per) + 32 * part);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) e[i] = 0.f;
+      for (int i = 0; i < 4; ++i) nx[i] = __ldcs(p + i);
     }
     if (turned && valid) {
+      const float2* c = cs + ti * half;
       if (inter) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (32 * part + 2 * i < rot) turn(e[2 * i], e[2 * i + 1], cs[ti][16 * part + i]);
+          if (32 * part + 2 * i < rot) turn(e[2 * i], e[2 * i + 1], c[16 * part + i]);
       } else {
         // the partners of 8 elements are 8 neighbouring ones, all on one side
 #pragma unroll
@@ -155,27 +196,18 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
           if (e0 < rot) {
             const bool low = e0 < half;
             const int f = low ? e0 : e0 - half;
+            const float sign = low ? -1.f : 1.f;
             float o[8];
             unpack8<T>(*reinterpret_cast<const uint4*>(src + (low ? e0 + half : f)), o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 c = cs[ti][f + j];
-              e[8 * i + j] = low ? e[8 * i + j] * c.x - o[j] * c.y : e[8 * i + j] * c.x + o[j] * c.y;
+            for (int j = 0; j < 8; j += 2) {
+              const float4 w = *reinterpret_cast<const float4*>(c + f + j);
+              e[8 * i + j] = e[8 * i + j] * w.x + o[j] * (w.y * sign);
+              e[8 * i + j + 1] = e[8 * i + j + 1] * w.z + o[j + 1] * (w.w * sign);
             }
           }
         }
       }
-    }
-    if (which == 2) {
-      __syncwarp();  // q_out may be q: partners are read before they are written
-      if (valid && posn[ti] != -2) {
-        T* dst = static_cast<T*>(x.out) + (n0 + ti) * x.ld_out + int64_t(h) * D;
-        const bool none = posn[ti] < 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(dst + 32 * part + 8 * i) = none ? make_uint4(0u, 0u, 0u, 0u) : pack8<T>(e + 8 * i);
-      }
-      continue;
     }
     hadamard32<TPV>(e, part);
     const float inv_sqrt_d = 1.0f / sqrtf(float(D));
@@ -201,47 +233,89 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
 }
 
 // ------------------------------------------------------------------ read
-// One (token, head) vector of the keys and of the values by d / 32 lanes each.
+// One (token, head) vector of the keys and of the values by d / 32 lanes; a CTA
+// looks its tokens' places up once.
 template <typename T, int D, bool BACK>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(RT)
 read_kernel(const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s, const uint8_t* __restrict__ v_q,
-            const __half* __restrict__ v_s, int64_t N, int Hkv, Batch t, T* __restrict__ k_out, T* __restrict__ v_out) {
+            const __half* __restrict__ v_s, int64_t N, int Hkv, Batch t, T* __restrict__ k_out, T* __restrict__ v_out, int tokens) {
   constexpr int TPV = D / 32;
-  const int64_t gt = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t vi = gt / TPV;
-  const int part = int(gt % TPV);
-  const bool valid = vi < N * Hkv;
-  const int n = valid ? int(vi / Hkv) : 0, h = valid ? int(vi % Hkv) : 0;
-  Place p = {-1, -1};
-  if (valid) p = place_of(t, n);
-  int page = -1;
-  if (p.b >= 0 && p.pos >= 0) page = page_at(t, p.b, p.pos / t.ps);
-  const int64_t at = page < 0 ? 0 : (int64_t(page) * Hkv + h) * t.ps + p.pos % t.ps;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    float s = 0.f;
+  __shared__ int row[ATOK], slot[ATOK];  // page (-1: zeros, -2: left as it is) and slot
+  const int64_t n0 = int64_t(blockIdx.x) * tokens;
+  const int nt = int(min(int64_t(tokens), N - n0));
+  if (int(threadIdx.x) < nt) {
+    const Place p = place_of(t, int(n0) + threadIdx.x);
+    int r = p.b < 0 ? -2 : -1, sl = 0;
+    if (p.b >= 0 && p.pos >= 0) {
+      const int index = p.pos / t.ps;
+      r = page_at(t, p.b, index);
+      sl = p.pos - index * t.ps;
+    }
+    row[threadIdx.x] = r;
+    slot[threadIdx.x] = sl;
+  }
+  __syncthreads();
+  const int total = nt * Hkv, part = int(threadIdx.x) % TPV;
+  constexpr int per = RT / TPV;
+  for (int base = 0; base < total; base += per) {  // the whole warp takes part in the transform
+    const int vi = base + int(threadIdx.x) / TPV;
+    const bool valid = vi < total;
+    const int ti = valid ? vi / Hkv : 0, h = valid ? vi - ti * Hkv : 0;
+    const int page = valid ? row[ti] : -2;
+    uint4 r[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    __half sc[2] = {__half(0.f), __half(0.f)};
     if (page >= 0) {
-      r = *reinterpret_cast<const uint4*>((which ? v_q : k_q) + at * (D / 2) + part * 16);
-      s = __half2float((which ? v_s : k_s)[at]);
+      const int64_t at = (int64_t(page) * Hkv + h) * t.ps + slot[ti];
+      r[0] = __ldcs(reinterpret_cast<const uint4*>(k_q + at * (D / 2) + part * 16));
+      r[1] = __ldcs(reinterpret_cast<const uint4*>(v_q + at * (D / 2) + part * 16));
+      sc[0] = k_s[at];
+      sc[1] = v_s[at];
     }
-    float e[32];
-    codes8(r.x, e);
-    codes8(r.y, e + 8);
-    codes8(r.z, e + 16);
-    codes8(r.w, e + 24);
-    if constexpr (BACK) {
-      hadamard32<TPV>(e, part);  // sums of codes are whole numbers: exact
-      s *= 1.0f / sqrtf(float(D));
-    }
-    if (p.b >= 0) {
-      T* dst = (which ? v_out : k_out) + (int64_t(n) * Hkv + h) * D + 32 * part;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) e[i] *= s;
+    for (int which = 0; which < 2; ++which) {
+      float s = __half2float(sc[which]);
+      float e[32];
+      codes8(r[which].x, e);
+      codes8(r[which].y, e + 8);
+      codes8(r[which].z, e + 16);
+      codes8(r[which].w, e + 24);
+      if constexpr (BACK) {
+        hadamard32<TPV>(e, part);  // sums of codes are whole numbers: exact
+        s *= 1.0f / sqrtf(float(D));
+      }
+      if (page != -2) {
+        T* dst = (which ? v_out : k_out) + ((n0 + ti) * Hkv + h) * D + 32 * part;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + 8 * i) = pack8<T>(e + 8 * i);
+        for (int i = 0; i < 32; ++i) e[i] *= s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __stcs(reinterpret_cast<uint4*>(dst + 8 * i), pack8<T>(e + 8 * i));
+      }
     }
   }
+}
+
+// Tokens of a CTA, and CTAs that share a group of tokens: some 12 units a
+// thread where there are enough tokens for four CTAs on every SM; else fewer
+// tokens, down to one whose heads are shared out.
+inline void rope_split(int64_t N, int64_t H, int64_t d, int sms, int* tokens, int* parts) {
+  const int64_t units = H * (d >> 4);
+  int64_t t = (12 * RT + units - 1) / units;
+  const int64_t enough = N / (int64_t(4) * sms);
+  t = t > enough ? enough : t;
+  t = t < 1 ? 1 : t > ATOK ? ATOK : t;
+  while (t > 1 && t * (d / 2) * int64_t(sizeof(float2)) > 16 * 1024) --t;
+  int64_t p = 1;
+  if (t == 1 && N * units < int64_t(4) * sms * RT) p = (units + RT - 1) / RT;
+  *tokens = int(t);
+  *parts = int(p);
+}
+// Tokens of a CTA whose vectors are worked on by d / 32 lanes each: four rounds of them, fewer where CTAs are few.
+inline int vector_tokens(int64_t N, int64_t H, int64_t d, int sms) {
+  const int64_t per = RT / (d / 32);
+  int64_t t = 4 * per / H;
+  const int64_t enough = N / (int64_t(4) * sms);
+  t = t > enough ? enough : t;
+  return int(t < 1 ? 1 : t > ATOK ? ATOK : t);
 }
 
 }  // namespace paged
@@ -267,14 +341,12 @@ extern "C" int quarot_rope(const void* q, int64_t Hq, int64_t ld_q, void* q_out,
   if (misaligned(positions, 4)) return QUAROT_ERR_ALIGNMENT;
   int sms = 0;
   if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
-  const int U = int(d >> 4), H = int(Hq + Hk);
-  const int HS = H;
-  const int64_t threads = N * HS * U;
-  const int64_t blocks = (threads + 255) / 256;
+  int tokens, parts;
+  rope_split(N, Hq > Hk ? Hq : Hk, d, sms, &tokens, &parts);
   const Heads hq = {q, q_out, ld_q, ld_qo, int(Hq)}, hk = {k, k_out, ld_k, ld_ko, int(Hk)};
   auto kern = dtype == QUAROT_FP16 ? rope_kernel<__half> : rope_kernel<__nv_bfloat16>;
-  kern<<<unsigned(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(hq, hk, N, int(d), positions, inv_freq, int(rot),
-                                                                       interleaved, scale, HS);
+  kern<<<dim3(unsigned((N + tokens - 1) / tokens), unsigned(parts)), RT, size_t(tokens) * (rot / 2) * sizeof(float2),
+         static_cast<cudaStream_t>(stream)>>>(hq, hk, N, int(d), positions, inv_freq, int(rot), interleaved, scale, tokens);
   return cuda_ok(cudaGetLastError()) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
 }
 
@@ -296,17 +368,17 @@ extern "C" int quarot_paged_append(const void* k, int64_t ld_k, const void* v, i
   if ((rc = check_cache(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_pages)) != QUAROT_OK) return rc;
   const Batch t = {page_table, lengths, cu_q, int(B), int(max_pages), int(n_pages), int(page_size)};
   const Heads hk = {k, nullptr, ld_k, 0, int(Hkv)}, hv = {v, nullptr, ld_v, 0, int(Hkv)}, hq = {q, q_out, ld_q, ld_qo, int(Hq)};
-  const int64_t per = AT / (d / 32);
-  auto blocks_of = [&](int64_t H) {
-    int64_t nt = per / H;
-    nt = nt < 1 ? 1 : nt > ATOK ? ATOK : nt;
-    return (N + nt - 1) / nt;
-  };
-  const int64_t bkv = blocks_of(Hkv), bq = Hq > 0 ? blocks_of(Hq) : 0;
+  int sms = 0;
+  if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
+  int q_tokens = 1, q_parts = 1;
+  if (Hq > 0) rope_split(N, Hq, d, sms, &q_tokens, &q_parts);
+  const int kt = vector_tokens(N, Hkv, d, sms);
+  const int64_t bkv = (N + kt - 1) / kt, bq = Hq > 0 ? (N + q_tokens - 1) / q_tokens * q_parts : 0;
+  if (2 * bkv + bq > 0x7fffffff) return QUAROT_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
-    kern<<<unsigned(2 * bkv + bq), AT, 0, static_cast<cudaStream_t>(stream)>>>(
+    kern<<<unsigned(2 * bkv + bq), RT, 0, static_cast<cudaStream_t>(stream)>>>(
         hk, hv, hq, N, inv_freq, int(rot), interleaved, scale, k_q, static_cast<__half*>(k_s), v_q,
-        static_cast<__half*>(v_s), t, int(bkv));
+        static_cast<__half*>(v_s), t, kt, int(bkv), q_tokens, q_parts);
   };
   if (dtype == QUAROT_FP16) d == 64 ? go(append_kernel<__half, 64>) : go(append_kernel<__half, 128>);
   else d == 64 ? go(append_kernel<__nv_bfloat16, 64>) : go(append_kernel<__nv_bfloat16, 128>);
@@ -325,11 +397,12 @@ extern "C" int quarot_paged_read(const uint8_t* k_q, const void* k_s, const uint
     return rc;
   if ((rc = check_cache(k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_pages)) != QUAROT_OK) return rc;
   const Batch t = {page_table, lengths, cu_q, int(B), int(max_pages), int(n_pages), int(page_size)};
-  const int64_t blocks = (N * Hkv * (d / 32) + 255) / 256;
-  if (blocks > 0x7fffffff) return QUAROT_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
+  const int tokens = vector_tokens(N, Hkv, d, sms);
   auto go = [&](auto kern, auto* ko, auto* vo) {
-    kern<<<unsigned(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        k_q, static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), N, int(Hkv), t, ko, vo);
+    kern<<<unsigned((N + tokens - 1) / tokens), RT, 0, static_cast<cudaStream_t>(stream)>>>(
+        k_q, static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), N, int(Hkv), t, ko, vo, tokens);
   };
   auto typed = [&](auto* ko, auto* vo) {
     using T = std::remove_pointer_t<decltype(ko)>;
