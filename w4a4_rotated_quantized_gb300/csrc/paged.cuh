@@ -71,58 +71,62 @@ __device__ __forceinline__ float2 turn_of(int pos, uint64_t step, float scale) {
   sincospif(float(int32_t(a >> 32)) * (1.0f / 2147483648.0f), &s, &c);
   return make_float2(c * scale, s * scale);
 }
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float u = a * cs.x - b * cs.y, w = b * cs.x + a * cs.y;
+__device__ __forceinline__ float2 negated(float2 v) { return make_float2(-v.x, -v.y); }
+// Two pairs (a, b), each element of both in one register pair.
+__device__ __forceinline__ void turn2(float2& a, float2& b, float2 c, float2 s) {
+  const float2 u = __ffma2_rn(b, negated(s), __fmul2_rn(a, c));
+  b = __ffma2_rn(a, s, __fmul2_rn(b, c));
   a = u;
-  b = w;
+}
+// A pair of neighbours.
+__device__ __forceinline__ float2 turn1(float2 v, float c, float s) {
+  return make_float2(v.x * c - v.y * s, v.y * c + v.x * s);
 }
 
 // ------------------------------------------------------------------ vectors
 // 8 elements of 16 bits from or to one 16-byte access.
 template <typename T>
-__device__ __forceinline__ void unpack8(uint4 r, float* v) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = fp8::to_f2<T>(w[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ void unpack8(uint4 r, float2* v) {
+  v[0] = fp8::to_f2<T>(r.x);
+  v[1] = fp8::to_f2<T>(r.y);
+  v[2] = fp8::to_f2<T>(r.z);
+  v[3] = fp8::to_f2<T>(r.w);
 }
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(fp8::from_f2<T>(make_float2(v[0], v[1])), fp8::from_f2<T>(make_float2(v[2], v[3])),
-                    fp8::from_f2<T>(make_float2(v[4], v[5])), fp8::from_f2<T>(make_float2(v[6], v[7])));
+__device__ __forceinline__ uint4 pack8(const float2* v) {
+  return make_uint4(fp8::from_f2<T>(v[0]), fp8::from_f2<T>(v[1]), fp8::from_f2<T>(v[2]), fp8::from_f2<T>(v[3]));
 }
-
-// x H of a vector of 32 * TPV elements, 32 consecutive ones in each of TPV
-// neighbouring lanes (the whole warp takes part).  Not divided by the root.
-template <int TPV>
-__device__ __forceinline__ void hadamard32(float* v, int part) {
+// x H of a vector of E * TPV elements, E consecutive ones in each of TPV
+// neighbouring lanes (the whole warp takes part), two to a register pair.  Not
+// divided by the root.
+template <int E, int TPV>
+__device__ __forceinline__ void hadamard(float2* v, int part) {
 #pragma unroll
-  for (int h = 1; h < 32; h <<= 1)
+  for (int i = 0; i < E / 2; ++i) v[i] = make_float2(v[i].x + v[i].y, v[i].x - v[i].y);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+  for (int h = 1; h < E / 2; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
       if ((i & h) == 0) {
-        const float a = v[i], b = v[i + h];
-        v[i] = a + b;
-        v[i + h] = a - b;
+        const float2 a = v[i], b = v[i + h];
+        v[i] = __fadd2_rn(a, b);
+        v[i + h] = __fadd2_rn(a, negated(b));
       }
 #pragma unroll
   for (int o = 1; o < TPV; o <<= 1) {
-    const bool upper = (part & o) != 0;
+    const float sign = (part & o) != 0 ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, v[i], o);
-      v[i] = upper ? other - v[i] : v[i] + other;
-    }
+    for (int i = 0; i < E / 2; ++i)
+      v[i] = __ffma2_rn(v[i], make_float2(sign, sign),
+                        make_float2(__shfl_xor_sync(0xffffffffu, v[i].x, o), __shfl_xor_sync(0xffffffffu, v[i].y, o)));
   }
 }
 
 // Codes of one 32-bit word, the even dim in the low nibble.
-__device__ __forceinline__ void codes8(uint32_t w, float* v) {
+__device__ __forceinline__ void codes8(uint32_t w, float2* v) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = float(int32_t(w << (28 - 4 * i)) >> 28);
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_float2(float(int32_t(w << (28 - 8 * i)) >> 28), float(int32_t(w << (24 - 8 * i)) >> 28));
 }
 
 // ------------------------------------------------------------------ checks

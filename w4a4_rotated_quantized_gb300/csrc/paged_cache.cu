@@ -28,18 +28,18 @@ struct Heads {
 constexpr int RT = 256;  // threads
 
 // Units of `nt` tokens from n0 on.  A thread has unit u = tid % U of every
-// (RT / U * parts)-th head; cs [token][pair].  skip: for each token 0 to turn
+// (RT / U * parts)-th head; cs holds a token's cosines, then its sines.  skip: for each token 0 to turn
 // it, 1 to write zeros, 2 to leave its output.
 template <typename T>
-__device__ __forceinline__ void turn_heads(const Heads& x, int64_t n0, int nt, int d, int rot, bool inter, const float2* cs,
+__device__ __forceinline__ void turn_heads(const Heads& x, int64_t n0, int nt, int d, int rot, bool inter, const float* cs,
                                            const int* skip, int part, int parts) {
   constexpr int AHEAD = 3;
   const int U = d >> 4, u = int(threadIdx.x) % U, per = RT / U * parts;
   if (int(threadIdx.x) >= RT / U * U) return;
   const bool turned = 16 * u < rot;
   const int e0 = turned && !inter ? 8 * u : 16 * u, e1 = turned && !inter ? e0 + (rot >> 1) : e0 + 8;
-  const float2* c = cs + 8 * u;
   const int half = rot >> 1;
+  const float* c = cs + 8 * u;
   int v = int(threadIdx.x) / U + RT / U * part;  // (token, head)
   int ti = v / x.H, h = v - ti * x.H;
   while (ti < nt) {
@@ -51,8 +51,8 @@ __device__ __forceinline__ void turn_heads(const Heads& x, int64_t n0, int nt, i
       hk[i] = h;
       if (ti < nt) {
         const T* src = static_cast<const T*>(x.in) + (n0 + ti) * x.ld_in + int64_t(h) * d;
-        r[i][0] = *reinterpret_cast<const uint4*>(src + e0);
-        r[i][1] = *reinterpret_cast<const uint4*>(src + e1);
+        r[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+        r[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
         cnt = i + 1;
         h += per;
         if (h >= x.H) {
@@ -68,33 +68,30 @@ __device__ __forceinline__ void turn_heads(const Heads& x, int64_t n0, int nt, i
       const int what = skip == nullptr ? 0 : skip[tk[i]];
       if (what == 2) continue;
       if (turned) {
-        float a[8], b[8];
+        float2 a[4], b[4];
         unpack8<T>(r[i][0], a);
         unpack8<T>(r[i][1], b);
-        float2 t[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 f = *reinterpret_cast<const float4*>(c + tk[i] * half + 2 * k);
-          t[2 * k] = make_float2(f.x, f.y);
-          t[2 * k + 1] = make_float2(f.z, f.w);
-        }
+        const float4* cf = reinterpret_cast<const float4*>(c + tk[i] * rot);
+        const float4* sf = reinterpret_cast<const float4*>(c + tk[i] * rot + half);
+        const float4 c0 = cf[0], c1 = cf[1], s0 = sf[0], s1 = sf[1];
         if (inter) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            turn(a[2 * k], a[2 * k + 1], t[k]);
-            turn(b[2 * k], b[2 * k + 1], t[4 + k]);
-          }
+          a[0] = turn1(a[0], c0.x, s0.x), a[1] = turn1(a[1], c0.y, s0.y);
+          a[2] = turn1(a[2], c0.z, s0.z), a[3] = turn1(a[3], c0.w, s0.w);
+          b[0] = turn1(b[0], c1.x, s1.x), b[1] = turn1(b[1], c1.y, s1.y);
+          b[2] = turn1(b[2], c1.z, s1.z), b[3] = turn1(b[3], c1.w, s1.w);
         } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) turn(a[k], b[k], t[k]);
+          turn2(a[0], b[0], make_float2(c0.x, c0.y), make_float2(s0.x, s0.y));
+          turn2(a[1], b[1], make_float2(c0.z, c0.w), make_float2(s0.z, s0.w));
+          turn2(a[2], b[2], make_float2(c1.x, c1.y), make_float2(s1.x, s1.y));
+          turn2(a[3], b[3], make_float2(c1.z, c1.w), make_float2(s1.z, s1.w));
         }
         r[i][0] = pack8<T>(a);
         r[i][1] = pack8<T>(b);
       }
       if (what == 1) r[i][0] = r[i][1] = make_uint4(0u, 0u, 0u, 0u);
       T* dst = static_cast<T*>(x.out) + (n0 + tk[i]) * x.ld_out + int64_t(hk[i]) * d;
-      *reinterpret_cast<uint4*>(dst + e0) = r[i][0];
-      *reinterpret_cast<uint4*>(dst + e1) = r[i][1];
+      __stcs(reinterpret_cast<uint4*>(dst + e0), r[i][0]);
+      __stcs(reinterpret_cast<uint4*>(dst + e1), r[i][1]);
     }
   }
 }
@@ -104,13 +101,16 @@ __global__ void __launch_bounds__(RT)
 rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ positions,
             const double* __restrict__ inv_freq, int rot, int inter, float scale, int tokens) {
   extern __shared__ __align__(16) unsigned char rsm[];
-  float2* cs = reinterpret_cast<float2*>(rsm);  // [tokens][half]
+  float* cs = reinterpret_cast<float*>(rsm);  // [tokens][cosines, sines]
   const int half = rot >> 1;
   const int64_t n0 = int64_t(blockIdx.x) * tokens;
   const int nt = int(min(int64_t(tokens), N - n0));
-  // a thread's pair is the same for every token that it makes an angle of, where half is a power of two
-  for (int i = threadIdx.x; i < nt * half; i += RT)
-    cs[i] = turn_of(positions[n0 + i / half], turn_step(inv_freq[i % half]), scale);
+  for (int i = threadIdx.x; i < nt * half; i += RT) {
+    const int n = i / half, f = i - n * half;
+    const float2 v = turn_of(positions[n0 + n], turn_step(inv_freq[f]), scale);
+    cs[n * rot + f] = v.x;
+    cs[n * rot + half + f] = v.y;
+  }
   __syncthreads();
   turn_heads<T>(q, n0, nt, d, rot, inter != 0, cs, nullptr, blockIdx.y, gridDim.y);
   if (k.H > 0) turn_heads<T>(k, n0, nt, d, rot, inter != 0, cs, nullptr, blockIdx.y, gridDim.y);
@@ -122,41 +122,42 @@ rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ posi
 // queries, so that places are looked up and angles made once for all heads.
 constexpr int ATOK = 32;      // most tokens of a CTA
 constexpr int AHALF = 64;     // most pairs of a head
+constexpr int CU = 257;       // entries of cu that a CTA keeps at hand
+
+// The batch with cu in shared memory, where it fits: a search in it is then a
+// few steps of some clocks each.  The whole CTA takes part.
+__device__ __forceinline__ Batch near(Batch t, int* cu) {
+  if (t.cu != nullptr && t.B < CU) {
+    for (int i = threadIdx.x; i <= t.B; i += RT) cu[i] = t.cu[i];
+    __syncthreads();
+    t.cu = cu;
+  }
+  return t;
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(RT)
+__global__ void __launch_bounds__(RT, 3)
 append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ inv_freq, int rot, int inter, float scale,
               uint8_t* __restrict__ k_q, __half* __restrict__ k_s, uint8_t* __restrict__ v_q, __half* __restrict__ v_s,
               Batch t, int kv_tokens, int kv_blocks, int q_tokens, int q_parts) {
   constexpr int TPV = D / 32;
-  __shared__ __align__(16) float2 cs[ATOK * AHALF];
+  __shared__ __align__(16) float cs[ATOK * AHALF * 2];  // a token's cosines, then its sines
   __shared__ uint64_t step[AHALF];
   __shared__ int row[ATOK], posn[ATOK], skip[ATOK];
-  // the queries' CTAs first: theirs is most of the memory's work
-  const int which = int(blockIdx.x) >= int(gridDim.x) - kv_blocks ? 1 : int(blockIdx.x) >= int(gridDim.x) - 2 * kv_blocks ? 0 : 2;
+  __shared__ int cu[CU];
+  // CTAs of keys, values and queries in turn, as long as there are all of them: the former are bound by issue, the
+  // latter by memory (one kind after the other: 4 x 2048 tokens 54 us, in turn 44 us)
+  const int m = min(kv_blocks, int(gridDim.x) - 2 * kv_blocks), b = int(blockIdx.x);
+  const int which = b < 3 * m ? b % 3 : m < kv_blocks ? (b - 3 * m) & 1 : 2;
+  int64_t blk = b < 3 * m ? b / 3 : m < kv_blocks ? m + ((b - 3 * m) >> 1) : b - 2 * m;
+  const int q_part = which == 2 ? int(blk % q_parts) : 0;
+  if (which == 2) blk /= q_parts;
   const Heads x = which == 0 ? k : which == 1 ? v : q;
-  const int64_t blk = which == 2 ? blockIdx.x / q_parts : which == 0 ? blockIdx.x - (gridDim.x - 2 * kv_blocks) : blockIdx.x - (gridDim.x - kv_blocks);
   const int nt_max = which == 2 ? q_tokens : kv_tokens;
   const int64_t n0 = blk * nt_max;
   const int nt = int(min(int64_t(nt_max), N - n0));
   const int half = rot >> 1;
   const bool turned = which != 1 && half > 0;
-  if (int(threadIdx.x) < nt) {
-    const Place p = place_of(t, int(n0) + threadIdx.x);
-    posn[threadIdx.x] = p.pos;
-    skip[threadIdx.x] = p.b < 0 ? 2 : p.pos < 0 ? 1 : 0;
-    if (which != 2) row[threadIdx.x] = p.b >= 0 && p.pos >= 0 ? page_at(t, p.b, p.pos / t.ps) : -1;
-  }
-  if (turned && int(threadIdx.x) < half) step[threadIdx.x] = turn_step(inv_freq[threadIdx.x]);
-  __syncthreads();
-  if (turned) {
-    for (int i = threadIdx.x; i < nt * half; i += RT) cs[i] = turn_of(posn[i / half], step[i % half], scale);
-    __syncthreads();
-  }
-  if (which == 2) {
-    turn_heads<T>(x, n0, nt, D, rot, inter != 0, cs, skip, int(blockIdx.x) % q_parts, q_parts);
-    return;
-  }
   constexpr int per = RT / TPV;  // vectors at a time
   const int total = nt * x.H, part = int(threadIdx.x) % TPV;
   // The next vector's 64 bytes are loaded before this one is worked on.
@@ -168,26 +169,53 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
   uint4 nx[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    nx[i] = first < total ? __ldcs(reinterpret_cast<const uint4*>(source(first) + 32 * part) + i) : make_uint4(0u, 0u, 0u, 0u);
+    nx[i] = which != 2 && first < total ? __ldcs(reinterpret_cast<const uint4*>(source(first) + 32 * part) + i) : make_uint4(0u, 0u, 0u, 0u);
+  t = near(t, cu);
+  if (int(threadIdx.x) < nt) {
+    const Place p = place_of(t, int(n0) + threadIdx.x);
+    posn[threadIdx.x] = p.pos;
+    skip[threadIdx.x] = p.b < 0 ? 2 : p.pos < 0 ? 1 : 0;
+    if (which != 2) row[threadIdx.x] = p.b >= 0 && p.pos >= 0 ? page_at(t, p.b, p.pos / t.ps) : -1;
+  }
+  if (turned && int(threadIdx.x) < half) step[threadIdx.x] = turn_step(inv_freq[threadIdx.x]);
+  __syncthreads();
+  if (turned) {
+    for (int i = threadIdx.x; i < nt * half; i += RT) {
+      const int n = i / half, f = i - n * half;
+      const float2 w = turn_of(posn[n], step[f], scale);
+      cs[n * rot + f] = w.x;
+      cs[n * rot + half + f] = w.y;
+    }
+    __syncthreads();
+  }
+  if (which == 2) {
+    turn_heads<T>(x, n0, nt, D, rot, inter != 0, cs, skip, q_part, q_parts);
+    return;
+  }
   for (int base = 0; base < total; base += per) {
     const int vi = base + first;
     const bool valid = vi < total;
     const int ti = valid ? vi / x.H : 0, h = valid ? vi - ti * x.H : 0;
     const T* src = static_cast<const T*>(x.in) + (n0 + ti) * x.ld_in + int64_t(h) * D;
-    float e[32];
+    float2 e[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack8<T>(nx[i], e + 8 * i);
+    for (int i = 0; i < 4; ++i) unpack8<T>(nx[i], e + 4 * i);
     if (vi + per < total) {
       const uint4* p = reinterpret_cast<const uint4*>(source(vi + per) + 32 * part);
 #pragma unroll
       for (int i = 0; i < 4; ++i) nx[i] = __ldcs(p + i);
     }
     if (turned && valid) {
-      const float2* c = cs + ti * half;
+      const float* c = cs + ti * rot;
       if (inter) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (32 * part + 2 * i < rot) turn(e[2 * i], e[2 * i + 1], c[16 * part + i]);
+        for (int i = 0; i < 4; ++i)
+          if (32 * part + 8 * i < rot) {
+            const float4 cf = *reinterpret_cast<const float4*>(c + 16 * part + 4 * i);
+            const float4 sf = *reinterpret_cast<const float4*>(c + half + 16 * part + 4 * i);
+            e[4 * i] = turn1(e[4 * i], cf.x, sf.x), e[4 * i + 1] = turn1(e[4 * i + 1], cf.y, sf.y);
+            e[4 * i + 2] = turn1(e[4 * i + 2], cf.z, sf.z), e[4 * i + 3] = turn1(e[4 * i + 3], cf.w, sf.w);
+          }
       } else {
         // the partners of 8 elements are 8 neighbouring ones, all on one side
 #pragma unroll
@@ -196,34 +224,54 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
           if (e0 < rot) {
             const bool low = e0 < half;
             const int f = low ? e0 : e0 - half;
-            const float sign = low ? -1.f : 1.f;
-            float o[8];
+            const float2 sign = make_float2(low ? -1.f : 1.f, low ? -1.f : 1.f);
+            float2 o[4];
             unpack8<T>(*reinterpret_cast<const uint4*>(src + (low ? e0 + half : f)), o);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const float4 w = *reinterpret_cast<const float4*>(c + f + j);
-              e[8 * i + j] = e[8 * i + j] * w.x + o[j] * (w.y * sign);
-              e[8 * i + j + 1] = e[8 * i + j + 1] * w.z + o[j + 1] * (w.w * sign);
+            for (int j = 0; j < 4; j += 2) {
+              const float4 cf = *reinterpret_cast<const float4*>(c + f + 2 * j), sf = *reinterpret_cast<const float4*>(c + half + f + 2 * j);
+              e[4 * i + j] = __ffma2_rn(__fmul2_rn(o[j], sign), make_float2(sf.x, sf.y), __fmul2_rn(e[4 * i + j], make_float2(cf.x, cf.y)));
+              e[4 * i + j + 1] = __ffma2_rn(__fmul2_rn(o[j + 1], sign), make_float2(sf.z, sf.w), __fmul2_rn(e[4 * i + j + 1], make_float2(cf.z, cf.w)));
             }
           }
         }
       }
     }
-    hadamard32<TPV>(e, part);
+    hadamard<32, TPV>(e, part);
     const float inv_sqrt_d = 1.0f / sqrtf(float(D));
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      e[i] *= inv_sqrt_d;
-      amax = fmaxf(amax, fabsf(e[i]));
+    for (int i = 0; i < 16; ++i) {
+      e[i] = __fmul2_rn(e[i], make_float2(inv_sqrt_d, inv_sqrt_d));
+      amax = fmaxf(amax, fmaxf(fabsf(e[i].x), fabsf(e[i].y)));
     }
 #pragma unroll
     for (int o = 1; o < TPV; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const __half S = quant_scale_fp16(amax, 1.0f);
     const float inv = 1.0f / __half2float(S);
-    uint32_t w[4] = {0, 0, 0, 0};
+    // Only where the scale is at its largest can a quotient round past 7 or -8
+    // (else S >= amax / 7 within 2^-11, or 3 % among the subnormals).
+    if (__any_sync(0xffffffffu, !(amax < 7.0f * 65504.0f))) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i >> 3] |= nibble_rne(fminf(fmaxf(e[i] * inv, -8.0f), 7.0f)) << (4 * (i & 7));
+      for (int i = 0; i < 16; ++i) {
+        const float sf = __half2float(S);
+        e[i] = make_float2(fminf(fmaxf(e[i].x, -8.0f * sf), 7.0f * sf), fminf(fmaxf(e[i].y, -8.0f * sf), 7.0f * sf));
+      }
+    }
+    // round(v / S) + 8 as a whole number (adding 1.5 * 2^23 rounds to even), and eight of them to a word in base 16,
+    // four at a time: exact in fp32, and no integer instruction for each
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 acc[2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 u = __fadd2_rn(__fmul2_rn(e[4 * i + j], make_float2(inv, inv)), make_float2(12582912.0f, 12582912.0f));
+        u = __fadd2_rn(u, make_float2(-12582904.0f, -12582904.0f));
+        acc[j >> 1] = (j & 1) ? __ffma2_rn(u, make_float2(256.0f, 4096.0f), acc[j >> 1]) : __fmul2_rn(u, make_float2(1.0f, 16.0f));
+      }
+      w[i] = (uint32_t(__float2int_rn(acc[0].x + acc[0].y)) | (uint32_t(__float2int_rn(acc[1].x + acc[1].y)) << 16)) ^ 0x88888888u;
+    }
     if (valid && row[ti] >= 0) {
       const int64_t at = (int64_t(row[ti]) * x.H + h) * t.ps + posn[ti] % t.ps;
       *reinterpret_cast<uint4*>((which == 0 ? k_q : v_q) + at * (D / 2) + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -233,16 +281,21 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
 }
 
 // ------------------------------------------------------------------ read
-// One (token, head) vector of the keys and of the values by d / 32 lanes; a CTA
-// looks its tokens' places up once.
+// d / 8 lanes own one (token, head) vector of the keys and of the values, one
+// packed word each, so that neighbouring lanes write neighbouring 16 bytes (32
+// elements a lane, as in append, wrote half sectors: 16 x 4096 tokens 77 us).
+// A CTA looks its tokens' places up once; four vectors' words are loaded before
+// the first is worked on.
 template <typename T, int D, bool BACK>
 __global__ void __launch_bounds__(RT)
 read_kernel(const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s, const uint8_t* __restrict__ v_q,
             const __half* __restrict__ v_s, int64_t N, int Hkv, Batch t, T* __restrict__ k_out, T* __restrict__ v_out, int tokens) {
-  constexpr int TPV = D / 32;
+  constexpr int TPV = D / 8, AHEAD = 4, per = RT / TPV;
   __shared__ int row[ATOK], slot[ATOK];  // page (-1: zeros, -2: left as it is) and slot
+  __shared__ int cu[CU];
   const int64_t n0 = int64_t(blockIdx.x) * tokens;
   const int nt = int(min(int64_t(tokens), N - n0));
+  t = near(t, cu);
   if (int(threadIdx.x) < nt) {
     const Place p = place_of(t, int(n0) + threadIdx.x);
     int r = p.b < 0 ? -2 : -1, sl = 0;
@@ -256,51 +309,53 @@ read_kernel(const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s, con
   }
   __syncthreads();
   const int total = nt * Hkv, part = int(threadIdx.x) % TPV;
-  constexpr int per = RT / TPV;
-  for (int base = 0; base < total; base += per) {  // the whole warp takes part in the transform
-    const int vi = base + int(threadIdx.x) / TPV;
-    const bool valid = vi < total;
-    const int ti = valid ? vi / Hkv : 0, h = valid ? vi - ti * Hkv : 0;
-    const int page = valid ? row[ti] : -2;
-    uint4 r[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    __half sc[2] = {__half(0.f), __half(0.f)};
-    if (page >= 0) {
-      const int64_t at = (int64_t(page) * Hkv + h) * t.ps + slot[ti];
-      r[0] = __ldcs(reinterpret_cast<const uint4*>(k_q + at * (D / 2) + part * 16));
-      r[1] = __ldcs(reinterpret_cast<const uint4*>(v_q + at * (D / 2) + part * 16));
-      sc[0] = k_s[at];
-      sc[1] = v_s[at];
+  for (int base = 0; base < total; base += per * AHEAD) {  // whole warps take part in the transform
+    uint32_t w[AHEAD][2];
+    __half sc[AHEAD][2];
+    int page[AHEAD], vi[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      vi[i] = base + i * per + int(threadIdx.x) / TPV;
+      const bool valid = vi[i] < total;
+      const int ti = valid ? vi[i] / Hkv : 0, h = valid ? vi[i] - ti * Hkv : 0;
+      page[i] = valid ? row[ti] : -2;
+      w[i][0] = w[i][1] = 0u;
+      sc[i][0] = sc[i][1] = __half(0.f);
+      if (page[i] >= 0) {
+        const int64_t at = (int64_t(page[i]) * Hkv + h) * t.ps + slot[ti];
+        w[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(k_q + at * (D / 2)) + part);
+        w[i][1] = __ldcs(reinterpret_cast<const uint32_t*>(v_q + at * (D / 2)) + part);
+        sc[i][0] = k_s[at];
+        sc[i][1] = v_s[at];
+      }
     }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float s = __half2float(sc[which]);
-      float e[32];
-      codes8(r[which].x, e);
-      codes8(r[which].y, e + 8);
-      codes8(r[which].z, e + 16);
-      codes8(r[which].w, e + 24);
-      if constexpr (BACK) {
-        hadamard32<TPV>(e, part);  // sums of codes are whole numbers: exact
-        s *= 1.0f / sqrtf(float(D));
-      }
-      if (page != -2) {
-        T* dst = (which ? v_out : k_out) + ((n0 + ti) * Hkv + h) * D + 32 * part;
+    for (int i = 0; i < AHEAD; ++i) {
+      if (base + i * per >= total) break;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) e[i] *= s;
+      for (int which = 0; which < 2; ++which) {
+        float s = __half2float(sc[i][which]);
+        float2 e[4];
+        codes8(w[i][which], e);
+        if constexpr (BACK) {  // sums of codes are whole numbers: exact
+          hadamard<8, TPV>(e, part);
+          s *= 1.0f / sqrtf(float(D));
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) __stcs(reinterpret_cast<uint4*>(dst + 8 * i), pack8<T>(e + 8 * i));
+        for (int j = 0; j < 4; ++j) e[j] = __fmul2_rn(e[j], make_float2(s, s));
+        if (page[i] != -2) __stcs(reinterpret_cast<uint4*>((which ? v_out : k_out) + (n0 * Hkv + vi[i]) * D + 8 * part), pack8<T>(e));
       }
     }
   }
 }
 
-// Tokens of a CTA, and CTAs that share a group of tokens: some 12 units a
-// thread where there are enough tokens for four CTAs on every SM; else fewer
+// Tokens of a CTA, and CTAs that share a group of tokens: some 6 units a
+// thread where there are enough tokens for two CTAs on every SM; else fewer
 // tokens, down to one whose heads are shared out.
 inline void rope_split(int64_t N, int64_t H, int64_t d, int sms, int* tokens, int* parts) {
   const int64_t units = H * (d >> 4);
-  int64_t t = (12 * RT + units - 1) / units;
-  const int64_t enough = N / (int64_t(4) * sms);
+  int64_t t = (6 * RT + units - 1) / units;
+  const int64_t enough = N / (int64_t(2) * sms);
   t = t > enough ? enough : t;
   t = t < 1 ? 1 : t > ATOK ? ATOK : t;
   while (t > 1 && t * (d / 2) * int64_t(sizeof(float2)) > 16 * 1024) --t;
@@ -309,11 +364,12 @@ inline void rope_split(int64_t N, int64_t H, int64_t d, int sms, int* tokens, in
   *tokens = int(t);
   *parts = int(p);
 }
-// Tokens of a CTA whose vectors are worked on by d / 32 lanes each: four rounds of them, fewer where CTAs are few.
-inline int vector_tokens(int64_t N, int64_t H, int64_t d, int sms) {
-  const int64_t per = RT / (d / 32);
+// Tokens of a CTA that works on `per` of their H vectors at a time: four rounds of them, fewer where
+// that leaves SMs without one (its look-ups take as long as several rounds: 5 x 700 tokens of 16 heads of 64 in 5 tokens a
+// CTA 20 us, in 23 11 us).
+inline int vector_tokens(int64_t N, int64_t H, int64_t per, int sms) {
   int64_t t = 4 * per / H;
-  const int64_t enough = N / (int64_t(4) * sms);
+  const int64_t enough = N / sms;
   t = t > enough ? enough : t;
   return int(t < 1 ? 1 : t > ATOK ? ATOK : t);
 }
@@ -372,7 +428,7 @@ extern "C" int quarot_paged_append(const void* k, int64_t ld_k, const void* v, i
   if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
   int q_tokens = 1, q_parts = 1;
   if (Hq > 0) rope_split(N, Hq, d, sms, &q_tokens, &q_parts);
-  const int kt = vector_tokens(N, Hkv, d, sms);
+  const int kt = vector_tokens(N, Hkv, RT / (d / 32), sms);
   const int64_t bkv = (N + kt - 1) / kt, bq = Hq > 0 ? (N + q_tokens - 1) / q_tokens * q_parts : 0;
   if (2 * bkv + bq > 0x7fffffff) return QUAROT_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
@@ -399,7 +455,7 @@ extern "C" int quarot_paged_read(const uint8_t* k_q, const void* k_s, const uint
   const Batch t = {page_table, lengths, cu_q, int(B), int(max_pages), int(n_pages), int(page_size)};
   int sms = 0;
   if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
-  const int tokens = vector_tokens(N, Hkv, d, sms);
+  const int tokens = vector_tokens(N, Hkv, RT / (d / 8), sms);
   auto go = [&](auto kern, auto* ko, auto* vo) {
     kern<<<unsigned((N + tokens - 1) / tokens), RT, 0, static_cast<cudaStream_t>(stream)>>>(
         k_q, static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), N, int(Hkv), t, ko, vo, tokens);
