@@ -992,8 +992,8 @@ struct Cfg {
   static constexpr int OFF_RAW = OFF_Q + ROWS * D * 2;
   static constexpr int OFF_KS = OFF_RAW + SP * STAGE;  // float [2][TILE] key scales of the score buffers
   static constexpr int OFF_X = OFF_KS + 2 * TILE * 4;  // float [4][ROWS] exchange of a row's quarters, three times; at first find_start's words
-  static constexpr int OFF_CUR = OFF_X + 12 * ROWS * 4; // cursors of two units
-  static constexpr int OFF_BAR = OFF_CUR + 128;
+  static constexpr int OFF_CUR = OFF_X + 12 * ROWS * 4; // cursors of four units
+  static constexpr int OFF_BAR = OFF_CUR + 256;
   static constexpr int NBAR = 2 * SP + 4 + 4 + 3 + 8 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 64;
@@ -1106,7 +1106,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers; 0x100: all tokens are there
   float* ksf = reinterpret_cast<float*>(sm + C::OFF_KS);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
-  int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [2][16]
+  int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [4][16]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
@@ -1165,7 +1165,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   // the unit that the feeder published: waits for it and reads its cursor
   auto unit_at = [&](uint32_t u) {
     wait(unit_full, u & 1, true);
-    return told_cursor(cursors + 16 * (u & 1));
+    return told_cursor(cursors + 16 * (u & 3));
   };
 
   if (warp == 0) {
@@ -1240,7 +1240,9 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         mma_commit(s_full + (m & 1));
         mma_commit(k_empty + (m & 1));
       };
+      // the queries are there while the unit before may still be at its last products: these read the buffer's place
       wait(q_full, u & 1);
+      if (u > 0) wait(unit_done, (u - 1) & 1);
       wait(k_full + (n & 1), (n >> 1) & 1);
       tc_after();
       if (elect_one()) issue_scores(n);
@@ -1369,7 +1371,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
     // ================================================================ units
     for (uint32_t u = 0; left > 0; ++u) {
       if (u > 0) wait(unit_empty, (u - 1) & 1);
-      if (lane == 0) tell_cursor(cur, cursors + 16 * (u & 1));
+      if (lane == 0) tell_cursor(cur, cursors + 16 * (u & 3));
 #pragma unroll 1
       for (int r = lane; r < ROWS; r += 32) {
         const int rr = cur.j * ROWS + r, i = rr / part.G;
@@ -1419,21 +1421,24 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       return __ffma2_rn(__ffma2_rn(d, s1, c), s2, __ffma2_rn(b, s1, a));
     };
     uint32_t n = 0;
-    for (uint32_t u = 0; left > 0; ++u) {
+    float f = 0.f, off = 0.f;
+    int end = 0, clear = 0, nt = 0;  // of the unit at work: what the row sees, tiles that all rows of the warp see whole, tiles
+    // The next unit: false where there is none.
+    auto begin = [&](uint32_t u) -> bool {
+      if (left <= 0) return false;
       cur = unit_at(u);
       if (cur.tiles == 0) {
         arrive(unit_empty);
-        break;
+        left = 0;
+        return false;
       }
-      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      nt = int(min(left, int64_t(cur.tiles - cur.tile)));
       left -= nt;
-      const Row row = row_of(part, cur.s, cur.j * ROWS + r);
-      // tiles of the unit that every row of the warp sees all tokens of (where the part has them all)
-      const int all_see = __reduce_min_sync(0xffffffffu, row.end);
-      int clear = cur.tile;
+      end = row_of(part, cur.s, cur.j * ROWS + r).end;
+      const int all_see = __reduce_min_sync(0xffffffffu, end);
+      clear = cur.tile;
       while (clear < cur.tile + nt && tile_at(part, cur, clear).t0 + TILE <= all_see) ++clear;
       // ---- the query: spans over the whole row, then this quarter's own
-      float f, off;
       {
         float2 x[E / 2];
         const uint32_t qr = sma + C::OFF_Q + r * (2 * D);
@@ -1494,6 +1499,10 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         f = fmaxf(2.0f * amax * qscale, 1e-37f);
         off = sum * (-8.0f / 512.0f);
       }
+      return true;
+    };
+    bool more = begin(0);
+    for (uint32_t u = 0; more; ++u) {
       // ---- tiles
       float m = kNone, l = 0.f;
       for (int k = 0; k < nt; ++k, ++n) {
@@ -1522,7 +1531,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         arrive(ks_empty + b);
         if (!(have & 0x100) || cur.tile + k >= clear) {  // columns that this row does not see
           const Span sp = tile_at(part, cur, cur.tile + k);
-          const int lo = sp.lo - sp.t0 - 32 * qq, hi = min(row.end, sp.hi) - sp.t0 - 32 * qq, h2 = have >> (2 * qq);
+          const int lo = sp.lo - sp.t0 - 32 * qq, hi = min(end, sp.hi) - sp.t0 - 32 * qq, h2 = have >> (2 * qq);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (e < lo || e >= hi || !((h2 >> (e >> 4)) & 1)) v[e] = __float_as_uint(-INFINITY);
@@ -1573,16 +1582,21 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         tc_before();
         arrive(p_full + b);
       }
-      // ---- the unit's outputs: a state, or, where this CTA had all of its tiles, the result
       {
         const float4 all = all_four(l, 2);
         l = (all.x + all.y) + (all.z + all.w);
       }
+      // The next unit's queries first: its scores can be computed while this one's outputs are written.
+      const int was_nt = nt;
+      more = begin(u + 1);
+      // ---- the unit's outputs: a state, or, where this CTA had all of its tiles, the result
       // (S of the last tile was issued before O += P V of the one before it, and a wait for a parity cannot tell a
       // phase from the one two earlier: the unit's end has a barrier of its own)
       wait(unit_done, u & 1);
       tc_after();
-      const bool starts = cur.tile == 0, ends = cur.tile + nt == cur.tiles;
+      const Cursor was = told_cursor(cursors + 16 * (u & 3));
+      const Row row = row_of(part, was.s, was.j * ROWS + r);
+      const bool starts = was.tile == 0, ends = was.tile + was_nt == was.tiles;
       const bool direct = todo != nullptr && starts && ends;
       const uint32_t o_t = quad + COL_O;
       float2 x[E / 2];
@@ -1617,7 +1631,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           sc *= 1.0f / sqrtf(float(D));
         }
         if (row.tok >= 0) {
-          T* dst = out + row.tok * ld_out + int64_t(cur.g * part.G + row.hh) * D + E * qq;
+          T* dst = out + row.tok * ld_out + int64_t(was.g * part.G + row.hh) * D + E * qq;
 #pragma unroll
           for (int c = 0; c < E / 8; ++c) {
             uint32_t o[4];
@@ -1627,8 +1641,8 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           }
         }
       } else {
-        const int J = (cur.s.rows + ROWS - 1) / ROWS;
-        const int64_t unit = unit_base(cur.s.tok0, part.prefix ? 0 : cur.b, part.G, part.Hkv, ROWS) + int64_t(cur.g) * J + cur.j;
+        const int J = (was.s.rows + ROWS - 1) / ROWS;
+        const int64_t unit = unit_base(was.s.tok0, part.prefix ? 0 : was.b, part.G, part.Hkv, ROWS) + int64_t(was.g) * J + was.j;
         const int64_t at = ((todo != nullptr ? 2 * int64_t(blockIdx.x) + (starts ? 1 : 0) : unit + blockIdx.x) * ROWS + r);
         float4* dst = reinterpret_cast<float4*>(ws.o + at * D + E * qq);
 #pragma unroll
@@ -1639,7 +1653,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             if (starts) ws.span[2 * unit] = blockIdx.x;
             if (ends) ws.span[2 * unit + 1] = blockIdx.x;
           } else if (ends) {
-            todo[blockIdx.x] = make_int4(int((cur.tile + per - 1) / per), cur.b, cur.g, cur.j);  // CTAs before this one that had tiles of it
+            todo[blockIdx.x] = make_int4(int((was.tile + per - 1) / per), was.b, was.g, was.j);  // CTAs before this one that had tiles of it
           }
         }
       }
