@@ -1516,16 +1516,14 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         tmem_ld16(s_t + 16, v + 16);
         const int have = there_s[b];
         const uint32_t kf = smem_u32(ksf + b * TILE + 32 * qq);
-        float4 s4[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s4[e].x), "=f"(s4[e].y), "=f"(s4[e].z), "=f"(s4[e].w) : "r"(kf + 16 * e));
         tc_wait_ld();
         const float2 o2 = make_float2(off, off);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), o2), make_float2(s4[e / 4].x, s4[e / 4].y));
-          const float2 c = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), o2), make_float2(s4[e / 4].z, s4[e / 4].w));
+          float4 s4;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s4.x), "=f"(s4.y), "=f"(s4.z), "=f"(s4.w) : "r"(kf + 4 * e));
+          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), o2), make_float2(s4.x, s4.y));
+          const float2 c = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), o2), make_float2(s4.z, s4.w));
           v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y), v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
         }
         arrive(ks_empty + b);
