@@ -27,6 +27,13 @@ struct Heads {
 };
 constexpr int RT = 256;  // threads
 
+// A decode step makes these calls one after another, each hardly longer than
+// its launch: they are programmatic dependents, like the 8-bit calls.
+__device__ __forceinline__ void begin() {
+  fp8::wait_for_previous();
+  fp8::next_may_start();
+}
+
 // Units of `nt` tokens from n0 on.  A thread has unit u = tid % U of every
 // (RT / U * parts)-th head; cs holds a token's cosines, then its sines.  skip: for each token 0 to turn
 // it, 1 to write zeros, 2 to leave its output.
@@ -105,6 +112,7 @@ rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ posi
   const int half = rot >> 1;
   const int64_t n0 = int64_t(blockIdx.x) * tokens;
   const int nt = int(min(int64_t(tokens), N - n0));
+  begin();
   for (int i = threadIdx.x; i < nt * half; i += RT) {
     const int n = i / half, f = i - n * half;
     const float2 v = turn_of(positions[n0 + n], turn_step(inv_freq[f]), scale);
@@ -146,7 +154,7 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
   __shared__ int row[ATOK], posn[ATOK], skip[ATOK];
   __shared__ int cu[CU];
   // CTAs of keys, values and queries in turn, as long as there are all of them: the former are bound by issue, the
-  // latter by memory (one kind after the other: 4 x 2048 tokens 54 us, in turn 44 us)
+  // latter by memory (4 x 2048 tokens, with reading back: queries first 59.9 us, in turn 52.4 us)
   const int m = min(kv_blocks, int(gridDim.x) - 2 * kv_blocks), b = int(blockIdx.x);
   const int which = b < 3 * m ? b % 3 : m < kv_blocks ? (b - 3 * m) & 1 : 2;
   int64_t blk = b < 3 * m ? b / 3 : m < kv_blocks ? m + ((b - 3 * m) >> 1) : b - 2 * m;
@@ -158,6 +166,7 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
   const int nt = int(min(int64_t(nt_max), N - n0));
   const int half = rot >> 1;
   const bool turned = which != 1 && half > 0;
+  begin();
   constexpr int per = RT / TPV;  // vectors at a time
   const int total = nt * x.H, part = int(threadIdx.x) % TPV;
   // The next vector's 64 bytes are loaded before this one is worked on.
@@ -295,6 +304,7 @@ read_kernel(const uint8_t* __restrict__ k_q, const __half* __restrict__ k_s, con
   __shared__ int cu[CU];
   const int64_t n0 = int64_t(blockIdx.x) * tokens;
   const int nt = int(min(int64_t(tokens), N - n0));
+  begin();
   t = near(t, cu);
   if (int(threadIdx.x) < nt) {
     const Place p = place_of(t, int(n0) + threadIdx.x);
@@ -365,8 +375,8 @@ inline void rope_split(int64_t N, int64_t H, int64_t d, int sms, int* tokens, in
   *parts = int(p);
 }
 // Tokens of a CTA that works on `per` of their H vectors at a time: four rounds of them, fewer where
-// that leaves SMs without one (its look-ups take as long as several rounds: 5 x 700 tokens of 16 heads of 64 in 5 tokens a
-// CTA 20 us, in 23 11 us).
+// that leaves SMs without one (its look-ups take as long as several rounds: 5 x 700 tokens of 16 heads of 64, 5 tokens a CTA
+// 20 us, 23 tokens 14 us; two or eight rounds: 4 x 2048 tokens 55.9 and 54.6 us against 52.4 us).
 inline int vector_tokens(int64_t N, int64_t H, int64_t per, int sms) {
   int64_t t = 4 * per / H;
   const int64_t enough = N / sms;
@@ -401,9 +411,9 @@ extern "C" int quarot_rope(const void* q, int64_t Hq, int64_t ld_q, void* q_out,
   rope_split(N, Hq > Hk ? Hq : Hk, d, sms, &tokens, &parts);
   const Heads hq = {q, q_out, ld_q, ld_qo, int(Hq)}, hk = {k, k_out, ld_k, ld_ko, int(Hk)};
   auto kern = dtype == QUAROT_FP16 ? rope_kernel<__half> : rope_kernel<__nv_bfloat16>;
-  kern<<<dim3(unsigned((N + tokens - 1) / tokens), unsigned(parts)), RT, size_t(tokens) * (rot / 2) * sizeof(float2),
-         static_cast<cudaStream_t>(stream)>>>(hq, hk, N, int(d), positions, inv_freq, int(rot), interleaved, scale, tokens);
-  return cuda_ok(cudaGetLastError()) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  return fp8::launch_dependent(kern, dim3(unsigned((N + tokens - 1) / tokens), unsigned(parts)), RT,
+                               size_t(tokens) * rot * sizeof(float), 1, static_cast<cudaStream_t>(stream), hq, hk, N, int(d),
+                               positions, inv_freq, int(rot), interleaved, scale, tokens);
 }
 
 extern "C" int quarot_paged_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* q, int64_t Hq,
@@ -432,13 +442,12 @@ extern "C" int quarot_paged_append(const void* k, int64_t ld_k, const void* v, i
   const int64_t bkv = (N + kt - 1) / kt, bq = Hq > 0 ? (N + q_tokens - 1) / q_tokens * q_parts : 0;
   if (2 * bkv + bq > 0x7fffffff) return QUAROT_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
-    kern<<<unsigned(2 * bkv + bq), RT, 0, static_cast<cudaStream_t>(stream)>>>(
-        hk, hv, hq, N, inv_freq, int(rot), interleaved, scale, k_q, static_cast<__half*>(k_s), v_q,
-        static_cast<__half*>(v_s), t, kt, int(bkv), q_tokens, q_parts);
+    return fp8::launch_dependent(kern, dim3(unsigned(2 * bkv + bq)), RT, 0, 1, static_cast<cudaStream_t>(stream), hk, hv, hq, N,
+                                 inv_freq, int(rot), interleaved, scale, k_q, static_cast<__half*>(k_s), v_q,
+                                 static_cast<__half*>(v_s), t, kt, int(bkv), q_tokens, q_parts);
   };
-  if (dtype == QUAROT_FP16) d == 64 ? go(append_kernel<__half, 64>) : go(append_kernel<__half, 128>);
-  else d == 64 ? go(append_kernel<__nv_bfloat16, 64>) : go(append_kernel<__nv_bfloat16, 128>);
-  return cuda_ok(cudaGetLastError()) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  if (dtype == QUAROT_FP16) return d == 64 ? go(append_kernel<__half, 64>) : go(append_kernel<__half, 128>);
+  return d == 64 ? go(append_kernel<__nv_bfloat16, 64>) : go(append_kernel<__nv_bfloat16, 128>);
 }
 
 extern "C" int quarot_paged_read(const uint8_t* k_q, const void* k_s, const uint8_t* v_q, const void* v_s, int64_t n_pages,
@@ -457,15 +466,15 @@ extern "C" int quarot_paged_read(const uint8_t* k_q, const void* k_s, const uint
   if (!sm_count(&sms)) return QUAROT_ERR_CUDA;
   const int tokens = vector_tokens(N, Hkv, RT / (d / 8), sms);
   auto go = [&](auto kern, auto* ko, auto* vo) {
-    kern<<<unsigned((N + tokens - 1) / tokens), RT, 0, static_cast<cudaStream_t>(stream)>>>(
-        k_q, static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), N, int(Hkv), t, ko, vo, tokens);
+    return fp8::launch_dependent(kern, dim3(unsigned((N + tokens - 1) / tokens)), RT, 0, 1, static_cast<cudaStream_t>(stream), k_q,
+                                 static_cast<const __half*>(k_s), v_q, static_cast<const __half*>(v_s), N, int(Hkv), t, ko, vo,
+                                 tokens);
   };
   auto typed = [&](auto* ko, auto* vo) {
     using T = std::remove_pointer_t<decltype(ko)>;
-    if (d == 64) unrotate ? go(read_kernel<T, 64, true>, ko, vo) : go(read_kernel<T, 64, false>, ko, vo);
-    else unrotate ? go(read_kernel<T, 128, true>, ko, vo) : go(read_kernel<T, 128, false>, ko, vo);
+    if (d == 64) return unrotate ? go(read_kernel<T, 64, true>, ko, vo) : go(read_kernel<T, 64, false>, ko, vo);
+    return unrotate ? go(read_kernel<T, 128, true>, ko, vo) : go(read_kernel<T, 128, false>, ko, vo);
   };
-  if (dtype == QUAROT_FP16) typed(static_cast<__half*>(k_out), static_cast<__half*>(v_out));
-  else typed(static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out));
-  return cuda_ok(cudaGetLastError()) ? QUAROT_OK : QUAROT_ERR_LAUNCH;
+  if (dtype == QUAROT_FP16) return typed(static_cast<__half*>(k_out), static_cast<__half*>(v_out));
+  return typed(static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out));
 }
