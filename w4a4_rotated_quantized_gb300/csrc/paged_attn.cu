@@ -396,8 +396,11 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // each score, 8 sum p' of each output.
 //
 // Softmax: p' = 2^(s - m) v_s, with m raised only when some s + log2 v_s
-// exceeds it by 8, so p' <= 2^8 and the largest is at least 1 (fp16, then its
-// pieces, hold it to 2^-12).  Sums of 2^(s - m) and of p' stay in fp32.
+// exceeds it by 8, and then to 5 below that, so p' <= 2^8 and the largest is at
+// least 2^5: fp16, then its pieces, hold it to 2^-12, and a small one to 2^-18.
+// (With one token that outweighs the others by far, 16 x 4096 tokens, their
+// rounding left 9e-4 of an output where the largest was 1; now 2.4e-4, of which
+// the output's own rounding is 2.1e-4.)  Sums of 2^(s - m) and of p' stay in fp32.
 //
 // A CTA is four warps that unpack and do the softmax, and a fifth that feeds
 // them: it looks up the pages, has the packed tiles copied to shared memory two
@@ -858,7 +861,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
             const float mo = mt[r], x = fmaxf(fmaxf(xch[r], xch[RP + r]), fmaxf(xch[2 * RP + r], xch[3 * RP + r]));
-            al[r] = x > mo ? ex2(mo - 8.0f - x) : 1.0f;
+            al[r] = x > mo ? ex2(mo - 3.0f - x) : 1.0f;
             (r & 1 ? l[r / 2].y : l[r / 2].x) *= al[r];
             (r & 1 ? z[r / 2].y : z[r / 2].x) *= al[r];
           }
@@ -879,7 +882,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
           __syncthreads();
           if (tid < RP) {
             const float x = fmaxf(fmaxf(xch[tid], xch[RP + tid]), fmaxf(xch[2 * RP + tid], xch[3 * RP + tid]));
-            if (x > mt[tid]) mt[tid] = x + 8.0f;
+            if (x > mt[tid]) mt[tid] = x + 3.0f;
           }
           __syncthreads();
           probabilities();
@@ -1925,7 +1928,7 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
 // ------------------------------------------------------------------ host
 // Which kernel a part gets, by the rows that see the same keys: up to 16, the
 // tokens as the MMA's M (each 4, 8 or 16 rows read the keys once); above, the
-// rows.  Sequences of more new rows than that are worked on whole, the shared
+// rows (64 sequences sharing 8000 tokens: 92 us and 46 us).  Sequences of more new rows than that are worked on whole, the shared
 // tokens with their own: the keys are read for every 128 rows anyway.
 struct Plan {
   bool many;
@@ -2013,7 +2016,8 @@ static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half*
   pre.RP = pp.RP;
   if (call.prefix && (rc = pp.many ? many_part(pre, pp, sp, nullptr) : few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
   if ((rc = few_part(own, po, so, call.prefix)) != QUAROT_OK) return rc;
-  // 256 sequences sharing 32768 tokens, 32 heads: a warp a row 8 us, a CTA a row 45 us; 1 x 4097: 5 us and 3 us
+  // a warp a row and a CTA a row: 256 sequences sharing 32768 tokens (8192 rows) 211 and 242 us, 64 sharing 8000 (2048
+  // rows) 46 and 53 us, 16 x 4096 (512) 26.3 and 25.6 us, 1 x 4097 (32) 15.4 and 10.3 us
   const unsigned rows = unsigned(own.N) * unsigned(Hq);
   if (rows > 1024)
     return fp8::launch_dependent(join_rows_kernel<T, D>, dim3((rows + 7) / 8), 256, 0, 1, st, own, so, pre, sp, Hq, unrotate, out,
