@@ -555,3 +555,97 @@ def test_calls_on_other_streams_at_once(q):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(want_b, got_b)
     q.quarot_check_error()
+
+
+# ---------------------------------------------------------------- sizes
+@pytest.mark.parametrize("hint", [1, 4096])
+def test_more_sequences_than_threads(q, hint):
+    """A batch whose sequences no block of threads holds at once; many are empty or all but."""
+    rng = np.random.default_rng(2)
+    B = 1000
+    lengths = rng.integers(0, 40, B)
+    lengths[rng.random(B) < 0.3] = 0
+    new = np.minimum(lengths, rng.integers(0, 4, B))
+    c = Case(lengths, 16, 1, 64, new, seed=5)
+    x = _queries(c.N, 2, 64, BF16, 3)
+    _check_attn(q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint), x, c)
+    kv = torch.randn(c.N, 1, 64, device=DEV).half()
+    q.quarot_paged_append(kv, kv, *c.cache, *c.where)
+    _check_append(c, c.np_cache(), kv, kv, np.zeros(0), False, 1.0)
+    k, v = q.quarot_paged_read(*c.cache, *c.where, n=c.N)
+    assert torch.equal(k, v)
+    q.quarot_check_error()
+
+
+def test_offsets_past_32_bits(q):
+    """Pages whose codes lie more than 4 GB into the cache."""
+    H, ps, d, T = 8, 64, 128, 150
+    n_pages = 2 ** 32 // (H * ps * d // 2) + 40
+    cache = [torch.empty((n_pages, H, ps, d // 2), dtype=torch.uint8, device=DEV), torch.empty((n_pages, H, ps), dtype=FP16, device=DEV)]
+    cache += [torch.empty_like(cache[0]), torch.empty_like(cache[1])]
+    small = Case([T, T], ps, H, d, [T, T])
+    kv = [torch.randn(2 * T, H, d, device=DEV).half() for _ in range(2)]
+    x = _queries(2 * T, 2 * H, d, FP16, 1)
+    table, lens, cu = small.where
+    far = table + (n_pages - small.n_pages)
+    one = _i32([0, T]), _i32([T, 2 * T])
+    for tab, c in ((table, small.cache), (far, cache)):
+        q.quarot_paged_append(*kv, *c, tab, lens, cu)
+    for a, b in zip(q.quarot_paged_read(*small.cache, table, lens, cu, n=2 * T), q.quarot_paged_read(*cache, far, lens, cu, n=2 * T)):
+        assert torch.equal(a, b)
+    for max_q in (1, 300):
+        a, b = (q.quarot_paged_attn(x, *c, tab, lens, cu, max_q=max_q) for tab, c in ((table, small.cache), (far, cache)))
+        assert torch.equal(a, b)
+    del one
+    q.quarot_check_error()
+
+
+@pytest.mark.parametrize("new,shared", [(None, 0), (None, 500), ([200, 1, 90], 0)])
+def test_the_same_bits_every_time(q, new, shared):
+    c = Case([1500, 700, 933], 32, 4, 128, new, shared, seed=2)
+    x = _queries(c.N, 32, 128, FP16, 4)
+    args = c.where
+    first = q.quarot_paged_attn(x, *c.cache, *args, max_q=None if new is None else 200, shared_len=shared)
+    for _ in range(100):
+        out = q.quarot_paged_attn(x, *c.cache, *args, max_q=None if new is None else 200, shared_len=shared)
+        assert torch.equal(out, first)
+    _check_attn(first, x, c)
+    q.quarot_check_error()
+
+
+# ---------------------------------------------------------------- the compiled calls
+def test_compiled_and_general_path_agree(q, monkeypatch):
+    c = Case([300, 70, 20], 32, 2, 128, [40, 1, 20], seed=7)
+    wide = torch.randn(c.N, 12, 128, device=DEV).half()
+    x, k, v = wide[:, :8], wide[:, 8:10], wide[:, 10:]
+    f = _gpu64(_freqs(64))
+    pos = _i32(np.arange(c.N) * 1000)
+    table, lens, cu = c.where
+    assert not isinstance(q._calls, q._GeneralOnly)
+
+    def all_calls():
+        cache = [t.clone() for t in c.cache]
+        turned = q.quarot_paged_append(k, v, *cache, table, lens, cu, q=x, inv_freq=f, interleaved=True, scale=0.5)
+        out = torch.empty(c.N, 8, 128, device=DEV, dtype=FP16)
+        ws = torch.empty(q.quarot_paged_workspace_bytes(c.N, 3, 8, 2, 128, 40, 10), dtype=torch.uint8, device=DEV)
+        got = q.quarot_paged_attn(turned, *cache, table, lens, cu, max_q=40, shared_len=10, sm_scale=0.1, out=out, workspace=ws)
+        assert got is out
+        return [*q.quarot_rope(x, k, pos, f), q.quarot_rope(x, None, pos, f, True, 2.0)[0], turned, *cache, out,
+                q.quarot_paged_attn(turned, *cache, table, lens, cu, unrotate_out=True),
+                *q.quarot_paged_read(*cache, table, lens, cu, n=c.N), *q.quarot_paged_read(*cache, table, lens, out_dtype=BF16, unrotate=True)]
+
+    fast = all_calls()
+    assert q._calls.rope(x, k, pos, f, False, 1.0, None, None) is not None
+    for none in (q._calls.rope(x, k, pos.long(), f, False, 1.0, None, None), q._calls.rope(x, k, pos, f[:12], False, 1.0, None, None),
+                 q._calls.append(k, v.float(), *c.cache, table, lens, cu, None, None, False, 1.0, None),
+                 q._calls.append(k, v, *c.cache, table, lens, cu, None, None, False, 1.0, x),
+                 q._calls.read(*c.cache, table, lens, cu, None, False, 0, None, None),
+                 q._calls.read(*c.cache, table, lens, cu, c.N, False, 7, None, None),
+                 q._calls.attn(x, *c.cache, table, lens, cu, 40, -1, 0.0, False, None, None),
+                 q._calls.attn(x[:, :3], *c.cache, table, lens, cu, 40, 0, 0.0, False, None, None),
+                 q._calls.attn(x, *c.cache[:3], c.cache[0], table, lens, cu, 40, 0, 0.0, False, None, None)):
+        assert none is None
+    monkeypatch.setattr(q, "_calls", q._GeneralOnly())
+    for a, b in zip(fast, all_calls()):
+        assert a.dtype == b.dtype and torch.equal(a, b)
+    q.quarot_check_error()

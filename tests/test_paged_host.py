@@ -176,3 +176,25 @@ def test_float64_rope_turns_pairs():
     assert abs(y[0, 0, 5] - 1.0) < 1e-12 and abs(y[0, 0, 1]) < 1e-12
     y = O.rope(x, [1], np.array([math.pi / 2] + [0.0] * 3), interleaved=True)  # pair 0 is (0, 1)
     assert abs(y[0, 0, 0] + 1.0) < 1e-12
+
+
+def test_the_version_tells_of_the_paged_cache(lib):
+    assert q.quarot_version() >> 16 == 1 and q.quarot_version() & 0xFFFF >= 3
+    import os
+    with open(os.path.join(os.path.dirname(q.__file__), os.pardir, "include", "quarot.h")) as f:
+        told = " ".join(f.read().split("1.3 adds")[1].split("*/")[0].replace("*", " ").split())
+    for name in ("rope", "paged_append", "paged_read", "paged_workspace_bytes", "paged_attn"):
+        assert f"quarot_{name}" in told
+    for name in ("rope", "append", "read", "attn"):
+        assert getattr(q._GeneralOnly(), name)(1, 2, 3) is None
+
+
+def test_compiled_calls_take_nothing_on_the_cpu(lib):
+    x = torch.zeros(2, 4, 128, dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    cache = (torch.zeros(3, 4, 16, 64, dtype=torch.uint8), torch.zeros(3, 4, 16, dtype=torch.float16)) * 2
+    where = (torch.zeros(2, 3, dtype=torch.int32), i, None)
+    assert q._calls.rope(x, x, i, None, False, 1.0, None, None) is None
+    assert q._calls.append(x, x, *cache, *where, None, None, False, 1.0, None) is None
+    assert q._calls.read(*cache, *where, None, False, 0, None, None) is None
+    assert q._calls.attn(x, *cache, *where, 1, 0, 0.0, False, None, None) is None
