@@ -64,6 +64,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
@@ -1031,6 +1036,16 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -1067,12 +1082,13 @@ __device__ __forceinline__ void hadamard_regs(float2* x) {
       if ((i & s) == 0) {
         const float2 a = x[i], b = x[i + s];
         x[i] = __fadd2_rn(a, b);
-        x[i + s] = __fadd2_rn(a, make_float2(-b.x, -b.y));
+        x[i + s] = __ffma2_rn(b, make_float2(-1.f, -1.f), a);
       }
 }
 
 struct Values {  // constants of the values' conversion, like Masks
-  uint32_t mask, flip;  // 0x000F000F, 0x64086408
+  uint32_t mask, flip;      // 0x000F000F, 0x64086408: 1024 + u of the lowest nibble
+  uint32_t mask16, flip16;  // 0x00F000F0, 0x64806480: 1024 + 16 u of the next
 };
 
 // direct: units that a CTA works on alone are written to out; of the others
@@ -1359,7 +1375,9 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[e] = hmul2(hadd2(((w[i][j] >> (4 * e)) & vals.mask) ^ vals.flip, 0xE408E408u /* -1032 */), vs2[i]);
+              o[e] = hmul2(e & 1 ? hfma2(((w[i][j] >> (4 * (e & 2))) & vals.mask16) ^ vals.flip16, 0x2C002C00u, 0xD480D480u)  // (1024 + 16 u) / 16 - 72
+                                 : hadd2(((w[i][j] >> (4 * e)) & vals.mask) ^ vals.flip, 0xE408E408u),  // (1024 + u) - 1032
+                           vs2[i]);
             const uint32_t chunk = WPT == 4 ? uint32_t(4 * (c4 & 1) + (j ^ (c4 & 2))) : uint32_t(2 * c4 + j);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v_row + 1024 * i + ((chunk ^ r4) << 4)), "r"(o[0]),
                          "r"(o[1]), "r"(o[2]), "r"(o[3])
@@ -1425,7 +1443,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
     };
     uint32_t n = 0;
     float f = 0.f, off = 0.f;
-    int end = 0, clear = 0, nt = 0;  // of the unit at work: what the row sees, tiles that all rows of the warp see whole, tiles
+    int end = 0, clear = 0, nt = 0;  // of the unit at work: what the row sees, tiles before one that not all rows of the warp see whole, tiles
     // The next unit: false where there is none.
     auto begin = [&](uint32_t u) -> bool {
       if (left <= 0) return false;
@@ -1439,8 +1457,11 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       left -= nt;
       end = row_of(part, cur.s, cur.j * ROWS + r).end;
       const int all_see = __reduce_min_sync(0xffffffffu, end);
-      clear = cur.tile;
-      while (clear < cur.tile + nt && tile_at(part, cur, clear).t0 + TILE <= all_see) ++clear;
+      clear = all_see / TILE;
+      if (!part.prefix) {
+        const int np = part.whole ? (min(cur.s.len, part.shared) + TILE - 1) / TILE : 0;
+        if (clear >= np) clear = np + max(clear - cur.s.tile0, 0);
+      }
       // ---- the query: spans over the whole row, then this quarter's own
       {
         float2 x[E / 2];
@@ -1468,31 +1489,43 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         const float up = amax > 0.f ? 256.0f / amax : 0.f;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) x[i] = __fmul2_rn(x[i], make_float2(up, up));
-        float sum = 0.f;
-#pragma unroll 1
-        for (int p = 0; p < 3; ++p) {
-          uint32_t o[E / 4];
+        // their sum is what they were made from less what is left in the end
+        float2 sums = make_float2(0.f, 0.f);
+        uint32_t rest[E / 2];  // of pairs of even, pairs of odd dims; after the first piece at most 8, in fp16 off by 2^-17 of the largest
+        uint32_t o[E / 4];
+        const uint32_t to = quad + COL_Q + qq * (D / 16);
+        auto put = [&](int p) {
+          if constexpr (E == 32) tmem_st8(to + p * (D / 4), o);
+          else tmem_st4(to + p * (D / 4), o);
+        };
 #pragma unroll
-          for (int w = 0; w < E / 8; ++w) {
-            // bytes of a word's dims: even ones, then odd ones
-            uint32_t e[4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float2 &a = x[4 * w + 2 * k], &b = x[4 * w + 2 * k + 1];  // dims 4 k, 4 k + 1 and 4 k + 2, 4 k + 3
-              e[k] = fp8::cvt_e4m3x2(make_float2(a.x, b.x));
-              e[2 + k] = fp8::cvt_e4m3x2(make_float2(a.y, b.y));
-              const float2 ev = h2_to_f2(h2_of_e4m3x2(e[k])), od = h2_to_f2(h2_of_e4m3x2(e[2 + k]));
-              sum += (ev.x + ev.y) + (od.x + od.y);
-              a = make_float2(a.x - ev.x, a.y - od.x);
-              b = make_float2(b.x - ev.y, b.y - od.y);
-            }
-            o[2 * w] = e[0] | (e[1] << 16);
-            o[2 * w + 1] = e[2] | (e[3] << 16);
-          }
-          const uint32_t to = quad + COL_Q + p * (D / 4) + qq * (D / 16);
-          if constexpr (E == 32) tmem_st8(to, o);
-          else tmem_st4(to, o);
+        for (int i = 0; i < E / 4; ++i) {  // dims 4 i, 4 i + 1 and 4 i + 2, 4 i + 3: bytes of a word's dims are the even ones, then the odd ones
+          const float2 a = x[2 * i], c = x[2 * i + 1];
+          sums = __fadd2_rn(sums, __fadd2_rn(a, c));
+          const uint32_t e0 = fp8::cvt_e4m3x2(make_float2(a.x, c.x)), e1 = fp8::cvt_e4m3x2(make_float2(a.y, c.y));
+          const float2 ev = h2_to_f2(h2_of_e4m3x2(e0)), od = h2_to_f2(h2_of_e4m3x2(e1));
+          rest[2 * i] = h2_of_f2(a.x - ev.x, c.x - ev.y);
+          rest[2 * i + 1] = h2_of_f2(a.y - od.x, c.y - od.y);
+          const int w = 2 * (i / 2);
+          o[w] = i & 1 ? o[w] | (e0 << 16) : e0;
+          o[w + 1] = i & 1 ? o[w + 1] | (e1 << 16) : e1;
         }
+        put(0);
+#pragma unroll
+        for (int p = 1; p < 3; ++p) {
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const uint32_t e = e4m3x2_of_h2(rest[i]);
+            rest[i] = hsub2(rest[i], h2_of_e4m3x2(e));
+            const int w = 2 * (i / 4) + (i & 1);
+            o[w] = i & 2 ? o[w] | (e << 16) : e;
+          }
+          put(p);
+        }
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i) rest[0] = hadd2(rest[0], rest[i]);
+        const float2 left_over = h2_to_f2(rest[0]);
+        float sum = (sums.x + sums.y) - (left_over.x + left_over.y);
         tc_wait_st();
         tc_before();
         all = all_four(sum, 1);
@@ -1596,33 +1629,29 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       wait(unit_done, u & 1);
       tc_after();
       const Cursor was = told_cursor(cursors + 16 * (u & 3));
-      const Row row = row_of(part, was.s, was.j * ROWS + r);
       const bool starts = was.tile == 0, ends = was.tile + was_nt == was.tiles;
       const bool direct = todo != nullptr && starts && ends;
       const uint32_t o_t = quad + COL_O;
       float2 x[E / 2];
-      // 16 columns are two words' dims: column 8 w + 2 k + e is dim 8 w + k + 4 e
+      // 8 columns are a word's dims: column 2 k + e is dim k + 4 e
       auto in_order = [&](const uint32_t* a, int i) {
-        auto dim = [&](int d) { return __uint_as_float(a[(d & 8) + 2 * (d & 3) + ((d >> 2) & 1)]); };
+        auto dim = [&](int d) { return __uint_as_float(a[2 * (d & 3) + (d >> 2)]); };
         return make_float2(dim(2 * i), dim(2 * i + 1));
       };
 #pragma unroll
-      for (int c = 0; c < E / 16; ++c) {
+      for (int c = 0; c < E / 8; ++c) {
+        uint32_t a[4][8];
         if (direct && unrotate) {
-          uint32_t a[2][16], bq[2][16];
-          tmem_ld16(o_t + 16 * c, a[0]);
-          tmem_ld16(o_t + E + 16 * c, a[1]);
-          tmem_ld16(o_t + 2 * E + 16 * c, bq[0]);
-          tmem_ld16(o_t + 3 * E + 16 * c, bq[1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld8(o_t + E * k + 8 * c, a[k]);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[8 * c + i] = spans(in_order(a[0], i), in_order(a[1], i), in_order(bq[0], i), in_order(bq[1], i));
+          for (int i = 0; i < 4; ++i) x[4 * c + i] = spans(in_order(a[0], i), in_order(a[1], i), in_order(a[2], i), in_order(a[3], i));
         } else {
-          uint32_t a[16];
-          tmem_ld16(o_t + E * qq + 16 * c, a);
+          tmem_ld8(o_t + E * qq + 8 * c, a[0]);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[8 * c + i] = in_order(a, i);
+          for (int i = 0; i < 4; ++i) x[4 * c + i] = in_order(a[0], i);
         }
       }
       if (direct) {
@@ -1631,6 +1660,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           hadamard_regs<E>(x);
           sc *= 1.0f / sqrtf(float(D));
         }
+        const Row row = row_of(part, was.s, was.j * ROWS + r);
         if (row.tok >= 0) {
           T* dst = out + row.tok * ld_out + int64_t(was.g * part.G + row.hh) * D + E * qq;
 #pragma unroll
@@ -1996,7 +2026,7 @@ static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half*
     auto kern = many::many_kernel<T, D>;
     if (!smem_attr_once(kern, many::Cfg<D>::SMEM, attr)) return QUAROT_ERR_LAUNCH;
     return fp8::launch_dependent(kern, dim3(unsigned(plan.ctas)), many::NT, many::Cfg<D>::SMEM, 1, st, q, ld_q, k_q, k_s, v_q, v_s,
-                                 part, qscale, ws, todo, unrotate, out, ld_out, masks, many::Values{0x000F000Fu, 0x64086408u});
+                                 part, qscale, ws, todo, unrotate, out, ld_out, masks, many::Values{0x000F000Fu, 0x64086408u, 0x00F000F0u, 0x64806480u});
   };
   const Plan &po = call.own, &pp = call.pre;
   own.RP = po.RP;
