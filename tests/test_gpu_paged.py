@@ -364,6 +364,24 @@ def test_attn_leaves_rows_behind_the_last_sequence(q, max_q):
     assert (out[7:] == 9.0).all()
 
 
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at,pitch", [(0, 0), (8, 0), (0, 8), (8, 8)])
+def test_attn_outputs_at_every_alignment(q, dtype, d, at, pitch):
+    """Outputs whose first row or whose pitch is a multiple of 16 bytes, not of 32."""
+    c = Case([300, 150], 32, 2, d, [260, 41], seed=d)
+    x = _queries(c.N, 8, d, dtype, 6)
+    flat = torch.full((at + c.N * (8 * d + pitch) + 64,), 3.0, dtype=dtype, device=DEV)
+    out = flat.as_strided((c.N, 8, d), (8 * d + pitch, d, 1), at)
+    for un in (False, True):
+        q.quarot_paged_attn(x, *c.cache, *c.where, max_q=260, unrotate_out=un, out=out)
+        q.quarot_check_error()
+        _check_attn(out, x, c, unrotate=un)
+    kept = torch.ones_like(flat, dtype=torch.bool)
+    kept.as_strided((c.N, 8, d), (8 * d + pitch, d, 1), at)[:] = False
+    assert (flat[kept] == 3.0).all()
+
+
 @pytest.mark.parametrize("max_q", [1, 1000])
 def test_pages_that_are_not_there(q, max_q):
     """A table entry outside the cache and a length past the table are errors that quarot_check_error reports; the other

@@ -972,6 +972,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 //               queries rotated and split into e4m3 pieces at a unit's start,
 //               scores to probabilities, outputs at its end
 //   warp 22     the next unit: which it is, and its queries
+//   warp 23     key scales
 // Tensor memory: the three pieces of the queries (A operand of S), two score
 // buffers, in which fp16 probabilities take the place of the scores that they
 // were made from, and O.  S(n + 1) runs while the softmax works on S(n).
@@ -980,11 +981,20 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // row's factor; the references are raised as in `few`, without the value
 // scales, which the values carry here.
 //
-// What bounds it: 12 MMAs of 128 x 128 x 32 for S and 8 of 128 x 128 x 16 for
-// P V a tile, some 90 clocks each.
+// What bounds it: the hand-overs between these roles.  A tile takes some 2800
+// clocks.  The MMAs need 1350 of them (12 of 128 x 128 x 32 for S and 8 of
+// 128 x 128 x 16 for P V, each of the two after what it waits for), the
+// converters 1600 busy and four waits, the softmax 2100 busy and two waits; with
+// no one of the three does it take more than a tenth less (256 sequences sharing
+// 32768 tokens: no exponentials 0, a third of the MMAs 0, no conversion 9 %).
+// Two score buffers are what tensor memory has room for.  A unit's start and end
+// cost some 14000 clocks more, of which the tensor cores wait for 8000: queries
+// rotated and split (e4m3 conversions run at a few lanes a clock), outputs
+// rotated back.  256 sharing 32768: 200 us, 687 TFLOP/s of the formula's
+// products; 4 x 2048 tokens: 337 us, 408 TFLOP/s.
 namespace many {
 
-constexpr int NT = 736, ROWS = 128, NCW = 4, NSW = 16, SP = 3, UNIT_READERS = 2 + NCW + NSW;
+constexpr int NT = 768, ROWS = 128, NCW = 4, NSW = 16, SP = 3, UNIT_READERS = 3 + NCW + NSW;
 constexpr uint32_t COL_Q = 0, COL_S = 128, COL_O = 384;  // S buffer b at COL_S + 128 b
 
 template <int D>
@@ -1123,6 +1133,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   volatile int* there = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);      // [SP] groups of 16 tokens that a packed tile has
   volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers; 0x100: all tokens are there
+  volatile int64_t* each = reinterpret_cast<volatile int64_t*>(sm + C::OFF_MISC + 32);  // tiles of a CTA
   float* ksf = reinterpret_cast<float*>(sm + C::OFF_KS);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
   int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [4][16]
@@ -1131,7 +1142,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   if (tid == 0) {
     for (int i = 0; i < SP; ++i) {
       mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, NCW);
+      mbar_init(raw_empty + i, NCW + 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, NCW);
@@ -1140,7 +1151,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, NSW);
-      mbar_init(ks_full + i, NCW);
+      mbar_init(ks_full + i, 1);
       mbar_init(ks_empty + i, NSW);
     }
     mbar_init(unit_full, 33);  // each lane's copies, and the cursor
@@ -1166,7 +1177,10 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   Cursor cur;
   int64_t per;
   int64_t left = find_start(part, cur, per, reinterpret_cast<int64_t*>(sm + C::OFF_X));
-  if (todo != nullptr && tid == 0) todo[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0) {
+    *each = per;  // (the softmax reads it behind barriers that follow this warp's copies)
+    if (todo != nullptr) todo[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
 
   auto wait = [&](uint64_t* bar, uint32_t phase, bool copy = false) {
     bool ok = mbar_try_wait(bar, phase);
@@ -1294,7 +1308,6 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   } else if (warp < 2 + NCW) {
     // ================================================================ converters
     const int cw = warp - 2, r4 = lane >> 2, c4 = lane & 3;
-    const int ctid = 32 * cw + lane;
     uint32_t n = 0;
     for (uint32_t u = 0; left > 0; ++u) {
       cur = unit_at(u);
@@ -1337,18 +1350,16 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         }
         to_async_proxy();
         arrive(k_full + b);
-        // ---- key scales, 0 where the part has no token
         uint32_t half;
         const uint32_t scales = sma + C::OFF_RAW + st * C::STAGE + 2 * C::CODES;
-        const int tok = sp.t0 + ctid;
-        const bool mine = tok >= sp.lo && tok < sp.hi && ((have >> (ctid >> 4)) & 1);
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * ctid));
-        if (n > 1) wait(ks_empty + b, ((n >> 1) - 1) & 1);
-        ksf[b * TILE + ctid] = mine ? __half2float(__ushort_as_half(uint16_t(half))) : 0.f;
-        if (ctid == 0) there_s[b] = have | (have == 0xFF && sp.t0 >= sp.lo && sp.t0 + TILE <= sp.hi ? 0x100 : 0);
-        arrive(ks_full + b);
         // ---- values: fp16 code * scale, pairs (k, k + 4) of a word's dims; 0 where the part has no token
-        words(raw + C::CODES);
+        // (4 words: lanes of the two halves of a token change their pairs, to store different chunks at a time)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = raw + C::CODES + 8 * (D / 2) * i, first = WPT == 4 ? 4 * (c4 & 2) : 0;
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at + first));
+          if constexpr (WPT == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][2]), "=r"(w[i][3]) : "r"(at + (first ^ 8)));
+        }
         uint32_t vs2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1362,14 +1373,6 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         const uint32_t v_row = sma + C::OFF_V + b * C::VBYTES + (32 * cw + r4) * 128 + (WPT == 4 ? (c4 >> 1) * C::ATOM : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (WPT == 4) {  // lanes of the two halves of a token store different chunks at a time
-            if (c4 & 2) {
-              uint32_t x = w[i][0];
-              w[i][0] = w[i][2], w[i][2] = x;
-              x = w[i][1];
-              w[i][1] = w[i][3], w[i][3] = x;
-            }
-          }
 #pragma unroll
           for (int j = 0; j < WPT; ++j) {
             uint32_t o[4];
@@ -1386,6 +1389,34 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         }
         to_async_proxy();
         arrive(v_full + b);
+      }
+    }
+  } else if (warp == 3 + NCW + NSW) {
+    // ================================================================ key scales
+    uint32_t n = 0;
+    for (uint32_t u = 0; left > 0; ++u) {
+      cur = unit_at(u);
+      arrive(unit_empty);
+      if (cur.tiles == 0) break;
+      const int nt = int(min(left, int64_t(cur.tiles - cur.tile)));
+      left -= nt;
+      for (int k = 0; k < nt; ++k, ++n) {
+        const Span sp = tile_at(part, cur, cur.tile + k);
+        const uint32_t st = n % SP, b = n & 1;
+        wait(raw_full + st, (n / SP) & 1, true);
+        const int have = there[st], tok = sp.t0 + 4 * lane;
+        uint2 h;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(h.x), "=r"(h.y) : "r"(sma + C::OFF_RAW + st * C::STAGE + 2 * C::CODES + 8 * lane));
+        arrive(raw_empty + st);
+        const float2 lo = h2_to_f2(h.x), hi = h2_to_f2(h.y);
+        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+        float e[4];  // 0 where the part has no token
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = tok + i >= sp.lo && tok + i < sp.hi && ((have >> (lane >> 2)) & 1) ? f[i] : 0.f;
+        if (n > 1) wait(ks_empty + b, ((n >> 1) - 1) & 1);
+        reinterpret_cast<float4*>(ksf + b * TILE)[lane] = make_float4(e[0], e[1], e[2], e[3]);
+        if (lane == 0) there_s[b] = have | (have == 0xFF && sp.t0 >= sp.lo && sp.t0 + TILE <= sp.hi ? 0x100 : 0);
+        arrive(ks_full + b);
       }
     }
   } else if (warp == 2 + NCW + NSW) {
@@ -1441,20 +1472,22 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
       const float2 s1 = make_float2(qq & 1 ? -1.f : 1.f, qq & 1 ? -1.f : 1.f), s2 = make_float2(qq & 2 ? -1.f : 1.f, qq & 2 ? -1.f : 1.f);
       return __ffma2_rn(__ffma2_rn(d, s1, c), s2, __ffma2_rn(b, s1, a));
     };
+    int rem = int(left);  // of this CTA's tiles
     uint32_t n = 0;
     float f = 0.f, off = 0.f;
-    int end = 0, clear = 0, nt = 0;  // of the unit at work: what the row sees, tiles before one that not all rows of the warp see whole, tiles
+    int tile = 0, end = 0, clear = 0, nt = 0;  // of the unit at work: what the row sees, tiles before one that not all rows of the warp see whole, tiles
     // The next unit: false where there is none.
     auto begin = [&](uint32_t u) -> bool {
-      if (left <= 0) return false;
-      cur = unit_at(u);
+      if (rem <= 0) return false;
+      const Cursor cur = unit_at(u);
+      tile = cur.tile;
       if (cur.tiles == 0) {
         arrive(unit_empty);
-        left = 0;
+        rem = 0;
         return false;
       }
-      nt = int(min(left, int64_t(cur.tiles - cur.tile)));
-      left -= nt;
+      nt = min(rem, cur.tiles - cur.tile);
+      rem -= nt;
       end = row_of(part, cur.s, cur.j * ROWS + r).end;
       const int all_see = __reduce_min_sync(0xffffffffu, end);
       clear = all_see / TILE;
@@ -1563,8 +1596,8 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y), v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
         }
         arrive(ks_empty + b);
-        if (!(have & 0x100) || cur.tile + k >= clear) {  // columns that this row does not see
-          const Span sp = tile_at(part, cur, cur.tile + k);
+        if (!(have & 0x100) || tile + k >= clear) {  // columns that this row does not see
+          const Span sp = tile_at(part, told_cursor(cursors + 16 * (u & 3)), tile + k);
           const int lo = sp.lo - sp.t0 - 32 * qq, hi = min(end, sp.hi) - sp.t0 - 32 * qq, h2 = have >> (2 * qq);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
@@ -1664,11 +1697,18 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         if (row.tok >= 0) {
           T* dst = out + row.tok * ld_out + int64_t(was.g * part.G + row.hh) * D + E * qq;
 #pragma unroll
-          for (int c = 0; c < E / 8; ++c) {
-            uint32_t o[4];
+          for (int c = 0; c < E / 16; ++c) {
+            uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = fp8::from_f2<T>(make_float2(x[4 * c + i].x * sc, x[4 * c + i].y * sc));
-            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < 8; ++i) o[i] = fp8::from_f2<T>(make_float2(x[8 * c + i].x * sc, x[8 * c + i].y * sc));
+            if (((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld_out * 2)) & 31) == 0) {  // whole sectors (4 x 2048 tokens: 337 us, 343 us without)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * c), "r"(o[0]), "r"(o[1]),
+                           "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
           }
         }
       } else {
@@ -1684,7 +1724,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             if (starts) ws.span[2 * unit] = blockIdx.x;
             if (ends) ws.span[2 * unit + 1] = blockIdx.x;
           } else if (ends) {
-            todo[blockIdx.x] = make_int4(int((was.tile + per - 1) / per), was.b, was.g, was.j);  // CTAs before this one that had tiles of it
+            todo[blockIdx.x] = make_int4(int((was.tile + *each - 1) / *each), was.b, was.g, was.j);  // CTAs before this one that had tiles of it
           }
         }
       }
