@@ -405,7 +405,9 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // least 2^5: fp16, then its pieces, hold it to 2^-12, and a small one to 2^-18.
 // (With one token that outweighs the others by far, 16 x 4096 tokens, their
 // rounding left 9e-4 of an output where the largest was 1; now 2.4e-4, of which
-// the output's own rounding is 2.1e-4.)  Sums of 2^(s - m) and of p' stay in fp32.
+// the output's own rounding is 2.1e-4.)  Sums of 2^(s - m) and of p' stay in fp32,
+// those of p' over what the products take, so that a rounding weighs a code and not
+// code + 8 (35 tokens: error 4.2e-4 without).
 //
 // A CTA is four warps that unpack and do the softmax, and a fifth that feeds
 // them: it looks up the pages, has the packed tiles copied to shared memory two
@@ -828,8 +830,10 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
             for (int h = 0; h < 2; ++h) {
               const float2 m = mtop[r + h], y = __fadd2_rn(s[r + h], make_float2(8.0f - m.x, 8.0f - m.y));
               w[r + h] = make_float2(ex2(y.x), ex2(y.y));
-              p[r + h] = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
-              pieces_of(h2_of_f2(p[r + h].x, p[r + h].y), c[h]);
+              const float2 x = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
+              const uint32_t as_used = h2_of_f2(x.x, x.y);
+              p[r + h] = h2_to_f2(as_used);
+              pieces_of(as_used, c[h]);
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) pw[k][r / 2] = c[0][k] | (c[1][k] << 16);
