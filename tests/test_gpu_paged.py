@@ -364,6 +364,32 @@ def test_attn_leaves_rows_behind_the_last_sequence(q, max_q):
     assert (out[7:] == 9.0).all()
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
+@pytest.mark.parametrize("where", [0, 77, 199])
+def test_infinite_values_stay_with_the_tokens_that_see_them(q, max_q, where):
+    """A value of infinite elements, and the largest scales: rows before it are what they are without it."""
+    new = 200
+    c = Case([new + 30], 32, 2, 128, [new], seed=8)
+    x, out = _queries(new, 8, 128, FP16, 3), []
+    page, slot = int(c.table[0, (where + 30) // 32]), (where + 30) % 32
+    v = torch.randn(1, 2, 128, device=DEV).half()
+    v[:, :, 5] = float("inf")
+    pool = [t.clone() for t in c.cache]
+    q.quarot_paged_append(v, v, *pool, _i32(c.table[:, :]), _i32([where + 31]))  # one token, at position where + 30
+    assert torch.isfinite(pool[3][page, :, slot]).all() and (pool[3][page, :, slot] > 8188).all()
+    for scale in (None, 65504.0):
+        if scale:
+            pool[1][page, :, slot] = pool[3][page, :, slot] = scale
+        y = q.quarot_paged_attn(x, *pool, *c.where, max_q=max_q)
+        q.quarot_check_error()
+        out.append(y[:where])
+    ref, tol = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps)
+    ref, tol = ref[:where], np.broadcast_to(tol, ref.shape)[:where]
+    for y in out:
+        assert torch.isfinite(y).all()
+        assert (np.abs(_np(y) - ref) <= tol + _half_step(ref + np.sign(ref) * tol, FP16)).all()
+
+
 @pytest.mark.parametrize("dtype", [FP16, BF16])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("at,pitch", [(0, 0), (8, 0), (0, 8), (8, 8)])

@@ -1370,6 +1370,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           const int t = 32 * cw + 8 * i + r4;
           asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * TILE + 2 * t));
           const bool in = sp.t0 + t >= sp.lo && sp.t0 + t < sp.hi && ((have >> (t >> 4)) & 1);
+          half = min(half & 0x7FFFu, 0x6FFFu) | (half & 0x8000u);  // 8188: a product stays finite, as rows that do not see it need
           vs2[i] = in ? half | (half << 16) : 0u;
         }
         arrive(raw_empty + st);
