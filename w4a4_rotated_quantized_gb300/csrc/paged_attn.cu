@@ -417,6 +417,10 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // was read.  The barrier also tells whether some thread's score passed its
 // reference; then the references are raised and the probabilities made again
 // (a unit's first tile sets them before).  Several CTAs on an SM fill each other's waits.
+//
+// What bounds it: a tile's chain of hand-overs, and with few tiles a CTA the
+// launches and the join.  32 query and 8 key heads of 128, with the join: 16 x 4096
+// tokens 26 us (2.7 TB/s of pages), 64 x 4096 66 us (4.2 TB/s), 1 x 4097 10 us.
 namespace few {
 
 constexpr int NT = 160;
