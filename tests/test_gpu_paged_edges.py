@@ -1,0 +1,52 @@
+"""The paged cache at the edges of its range: long and unequal sequences, loud and missing values, pages that change hands."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as O
+from test_gpu_paged import BF16, FP16, _i32, _np
+from test_gpu_parity import DEV, q  # noqa: F401  (q: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _row_errors(out, ref):
+    """Norm of each row's difference over its own norm."""
+    return np.linalg.norm(_np(out) - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+
+
+# ---------------------------------------------------------------- precision
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+def test_one_loud_token_among_many_small_ones(q, dtype):
+    """A token that outweighs each of 32767 others 2^24 times, with a CTA that has all of them (38 sequences x 16 heads are
+    608 units).  Rows: the loud token's probability and the output are rounded, half a step of fp16 and of the output's
+    type; sums of 1024 products of 32 tokens, 2^-24 each of values 15 / |o| times as large; the small tokens' share."""
+    B, H, d, ps, L = 38, 16, 64, 64, 32768
+    rng = np.random.default_rng(5)
+    pages = L // ps
+    shape = (pages, H, ps)
+    kq, vq = (rng.integers(0, 256, shape + (d // 2,), dtype=np.uint8) for _ in range(2))
+    ks, vs = np.full(shape, 0.35, np.float16), rng.uniform(0.2, 0.4, shape).astype(np.float16)
+    x = (rng.standard_normal((1, H, d)) * 0.05).astype(np.float32)
+    x = torch.from_numpy(x).to(dtype).to(DEV).expand(B, H, d).contiguous()
+    turned = _np(x[0]) @ O.hadamard(d)
+    c = np.round(turned / np.abs(turned).max(-1, keepdims=True) * 7).astype(np.int64)  # a key along each head's query
+    kq[0, :, 5] = ((c[:, 0::2] & 15) | ((c[:, 1::2] & 15) << 4)).astype(np.uint8)
+    ks[0, :, 5] = (24 * np.log(2) / ((c * turned).sum(-1) / np.sqrt(d))).astype(np.float16)
+    cache = [torch.from_numpy(a).to(DEV) for a in (kq, ks, vq, vs)]
+    table = np.tile(np.arange(pages), (B, 1))
+    out = q.quarot_paged_attn(x, *cache, _i32(table), _i32([L] * B), max_q=1)
+    q.quarot_check_error()
+    (kc, ksd), (vc, vsd) = (O.tokens([kq, ks, vq, vs], table[0], ps, L, w) for w in (0, 1))
+    half = torch.finfo(dtype).eps / 2
+    for h in range(H):
+        s = (kc[:, h] @ turned[h]) * ksd[:, h] / np.sqrt(d)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        assert p[5] > 0.99 and np.median(p) < 2.0 ** -22.5
+        v = (p * vsd[:, h])[:, None] * vc[:, h]
+        ref = v.sum(0)
+        err = np.linalg.norm(_np(out[:, h]) - ref, axis=-1)
+        small = np.linalg.norm(ref - v[5])
+        sums = L / 32 * 2.0 ** -24 * 15 * (p * vsd[:, h]).sum() * np.sqrt(d)
+        assert (err <= (half + 2.0 ** -11) * np.linalg.norm(ref) + small + sums).all(), (h, err.max() / np.linalg.norm(ref))

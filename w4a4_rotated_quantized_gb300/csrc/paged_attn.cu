@@ -144,14 +144,18 @@ __device__ __forceinline__ uint32_t rest16(uint32_t a, uint32_t b) {
   asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(0x4C004C00u));
   return d;
 }
-// An fp16 pair as three e4m3 pairs, a = c0 + c1 / 16 + c2 / 256: 4 bits of
-// fraction each hold all 11 of an fp16 (below 2^-6 fewer, never below 2^-18).
-__device__ __forceinline__ void pieces_of(uint32_t a, uint32_t* c) {
+// An fp16 pair as three e4m3 pairs, a = c0 + c1 / 16 + c2 / 256 + what is
+// returned / 256: 4 bits of fraction each hold all 11 of an fp16 down to 2^-6,
+// fewer below, and nothing below 2^-18.
+__device__ __forceinline__ uint32_t pieces_of(uint32_t a, uint32_t* c) {
   c[0] = e4m3x2_of_h2(a);
   a = rest16(a, h2_of_e4m3x2(c[0]));
   c[1] = e4m3x2_of_h2(a);
   a = rest16(a, h2_of_e4m3x2(c[1]));
   c[2] = e4m3x2_of_h2(a);
+  uint32_t left;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(a), "r"(h2_of_e4m3x2(c[2])));
+  return left;
 }
 
 // ------------------------------------------------------------------ units
@@ -406,8 +410,10 @@ __device__ __forceinline__ Row row_of(const Part& p, const Seq& s, int rr) {
 // (With one token that outweighs the others by far, 16 x 4096 tokens, their
 // rounding left 9e-4 of an output where the largest was 1; now 2.4e-4, of which
 // the output's own rounding is 2.1e-4.)  Sums of 2^(s - m) and of p' stay in fp32,
-// those of p' over what the products take, so that a rounding weighs a code and not
-// code + 8 (35 tokens: error 4.2e-4 without).
+// those of p' over what the products take, which is the pieces' sum, so that a
+// rounding weighs a code and not code + 8 (35 tokens: error 4.2e-4 without; over the
+// fp16 values, whose small ones lose bits in the pieces, 32768 tokens of which one
+// outweighs the others 2^24 times: 4.5e-3, now 3.9e-4).
 //
 // A CTA is four warps that unpack and do the softmax, and a fifth that feeds
 // them: it looks up the pages, has the packed tiles copied to shared memory two
@@ -835,9 +841,9 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
               const float2 m = mtop[r + h], y = __fadd2_rn(s[r + h], make_float2(8.0f - m.x, 8.0f - m.y));
               w[r + h] = make_float2(ex2(y.x), ex2(y.y));
               const float2 x = __fmul2_rn(w[r + h], make_float2(scales.y, scales.y));
-              const uint32_t as_used = h2_of_f2(x.x, x.y);
-              p[r + h] = h2_to_f2(as_used);
-              pieces_of(as_used, c[h]);
+              const uint32_t rounded = h2_of_f2(x.x, x.y);
+              // what the products take: the pieces' sum, exact in fp32
+              p[r + h] = __ffma2_rn(h2_to_f2(pieces_of(rounded, c[h])), make_float2(-0.00390625f, -0.00390625f), h2_to_f2(rounded));
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) pw[k][r / 2] = c[0][k] | (c[1][k] << 16);
