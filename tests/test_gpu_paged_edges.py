@@ -50,3 +50,24 @@ def test_one_loud_token_among_many_small_ones(q, dtype):
         small = np.linalg.norm(ref - v[5])
         sums = L / 32 * 2.0 ** -24 * 15 * (p * vsd[:, h]).sum() * np.sqrt(d)
         assert (err <= (half + 2.0 ** -11) * np.linalg.norm(ref) + small + sums).all(), (h, err.max() / np.linalg.norm(ref))
+
+
+# ---------------------------------------------------------------- nothing to see
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("new", [None, [1, 40, 0]])
+def test_a_table_without_columns(q, hint, new):
+    """Sequences with tokens and a table that has room for none: zeros, and an error that quarot_check_error reports."""
+    lengths, N = [1, 50, 7], 3 if new is None else 41
+    cache = [torch.ones((4, 2, 16, 64), dtype=torch.uint8, device=DEV), torch.ones((4, 2, 16), dtype=FP16, device=DEV)] * 2
+    where = torch.empty((3, 0), dtype=torch.int32, device=DEV), _i32(lengths), None if new is None else _i32([0, 1, 41, 41])
+    x = torch.randn(N, 8, 128, device=DEV).half()
+    out = torch.full_like(x, 3.0)
+    q.quarot_paged_attn(x, *cache, *where, max_q=hint, out=out)
+    with pytest.raises(q.QuarotError) as e:
+        q.quarot_check_error()
+    assert e.value.status == 1 and (out == 0).all()
+    k, v = q.quarot_paged_read(*cache, *where, n=N)
+    with pytest.raises(q.QuarotError):
+        q.quarot_check_error()
+    assert (k == 0).all() and (v == 0).all()
+    q.quarot_check_error()

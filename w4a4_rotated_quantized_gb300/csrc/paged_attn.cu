@@ -1764,7 +1764,7 @@ join_units_kernel(Part part, Space ws, const int4* __restrict__ todo, int unrota
   fp8::wait_for_previous();
   for (int n = 8 * (blockIdx.y * gridDim.x + blockIdx.x) + (threadIdx.x >> 5); n < part.N; n += 8 * gridDim.x * gridDim.y) {
     const Place p = place_of(part.t, n);
-    if (p.b >= 0 && p.pos < 0)
+    if (p.b >= 0 && min(p.pos + 1, part.t.max_pages * part.t.ps) <= 0)
       for (int e = 8 * (threadIdx.x & 31); e < part.G * part.Hkv * D; e += 256)
         *reinterpret_cast<uint4*>(out + n * ld_out + e) = make_uint4(0u, 0u, 0u, 0u);
   }
