@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged_oracle as O
-from test_gpu_paged import BF16, FP16, _i32, _np
+from test_gpu_paged import BF16, FP16, Case, _check_attn, _i32, _np, _queries
 from test_gpu_parity import DEV, q  # noqa: F401  (q: fixture)
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +71,19 @@ def test_a_table_without_columns(q, hint, new):
         q.quarot_check_error()
     assert (k == 0).all() and (v == 0).all()
     q.quarot_check_error()
+
+
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e-30, 1e-35, 1e-37, 1e-38, 1e-40, 0.0])
+def test_queries_near_nothing(q, hint, d, size):
+    """bf16 queries down to the type's subnormals: all scores are 0, and a row is the mean of the values that it sees.  Between
+    them rows of ordinary size stay what they are."""
+    c = Case([300, 70], 32, 2, d, [40, 33], seed=d)
+    x = _queries(c.N, 8, d, BF16, 4)
+    x[::2] *= size
+    assert (x[::2] != 0).any() == (size > 0)
+    for un in (False, True):
+        out = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint, unrotate_out=un)
+        q.quarot_check_error()
+        _check_attn(out, x, c, unrotate=un)

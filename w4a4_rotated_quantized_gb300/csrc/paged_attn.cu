@@ -161,6 +161,7 @@ __device__ __forceinline__ uint32_t pieces_of(uint32_t a, uint32_t* c) {
 // ------------------------------------------------------------------ units
 constexpr int TILE = 128;  // tokens
 constexpr int kTries = 1 << 18;
+constexpr float kLeast = 0x1p-112f;  // a query's largest element counts as this much at least: 256 over it stays finite, and its scores are 0
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing: 2^(kNone - s) is 0
 
 // One part of a call: the shared prefix (rows of all N tokens as one list,
@@ -724,7 +725,8 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 #pragma unroll
           for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
           // pieces of x * 256 / amax: the first of up to 256, the others' sixteenths
-          const float up = amax > 0.f ? 256.0f / amax : 0.f;
+          amax = fmaxf(amax, kLeast);
+          const float up = 256.0f / amax;
           uint32_t c[E / 2][3];
           float sum = 0.f;
 #pragma unroll
@@ -1534,7 +1536,8 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         float4 all = all_four(amax, 0);
         amax = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
         // pieces of x * 256 / amax that add up to it: each of 4 bits, off by 2^-15 of the largest in the end
-        const float up = amax > 0.f ? 256.0f / amax : 0.f;
+        amax = fmaxf(amax, kLeast);
+        const float up = 256.0f / amax;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) x[i] = __fmul2_rn(x[i], make_float2(up, up));
         // their sum is what they were made from less what is left in the end
