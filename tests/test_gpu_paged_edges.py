@@ -87,3 +87,42 @@ def test_queries_near_nothing(q, hint, d, size):
         out = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint, unrotate_out=un)
         q.quarot_check_error()
         _check_attn(out, x, c, unrotate=un)
+
+
+# ---------------------------------------------------------------- loud values
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("d,new,shared", [(128, [40, 1, 70], 0), (64, [40, 1, 70], 0), (128, None, 0), (128, [9, 1, 3], 100)])
+def test_every_value_scale_counts_as_it_is(q, hint, d, new, shared):
+    """Value scales up to 65504 in many places, seen and unseen: the same outputs whatever the kernel."""
+    c = Case([300, 131, 260], 32, 2, d, new, shared, seed=d)
+    g = torch.Generator().manual_seed(1)
+    pick = torch.rand(c.cache[3].shape, generator=g).to(DEV)
+    for lo, hi, s in ((0.0, 0.02, 20000.0), (0.02, 0.03, 65504.0), (0.03, 0.04, 8188.0), (0.04, 0.05, 8192.0), (0.05, 0.06, 2.0 ** -24)):
+        c.cache[3][(pick >= lo) & (pick < hi)] = s
+    x = _queries(c.N, 8, d, BF16, 4)
+    for un in (False, True):
+        out = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint, shared_len=shared, unrotate_out=un)
+        q.quarot_check_error()
+        _check_attn(out, x, c, unrotate=un)
+        ref, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps, shared=shared, unrotate=un)
+        assert _row_errors(out, ref).max() < 2.0 ** -7  # the output's half step is 2^-8 of an element at the most
+
+
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("at", [0, 77, 199])
+def test_rows_from_a_loud_token_on_see_all_of_it(q, hint, at):
+    """A value of infinite elements, which the cache holds at its largest scale: rows from it on have that value's weight."""
+    new = 200
+    c = Case([new + 30], 32, 2, 128, [new], seed=8)
+    page, slot = int(c.table[0, (at + 30) // 32]), (at + 30) % 32
+    v = torch.randn(1, 2, 128, device=DEV).bfloat16()
+    v[:, :, 5] = float("inf")
+    q.quarot_paged_append(v, v, *c.cache, _i32(c.table), _i32([at + 31]))
+    assert (c.cache[3][page, :, slot] == 65504.0).all()
+    c.cache[1][page, :, slot] = 0.25
+    x = _queries(new, 8, 128, BF16, 3)
+    out = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    q.quarot_check_error()
+    _check_attn(out, x, c)
+    ref, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps)
+    assert _row_errors(out, ref)[at:].max() < 2.0 ** -7

@@ -1010,6 +1010,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // products; 4 x 2048 tokens: 337 us, 408 TFLOP/s.
 namespace many {
 
+constexpr uint32_t kLoud = 0x6FFF;  // 8188 in fp16
 constexpr int NT = 768, ROWS = 128, NCW = 4, NSW = 16, SP = 3, UNIT_READERS = 3 + NCW + NSW;
 constexpr uint32_t COL_Q = 0, COL_S = 128, COL_O = 384;  // S buffer b at COL_S + 128 b
 
@@ -1030,7 +1031,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_CUR + 256;
   static constexpr int NBAR = 2 * SP + 4 + 4 + 3 + 8 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 64;
+  static constexpr int SMEM = OFF_MISC + 64;  // 48 of them used
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -1150,6 +1151,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
   volatile int* there = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);      // [SP] groups of 16 tokens that a packed tile has
   volatile int* there_s = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 24);   // [2] of the score buffers; 0x100: all tokens are there
   volatile int64_t* each = reinterpret_cast<volatile int64_t*>(sm + C::OFF_MISC + 32);  // tiles of a CTA
+  volatile uint8_t* eighth = sm + C::OFF_MISC + 40;  // [2 value tiles][4] whether values of 32 tokens are an eighth
   float* ksf = reinterpret_cast<float*>(sm + C::OFF_KS);
   float* xch = reinterpret_cast<float*>(sm + C::OFF_X);
   int* cursors = reinterpret_cast<int*>(sm + C::OFF_CUR);  // [4][16]
@@ -1310,9 +1312,17 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
         tc_after();
         if (elect_one()) {
           const uint64_t vd = desc_sw128_mn(sma + C::OFF_V + (n & 1) * C::VBYTES, C::ATOM, 1024);
+          auto products = [&](int kk, bool acc) {
+            mma16_ts(tmem + COL_O, tmem + COL_S + 128 * (n & 1) + 32 * (kk >> 1) + 8 * (kk & 1), vd + 128 * kk, idesc16(D), acc);
+          };
 #pragma unroll
-          for (int kk = 0; kk < TILE / 16; ++kk)
-            mma16_ts(tmem + COL_O, tmem + COL_S + 128 * (n & 1) + 32 * (kk >> 1) + 8 * (kk & 1), vd + 128 * kk, idesc16(D), k > 0 || kk > 0);
+          for (int kk = 0; kk < TILE / 16; ++kk) products(kk, k > 0 || kk > 0);
+          const uint32_t again = *reinterpret_cast<volatile uint32_t*>(const_cast<uint8_t*>(eighth) + 4 * (n & 1));
+          if (again != 0) {  // values of an eighth eight times
+#pragma unroll 1
+            for (int kk = 0; kk < 7 * TILE / 16; ++kk)
+              if ((again >> (8 * ((kk & 7) >> 1))) & 1) products(kk & 7, true);
+          }
           mma_commit(o_done);
           mma_commit(v_empty + (n & 1));
           if (k + 1 == nt) mma_commit(unit_done);
@@ -1377,16 +1387,28 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
           if constexpr (WPT == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][2]), "=r"(w[i][3]) : "r"(at + (first ^ 8)));
         }
         uint32_t vs2[4];
+        bool loud = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 32 * cw + 8 * i + r4;
           asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(scales + 2 * TILE + 2 * t));
           const bool in = sp.t0 + t >= sp.lo && sp.t0 + t < sp.hi && ((have >> (t >> 4)) & 1);
-          half = min(half & 0x7FFFu, 0x6FFFu) | (half & 0x8000u);  // 8188: a product stays finite, as rows that do not see it need
-          vs2[i] = in ? half | (half << 16) : 0u;
+          half = in ? min(half & 0x7FFFu, 0x7BFFu) | (half & 0x8000u) : 0u;  // what is not finite counts as 65504
+          loud |= (half & 0x7FFFu) > kLoud;
+          vs2[i] = half | (half << 16);
+        }
+        // With a scale above 8188 a code times it could pass fp16's largest, and products have to stay finite for rows that
+        // do not see the token too: these 32 tokens' values are an eighth then (to 2^-25), and their products are added eight
+        // times.  (Eight times the probabilities instead: the flag comes too late, or holds the keys up; 4 x 2048 tokens 353 us
+        // and more, this way 345, scales cut off at 8188 340.)
+        const bool any = __any_sync(0xffffffffu, loud);
+        if (any) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs2[i] = hmul2(vs2[i], 0x30003000u);
         }
         arrive(raw_empty + st);
         if (n > 1) wait(v_empty + b, ((n >> 1) - 1) & 1);
+        if (lane == 0) eighth[4 * b + cw] = any;
         const uint32_t v_row = sma + C::OFF_V + b * C::VBYTES + (32 * cw + r4) * 128 + (WPT == 4 ? (c4 >> 1) * C::ATOM : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
