@@ -595,6 +595,8 @@ size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hk
  *               are read from sequence 0's pages, once for the whole batch;
  *               0: nothing is shared
  *   sm_scale    softmax scale; <= 0 selects 1/sqrt(d)
+ *               (A value scale that is not finite, which quarot_paged_append
+ *               never stores, counts as 65504.)
  *   workspace   device scratch of ws_bytes >= quarot_paged_workspace_bytes(),
  *               256-byte aligned, owned by the caller until the call is over;
  *               needs no initialisation and is clobbered

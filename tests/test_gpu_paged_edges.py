@@ -126,3 +126,26 @@ def test_rows_from_a_loud_token_on_see_all_of_it(q, hint, at):
     _check_attn(out, x, c)
     ref, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps)
     assert _row_errors(out, ref)[at:].max() < 2.0 ** -7
+
+
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_scales_that_are_not_finite(q, hint, bad):
+    """Among drafts of several tokens: rows before such a token are what they are without it; from it on a value scale counts
+    as 65504, in either kernel."""
+    c = Case([140, 37], 16, 2, 128, [12, 9], seed=3)
+    x = _queries(c.N, 8, 128, BF16, 6)
+    page, slot = int(c.table[0, 133 // 16]), 133 % 16  # position 133: rows 0 .. 4 of the first sequence are before it
+    clean = [t.clone() for t in c.cache]
+    keep = [0, 1, 2, 3, 4] + list(range(12, 21))
+    want = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    c.cache[1][page, :, slot] = c.cache[3][page, :, slot] = bad
+    got = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    assert torch.equal(got[keep], want[keep])
+    c.cache[1][page, :, slot] = clean[1][page, :, slot]
+    got = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    assert torch.equal(got[keep], want[keep])
+    c.cache[3][page, :, slot] = 65504.0
+    _check_attn(got, x, c)
+    assert torch.equal(got, q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint))
+    q.quarot_check_error()

@@ -794,6 +794,7 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
         uint32_t k_half, v_half;
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(k_half) : "r"(raw + C::CODES + 2 * tid));
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v_half) : "r"(raw + C::CODES + 2 * TILE + 2 * tid));
+        v_half = min(v_half & 0x7FFFu, 0x7BFFu) | (v_half & 0x8000u);  // what is not finite counts as 65504: times a probability of 0 it is 0
         int tok = (t_lo + it) * TILE + tid;
         const bool absent = !((there[n & 1] >> (tid >> 4)) & 1) || tok < lo || tok >= hi;
         if (it > 0) wait(bar_o, (n - 1) & 1, false);
