@@ -92,3 +92,50 @@ def attn(q, cache, table, lengths, cu, ps, shared=0, sm_scale=None, unrotate=Fal
                 t = np.full(d, np.sqrt((t * t).sum()))
             out[i, hh], tol[i, hh] = o, t
     return out, tol
+
+
+def attn_rows(q, cache, table, lengths, cu, ps, few, eps, shared=0, sm_scale=None):
+    """(norms, bounds) [N, Hq]: the norm of each row of attn(), and how far, in norm, a kernel's row may be from it, in either
+    basis.  few: up to 16 rows that see the same keys; eps: torch.finfo(output type).eps.
+
+    The output's rounding is at most half a step of each element.  Everything else is many small roundings, each anywhere
+    within its half step (its deviation a root of 3 less), whose sum is bounded by six deviations:
+      - probabilities, 2^-11 of themselves (few: of themselves times the value scale, and 2^-23 of the largest of these at
+        least; else 2^-25 of the largest), and where the rows are many also values, 2^-11;
+      - the rotated query's elements, 2^-15 of the largest one, which move all scores together;
+      - scores, 2^-22 of 15 sum|q~| times the key scale: sums in fp32 with the codes read as 0 .. 15;
+    and the outputs' sums in fp32, one for every 32 tokens, leave 2^-24 of 15 sum w an element each (all one way).
+    """
+    n, hq, d = q.shape
+    hkv = cache[0].shape[1]
+    grp, h = hq // hkv, hadamard(d)
+    sm = 1.0 / np.sqrt(d) if not sm_scale or sm_scale <= 0 else sm_scale
+    norms, bounds = np.zeros((n, hq)), np.zeros((n, hq))
+    for i, (b, pos) in enumerate(places(lengths, cu, n)):
+        if b < 0 or pos < 0:
+            continue
+        own = [tokens(cache, table[b], ps, pos + 1, w) for w in (0, 1)]
+        if shared:
+            m = min(shared, pos + 1)
+            first = [tokens(cache, table[0], ps, m, w) for w in (0, 1)]
+            own = [tuple(np.concatenate([f[j], o[j][m:]]) for j in (0, 1)) for f, o in zip(first, own)]
+        (kc, ks), (vc, vs) = own
+        qr = q[i].astype(np.float64) @ h
+        for hh in range(hq):
+            g = hh // grp
+            k, c = kc[:, g] * ks[:, g, None], vc[:, g]
+            x = sm * (k @ qr[hh])
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            w = p * vs[:, g]
+            o = w @ c
+            length2 = (c * c).sum(1)
+            least = 2.0 ** -23 * w.max() if few else 2.0 ** -25 * p.max() * vs[:, g]
+            var = ((2.0 ** -22 * w * w * (1 if few else 2) + least * least) * length2).sum()
+            pull = p[:, None] * (vs[:, g, None] * c - o)  # of a score on the output
+            var += (sm * 2.0 ** -15 * np.abs(qr[hh]).max() * np.linalg.norm(k.T @ pull)) ** 2
+            var += ((sm * 2.0 ** -22 * 15 * np.abs(qr[hh]).sum() * ks[:, g]) ** 2 * (pull * pull).sum(1)).sum()
+            norms[i, hh] = np.linalg.norm(o)
+            sums = 2.0 ** -24 * np.ceil(len(p) / 32) * 15 * w.sum() * np.sqrt(d)
+            bounds[i, hh] = eps / 2 * norms[i, hh] + 2.0 ** -25 * np.sqrt(d) + 6 * np.sqrt(var / 3) + sums
+    return norms, bounds

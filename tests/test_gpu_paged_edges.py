@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged_oracle as O
-from test_gpu_paged import BF16, FP16, Case, _check_attn, _i32, _np, _queries
+from test_gpu_paged import ATTN, BF16, FP16, Case, _check_attn, _i32, _np, _queries
 from test_gpu_parity import DEV, q  # noqa: F401  (q: fixture)
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +149,46 @@ def test_scales_that_are_not_finite(q, hint, bad):
     _check_attn(got, x, c)
     assert torch.equal(got, q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint))
     q.quarot_check_error()
+
+
+# ---------------------------------------------------------------- rows, in norm
+def _check_rows(q, c, x, hint):
+    """Both bases: rotated rows within attn_rows' bound, unrotated ones those times H but for the two outputs' roundings."""
+    both = [q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint, shared_len=c.shared, unrotate_out=un) for un in (False, True)]
+    q.quarot_check_error()
+    eps = torch.finfo(x.dtype).eps
+    kinds = [O.attn_rows(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps, few, eps, shared=c.shared)
+             for few in ([True, False] if c.shared and hint == 1 else [hint == 1])]  # a prefix may be worked on as many rows
+    ref, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps, shared=c.shared)
+    err = np.linalg.norm(_np(both[0]) - ref, axis=-1)
+    bound = np.maximum.reduce([b for _, b in kinds])
+    assert (err <= bound).all(), (float((err / bound).max()), float((err / kinds[0][0]).max()))
+    d = x.shape[-1]
+    turned = _np(both[0]) @ O.hadamard(d)
+    off = np.linalg.norm(turned - _np(both[1]), axis=-1)
+    # half a step of each, and 2^-20 for the transform in fp32
+    assert (off <= (eps + 2.0 ** -20) * np.linalg.norm(turned, axis=-1) * 1.01 + 2.0 ** -24 * np.sqrt(d)).all()
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("hint", [1, 4096])
+@pytest.mark.parametrize("lengths,new,ps,Hkv,Hq,d,shared", ATTN)
+def test_rows_in_both_bases(q, dtype, hint, lengths, new, ps, Hkv, Hq, d, shared):
+    c = Case(lengths, ps, Hkv, d, new, shared, seed=ps + Hq)
+    _check_rows(q, c, _queries(c.N, Hq, d, dtype, 5), hint)
+
+
+@pytest.mark.parametrize("hint", [1, 4096])
+@pytest.mark.parametrize("lengths,new,ps,Hkv,Hq,d,shared", [
+    ([20000, 9001], [3, 1], 64, 1, 4, 128, 0), ([33333], [2], 16, 1, 8, 64, 0), ([40000, 39000, 17000], None, 128, 1, 4, 128, 16384),
+    ([65536 + 77], None, 256, 2, 2, 64, 0), ([9000, 9100], [5, 4], 48, 1, 16, 128, 8192)])
+def test_rows_of_long_sequences(q, hint, lengths, new, ps, Hkv, Hq, d, shared):
+    c = Case(lengths, ps, Hkv, d, new, shared, seed=ps)
+    _check_rows(q, c, _queries(c.N, Hq, d, FP16, 5), hint)
+
+
+@pytest.mark.parametrize("new", [[130, 700, 3], [1000]])
+def test_rows_of_units_cut_between_ctas(q, new):
+    """More tiles than CTAs, so that units end in another CTA than they begin in: joined states beside direct results."""
+    c = Case([n + 500 for n in new], 32, 4, 64, new, seed=1)
+    _check_rows(q, c, _queries(c.N, 8, 64, FP16, 5), 4096)
