@@ -192,3 +192,111 @@ def test_rows_of_units_cut_between_ctas(q, new):
     """More tiles than CTAs, so that units end in another CTA than they begin in: joined states beside direct results."""
     c = Case([n + 500 for n in new], 32, 4, 64, new, seed=1)
     _check_rows(q, c, _queries(c.N, 8, 64, FP16, 5), 4096)
+
+
+# ---------------------------------------------------------------- as they would be used
+def test_pages_that_change_hands(q):
+    """Four slots over one pool: sequences come, decode, draft, leave; another takes the pages of the one that left."""
+    Hq, Hkv, d, ps, slots, cap = 8, 2, 128, 32, 4, 12
+    rope = q.QuarotRope(128, base=50000.0)
+    pool = q.QuarotPagedKVCache(30, Hkv, ps, d, rope=rope)
+    free, owned = list(np.random.default_rng(4).permutation(30)), [[] for _ in range(slots)]
+    lengths = np.zeros(slots, np.int64)
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    tok = lambda n, h: torch.randn(n, h, d, device=DEV, generator=gen).to(BF16)  # noqa: E731
+    held = {}  # what the pool has to hold of each slot: keys and values before they were quantized
+
+    def step(new):
+        for b, n in enumerate(new):
+            lengths[b] += n
+            while len(owned[b]) * ps < lengths[b]:
+                owned[b].append(free.pop())
+        table = np.zeros((slots, cap), np.int64)
+        for b in range(slots):
+            table[b, :len(owned[b])] = owned[b]
+        one_each = all(n == 1 or lengths[b] == 0 for b, n in enumerate(new))
+        cu = None if one_each else np.concatenate([[0], np.cumsum(new)])
+        N = slots if one_each else int(cu[-1])
+        x, k, v = tok(N, Hq), tok(N, Hkv), tok(N, Hkv)
+        where = _i32(table), _i32(lengths), None if cu is None else _i32(cu)
+        turned = pool.append(k, v, *where, q=x)
+        out = pool.attend(turned, *where, max_q=max(max(new), 1))
+        q.quarot_check_error()
+        c = Case.__new__(Case)
+        c.cache, c.table, c.lengths, c.cu, c.ps, c.shared = pool.tensors, table, lengths.copy(), cu, ps, 0
+        _check_attn(out, turned, c)
+        for i, (b, p) in enumerate(O.places(lengths, cu, N)):
+            if p < 0:
+                assert (out[i] == 0).all() and (turned[i] == 0).all()
+            else:
+                held[b, p] = k[i], v[i]
+        return where
+
+    def leave(b):
+        free.extend(owned[b])
+        owned[b], lengths[b] = [], 0
+        for key in [key for key in held if key[0] == b]:
+            del held[key]
+
+    step([70, 33, 0, 0])
+    step([1, 1, 100, 0])     # a prompt beside decoding sequences
+    step([3, 1, 2, 0])       # drafts
+    left = set(owned[0])
+    leave(0)
+    step([0, 1, 1, 0])       # one token each, an empty slot among them
+    step([0, 1, 1, 90])      # a prompt in another slot
+    assert left & set(owned[3])
+    step([0, 1, 1, 1])
+    step([64, 1, 1, 1])      # and one in the slot that was left
+    where = step([1, 1, 1, 1])
+    # what the pool holds of everyone, against the tokens themselves
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    kk, vv = pool.read(where[0], where[1], _i32(cu), n=int(cu[-1]), unrotate=True, out_dtype=BF16)
+    assert len(held) == cu[-1]
+    for i, (b, p) in enumerate(O.places(lengths, cu, int(cu[-1]))):
+        k, v = (_np(t)[None] for t in held[b, p])
+        for got, want in ((kk[i], O.rope(k, [p], _np(rope.inv_freq))[0]), (vv[i], v[0])):
+            # rotated elements are off by half a scale, a 14th of the largest one; the rotation keeps the norm; bf16 out
+            scale = np.abs(want @ O.hadamard(d)).max(-1) / 7
+            err, norm = np.linalg.norm(_np(got) - want, axis=-1), np.linalg.norm(want, axis=-1)
+            assert (err <= (np.sqrt(d) * scale / 2 + norm * 2.0 ** -8) * 1.01).all()
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_of_edge_values(q, dtype, d):
+    """The type's largest and smallest values, zeros, one loud element; beside them an infinite and a NaN element, whose
+    vectors get a finite scale and leave the other heads alone."""
+    H, n = 2, 8
+    big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).tiny
+    k = torch.zeros(n, H, d, dtype=torch.float64)
+    k[1] = min(big, 1e30)
+    k[2, :, 5] = 65504.0
+    k[3] = -tiny
+    k[4, 1] = torch.linspace(-3, 3, d)
+    k[5, 0, 3], k[5, 1] = float("inf"), torch.linspace(-3, 3, d)
+    k[6, 0, 9], k[6, 1] = float("nan"), torch.linspace(-3, 3, d)
+    k[7] = torch.linspace(2.0 ** -14, 2.0 ** -13, d)
+    k = k.to(dtype).to(DEV)
+    c = Case([n], 16, H, d, [n])
+    q.quarot_paged_append(k, k, *c.cache, *c.where)
+    q.quarot_check_error()
+    cache, x, h = c.np_cache(), _np(k), O.hadamard(d)
+    for which in (0, 1):
+        code, s = (a[c.table[0, 0]][:, :n] for a in (cache[2 * which], cache[2 * which + 1].astype(np.float64)))
+        assert np.isfinite(s).all() and (s > 0).all()
+        code = O.codes(code)
+        for i in range(n):
+            for hh in range(H):
+                if not np.isfinite(x[i, hh]).all():
+                    continue
+                y = x[i, hh] @ h
+                top = np.abs(y).max()
+                want = min(max(top, 1e-5) / 7, 65504.0)
+                own = np.abs(x[i, hh]).sum() / np.sqrt(d) * (5 + np.log2(d)) * 2.0 ** -24  # as for ordinary values
+                assert abs(s[hh, i] - want) <= want * 2.0 ** -11 + 2.0 ** -25 + own / 7
+                near = np.clip(y / s[hh, i], -8, 7)
+                assert (np.abs(code[hh, i] - near) <= 0.5 + 2.0 ** -12 + own / s[hh, i]).all()
+        assert (code[1, 5] == code[1, 4]).all() and (code[1, 6] == code[1, 4]).all()
+        assert s[1, 5] == s[1, 4] == s[1, 6]
+    assert (cache[0][c.table[0, 0]][:, 0] == 0).all()
