@@ -1090,12 +1090,16 @@ class QuarotRope:
                  low_freq: float = 1.0, high_freq: float = 4.0, device=None):
         if rot <= 0 or rot % 16:
             raise QuarotError(2, f"{rot} rotated elements: a multiple of 16 is needed")
-        if not base > 1.0 or not factor >= 1.0:
+        if not 1.0 < base < math.inf or not 1.0 <= factor < math.inf:
             raise QuarotError(1, "base must be above 1 and factor at least 1")
         if scaling not in (None, "linear", "ntk", "yarn", "smooth"):
             raise QuarotError(1, f"unknown scaling {scaling!r}")
         if scaling in ("yarn", "smooth") and not (original_len or 0) > 0:
             raise QuarotError(1, f"{scaling} needs original_len")
+        if scaling == "yarn" and not 0.0 < beta_slow <= beta_fast < math.inf:
+            raise QuarotError(1, "yarn needs 0 < beta_slow <= beta_fast")
+        if scaling == "smooth" and not 0.0 < low_freq < high_freq < math.inf:
+            raise QuarotError(1, "smooth needs 0 < low_freq < high_freq")
         if scaling == "ntk":
             base = base * factor ** (rot / (rot - 2))
         i = torch.arange(rot // 2, dtype=torch.float64)
