@@ -300,3 +300,13 @@ def test_append_of_edge_values(q, dtype, d):
         assert (code[1, 5] == code[1, 4]).all() and (code[1, 6] == code[1, 4]).all()
         assert s[1, 5] == s[1, 4] == s[1, 6]
     assert (cache[0][c.table[0, 0]][:, 0] == 0).all()
+
+
+def test_read_refuses_numbers_of_tokens(q):
+    """Before anything is allocated."""
+    c = Case([5, 9], 16, 2, 64, [2, 3])
+    for n, status in ((-1, 1), (-2 ** 40, 1), (2 ** 24 + 1, 2), (2 ** 40, 2)):
+        with pytest.raises(q.QuarotError) as e:
+            q.quarot_paged_read(*c.cache, *c.where, n=n)
+        assert e.value.status == status
+    assert q.quarot_paged_read(*c.cache, *c.where, n=0)[0].shape == (0, 2, 64)

@@ -1014,6 +1014,8 @@ def quarot_paged_read(k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, n=None
         if cu_q is not None:
             raise QuarotError(1, "n is needed with cu_q")
         n = B
+    if not 0 <= n <= 1 << 24:
+        raise QuarotError(1 if n < 0 else 2, f"n is {n}")
     if out_dtype not in _DTYPES:
         raise QuarotError(1, "out_dtype must be float16 or bfloat16")
     shape = (int(n), H, d)
