@@ -310,3 +310,12 @@ def test_read_refuses_numbers_of_tokens(q):
             q.quarot_paged_read(*c.cache, *c.where, n=n)
         assert e.value.status == status
     assert q.quarot_paged_read(*c.cache, *c.where, n=0)[0].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("hint", [1, 4096])
+@pytest.mark.parametrize("lengths,new,ps,Hkv,Hq,d,shared", [
+    ([500, 100, 399, 400, 401, 0], None, 32, 2, 8, 128, 400), ([500, 100, 399, 400, 401], [3, 9, 1, 2, 30], 16, 2, 8, 64, 400),  # shorter than the prefix
+    ([300, 77], [2, 1], 16, 1, 33, 128, 0), ([200, 5], None, 16, 1, 160, 64, 0), ([130], [2], 32, 1, 1024, 64, 100)])  # groups wider than a tile
+def test_rows_of_short_sequences_and_wide_groups(q, hint, lengths, new, ps, Hkv, Hq, d, shared):
+    c = Case(lengths, ps, Hkv, d, new, shared, seed=Hq)
+    _check_rows(q, c, _queries(c.N, Hq, d, FP16, 5), hint)
