@@ -592,8 +592,10 @@ size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hk
  *   max_q       the most new tokens that a sequence has (a hint that chooses
  *               the kernel: any value > 0 gives right results)
  *   shared_len  tokens 0 .. shared_len - 1 of all sequences are the same and
- *               are read from sequence 0's pages, once for the whole batch;
- *               0: nothing is shared
+ *               are read from sequence 0's pages: once for the whole batch
+ *               where min(max_q, N) Hq / Hkv is at most 16 (one token, drafts
+ *               of a few), else once a sequence and 128 rows; 0: nothing is
+ *               shared
  *   sm_scale    softmax scale; <= 0 selects 1/sqrt(d)
  *               (A value scale that is not finite, which quarot_paged_append
  *               never stores, counts as 65504.)

@@ -1042,7 +1042,9 @@ def quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q=None, max
     sequence up to itself -> out [N, Hq, d].  page_table, lengths, cu_q as in
     quarot_paged_append; max_q: the most new tokens of a sequence, where known
     (it chooses the kernel); the first shared_len tokens of all sequences are
-    the same: they are read from the first sequence's pages, once for all."""
+    the same: they are read from the first sequence's pages, once for all
+    where max_q times the heads of a group is at most 16, else once a sequence
+    and 128 rows."""
     if stream is not None:
         with _on(stream, q):
             return quarot_paged_attn(q, k_q, k_s, v_q, v_s, page_table, lengths, cu_q, max_q, shared_len, sm_scale,

@@ -43,8 +43,8 @@ __device__ __forceinline__ Place place_of(const Batch& t, int n) {
   return p;
 }
 
-// Page and slot of position pos >= 0 of sequence b, as a row of [n_pages * ps];
-// -1 (and an error for quarot_check_error) where the table has no page for it.
+// The index-th page of sequence b; -1 (and an error for quarot_check_error)
+// where the table has none.
 __device__ __forceinline__ int page_at(const Batch& t, int b, int index) {
   const int page = index < t.max_pages ? t.table[int64_t(b) * t.max_pages + index] : -1;
   if (page >= 0 && page < t.n_pages) return page;

@@ -1001,9 +1001,9 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // What bounds it: the hand-overs between these roles.  A tile takes some 2800
 // clocks.  The MMAs need 1350 of them (12 of 128 x 128 x 32 for S and 8 of
 // 128 x 128 x 16 for P V, each of the two after what it waits for), the
-// converters 1600 busy and four waits, the softmax 2100 busy and two waits; with
-// no one of the three does it take more than a tenth less (256 sequences sharing
-// 32768 tokens: no exponentials 0, a third of the MMAs 0, no conversion 9 %).
+// converters 1600 busy and four waits, the softmax 2100 busy and two waits.  256
+// sequences sharing 32768 tokens take 19 % less without the softmax, 9 % without
+// the conversion, and nothing less without the exponentials or a third of the MMAs.
 // Two score buffers are what tensor memory has room for.  A unit's start and end
 // cost some 14000 clocks more, of which the tensor cores wait for 8000: queries
 // rotated and split (e4m3 conversions run at a few lanes a clock), outputs
@@ -2039,8 +2039,15 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
 // ------------------------------------------------------------------ host
 // Which kernel a part gets, by the rows that see the same keys: up to 16, the
 // tokens as the MMA's M (each 4, 8 or 16 rows read the keys once); above, the
-// rows (64 sequences sharing 8000 tokens: 92 us and 46 us).  Sequences of more new rows than that are worked on whole, the shared
-// tokens with their own: the keys are read for every 128 rows anyway.
+// rows (64 sequences sharing 8000 tokens, 256 rows: 92 us and 46 us).  For 16
+// sequences of 4096 tokens and 8 key heads, whatever the group, and heads of 64 alike:
+//   rows a sequence and key head    20    32    64   128
+//   tokens as M, 16 rows a pass    59.3  63.2 113.3 212.9 us
+//   rows as M                      79.0  79.1  79.4  62.9 us
+// so from 17 to some 40 rows (drafts) the first would still be faster.
+// Sequences of more than 16 new rows are worked on whole, the shared tokens with
+// their own: from 128 rows on the keys are read for every 128 of them anyway;
+// below, each sequence reads the prefix for itself.
 struct Plan {
   bool many;
   int RP, ctas;

@@ -129,9 +129,10 @@ rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ posi
 // As in quarot_kv_write, d / 32 lanes own one (token, head) vector, 32
 // elements each.  A CTA takes some neighbouring tokens' keys, values or
 // queries, so that places are looked up and angles made once for all heads.
-// Bound by issue (keys and values: rotation and quantizer) and HBM (queries): 4 x
-// 2048 tokens of 32 + 8 + 8 heads of 128 43 us; 16 x 1 4.4 us, a launch and its
-// look-ups.
+// Bound by latency: with 80 registers a thread a third of the warps are there to
+// cover loads, shuffles and the quantizer's chain, and neither issue (55 % of the
+// clocks) nor HBM (32 %) is full.  4 x 2048 tokens of 32 + 8 + 8 heads of 128 43 us;
+// 16 x 1 4.4 us, a launch and its look-ups.
 constexpr int ATOK = 32;      // most tokens of a CTA
 constexpr int AHALF = 64;     // most pairs of a head
 constexpr int CU = 257;       // entries of cu that a CTA keeps at hand
@@ -157,8 +158,8 @@ append_kernel(Heads k, Heads v, Heads q, int64_t N, const double* __restrict__ i
   __shared__ uint64_t step[AHALF];
   __shared__ int row[ATOK], posn[ATOK], skip[ATOK];
   __shared__ int cu[CU];
-  // CTAs of keys, values and queries in turn, as long as there are all of them: the former are bound by issue, the
-  // latter by memory (4 x 2048 tokens, with reading back: queries first 59.9 us, in turn 52.4 us)
+  // CTAs of keys, values and queries in turn, as long as there are all of them: the former mostly compute, the
+  // latter mostly move memory (4 x 2048 tokens, with reading back: queries first 59.9 us, in turn 52.4 us)
   const int m = min(kv_blocks, int(gridDim.x) - 2 * kv_blocks), b = int(blockIdx.x);
   const int which = b < 3 * m ? b % 3 : m < kv_blocks ? (b - 3 * m) & 1 : 2;
   int64_t blk = b < 3 * m ? b / 3 : m < kv_blocks ? m + ((b - 3 * m) >> 1) : b - 2 * m;
