@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged_oracle as O
-from test_gpu_paged import ATTN, BF16, FP16, Case, _check_attn, _i32, _np, _queries
+from test_gpu_paged import ATTN, BF16, FP16, Case, _check_attn, _i32, _np, _queries, _raw
 from test_gpu_parity import DEV, q  # noqa: F401  (q: fixture)
 
 pytestmark = pytest.mark.gpu
@@ -319,3 +319,52 @@ def test_read_refuses_numbers_of_tokens(q):
 def test_rows_of_short_sequences_and_wide_groups(q, hint, lengths, new, ps, Hkv, Hq, d, shared):
     c = Case(lengths, ps, Hkv, d, new, shared, seed=Hq)
     _check_rows(q, c, _queries(c.N, Hq, d, FP16, 5), hint)
+
+
+@pytest.mark.parametrize("Hq", [0, 2])
+def test_quotients_of_a_half_go_to_the_even_code(q, Hq):
+    """Codes of bf16 values with heads of 64, whose transform is exact in fp32 and whose quotients meet a half again and
+    again; and of keys that are turned by nothing (position 0), so that they go through the turn as they are."""
+    d, H, n, ps = 64, 8, 8192, 64
+    gen = torch.Generator().manual_seed(11)
+    v = torch.randn((n, H, d), generator=gen)
+    v[..., 7] *= 20
+    v = v.to(BF16).to(DEV)
+    table = torch.randperm(n, generator=gen).to(torch.int32)[:, None].to(DEV)  # a page a sequence
+    cache = [torch.zeros((n, H, 16, d // 2), dtype=torch.uint8, device=DEV), torch.zeros((n, H, 16), dtype=FP16, device=DEV)]
+    cache += [torch.zeros_like(t) for t in cache]
+    f = torch.full((16,), 0.25, dtype=torch.float64, device=DEV) if Hq else None
+    ones = torch.ones(n, dtype=torch.int32, device=DEV)
+    q.quarot_paged_append(v, v, *cache, table, ones, inv_freq=f)
+    q.quarot_check_error()
+    h = torch.from_numpy(O.hadamard(d)).to(DEV)
+    y = v.double() @ h
+    met = 0
+    for which in (0, 1):
+        code, s = cache[2 * which][table[:, 0].long(), :, 0], cache[2 * which + 1][table[:, 0].long(), :, 0]
+        code = torch.from_numpy(O.codes(_raw(code))).to(DEV)
+        u = y / s.double()[..., None]
+        want = u.round().clamp(-8, 7)  # half to even
+        # fp32 leaves 2^-18 of a step where the transform is not exact
+        sure = ((u - u.floor() - 0.5).abs() > 2.0 ** -18) | (u - u.floor() == 0.5)
+        met += int((u - u.floor() == 0.5).sum())
+        wrong = (code != want) & sure
+        assert not wrong.any(), (which, int(wrong.sum()), int(((code != want) & ~sure).sum()))
+    assert met > 10
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_unturned_fp16_vectors_are_quarot_kv_writes(q, d):
+    """17 million codes and more, bit for bit."""
+    B, T, H, ps = 4, 2048, 8, 64
+    table = torch.arange(B * T // ps, dtype=torch.int32, device=DEV).view(B, -1)
+    for seed in range(2048 * 128 // (T * d)):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        k, v = (torch.randn(B, T, H, d, device=DEV, generator=g).half() for _ in range(2))
+        flat = q.new_kv_cache(B, H, T, d, torch.device(DEV))
+        q.quarot_kv_write(k, v, 0, *flat)
+        pool = [torch.zeros((B * T // ps, H, ps) + a.shape[3:], dtype=a.dtype, device=DEV) for a in flat]
+        q.quarot_paged_append(k.view(-1, H, d), v.view(-1, H, d), *pool, table, _i32([T] * B), _i32(np.arange(B + 1) * T))
+        for a, p in zip(flat, pool):
+            assert torch.equal(p.view((B, T // ps, H, ps) + a.shape[3:]).movedim(2, 1).flatten(2, 3), a)
+    q.quarot_check_error()
