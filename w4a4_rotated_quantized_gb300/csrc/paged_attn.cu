@@ -1007,8 +1007,8 @@ few_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k_
 // Two score buffers are what tensor memory has room for.  A unit's start and end
 // cost some 14000 clocks more, of which the tensor cores wait for 8000: queries
 // rotated and split (e4m3 conversions run at a few lanes a clock), outputs
-// rotated back.  256 sharing 32768: 200 us, 687 TFLOP/s of the formula's
-// products; 4 x 2048 tokens: 337 us, 408 TFLOP/s.
+// rotated back.  256 sharing 32768: 198 us, 697 TFLOP/s of the formula's
+// products; 4 x 2048 tokens: 344 us, 400 TFLOP/s.
 namespace many {
 
 constexpr uint32_t kLoud = 0x6FFF;  // 8188 in fp16

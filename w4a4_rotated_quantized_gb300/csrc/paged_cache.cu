@@ -133,8 +133,8 @@ rope_kernel(Heads q, Heads k, int64_t N, int d, const int32_t* __restrict__ posi
 // queries, so that places are looked up and angles made once for all heads.
 // Bound by latency: with 80 registers a thread a third of the warps are there to
 // cover loads, shuffles and the quantizer's chain, and neither issue (55 % of the
-// clocks) nor HBM (32 %) is full.  4 x 2048 tokens of 32 + 8 + 8 heads of 128 43 us;
-// 16 x 1 4.4 us, a launch and its look-ups.
+// clocks) nor HBM (31 %) is full.  4 x 2048 tokens of 32 + 8 + 8 heads of 128 44 us;
+// 16 x 1 4.1 us, a launch and its look-ups.
 constexpr int ATOK = 32;      // most tokens of a CTA
 constexpr int AHALF = 64;     // most pairs of a head
 constexpr int CU = 257;       // entries of cu that a CTA keeps at hand
