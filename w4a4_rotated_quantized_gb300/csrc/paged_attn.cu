@@ -1742,7 +1742,7 @@ many_kernel(const T* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ k
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = fp8::from_f2<T>(make_float2(x[8 * c + i].x * sc, x[8 * c + i].y * sc));
-            if (((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld_out * 2)) & 31) == 0) {  // whole sectors (4 x 2048 tokens: 337 us, 343 us without)
+            if (((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld_out * 2)) & 31) == 0) {  // whole sectors (4 x 2048 tokens: 346 us, 352 us without)
               asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * c), "r"(o[0]), "r"(o[1]),
                            "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
                            : "memory");
@@ -2039,7 +2039,8 @@ join_kernel(Part own, Space so, Part pre, Space sp, int Hq, int unrotate, T* __r
 // ------------------------------------------------------------------ host
 // Which kernel a part gets, by the rows that see the same keys: up to 16, the
 // tokens as the MMA's M (each 4, 8 or 16 rows read the keys once); above, the
-// rows (64 sequences sharing 8000 tokens, 256 rows: 92 us and 46 us).  For 16
+// rows (64 sequences sharing 8000 tokens, 256 rows: 96 us and 46 us; 256 sharing
+// 32768: 728 and 202 us; 4 x 2048 new tokens: 2195 and 346 us).  For 16
 // sequences of 4096 tokens and 8 key heads, whatever the group, and heads of 64 alike:
 //   rows a sequence and key head    20    32    64   128
 //   tokens as M, 16 rows a pass    59.3  63.2 113.3 212.9 us
@@ -2134,8 +2135,8 @@ static int attn_impl(const T* q, int64_t ld_q, const uint8_t* k_q, const __half*
   pre.RP = pp.RP;
   if (call.prefix && (rc = pp.many ? many_part(pre, pp, sp, nullptr) : few_part(pre, pp, sp, 0)) != QUAROT_OK) return rc;
   if ((rc = few_part(own, po, so, call.prefix)) != QUAROT_OK) return rc;
-  // a warp a row and a CTA a row: 256 sequences sharing 32768 tokens (8192 rows) 211 and 242 us, 64 sharing 8000 (2048
-  // rows) 46 and 53 us, 16 x 4096 (512) 26.3 and 25.6 us, 1 x 4097 (32) 15.4 and 10.3 us
+  // a warp a row and a CTA a row: 256 sequences sharing 32768 tokens (8192 rows) 202 and 232 us, 64 sharing 8000 (2048
+  // rows) 46 and 52 us, 16 x 4096 (512) 27.5 and 26.7 us, 1 x 4097 (32) 15.3 and 10.1 us
   const unsigned rows = unsigned(own.N) * unsigned(Hq);
   if (rows > 1024)
     return fp8::launch_dependent(join_rows_kernel<T, D>, dim3((rows + 7) / 8), 256, 0, 1, st, own, so, pre, sp, Hq, unrotate, out,
