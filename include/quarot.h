@@ -598,7 +598,9 @@ size_t quarot_paged_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hk
  *               shared
  *   sm_scale    softmax scale; <= 0 selects 1/sqrt(d)
  *               (A value scale that is not finite, which quarot_paged_append
- *               never stores, counts as 65504.)
+ *               never stores, counts as 65504.  Where more than 16 query rows
+ *               see the same keys, values are fp16; those of 32 neighbouring
+ *               tokens of which one has a scale above 8188 are held to 2^-22.)
  *   workspace   device scratch of ws_bytes >= quarot_paged_workspace_bytes(),
  *               256-byte aligned, owned by the caller until the call is over;
  *               needs no initialisation and is clobbered

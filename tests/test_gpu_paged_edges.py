@@ -368,3 +368,27 @@ def test_unturned_fp16_vectors_are_quarot_kv_writes(q, d):
         for a, p in zip(flat, pool):
             assert torch.equal(p.view((B, T // ps, H, ps) + a.shape[3:]).movedim(2, 1).flatten(2, 3), a)
     q.quarot_check_error()
+
+
+@pytest.mark.parametrize("hint", [1, 1000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_values_beside_a_loud_one(q, hint, d):
+    """Values of 10^-5 and a token at the largest scale among them: rows that do not see it are right to 2^-22, beside the
+    roundings of probabilities, values (2^-11 each) and of the output; those further on than its 32 tokens' group and
+    before it have no more than these."""
+    new, at = 200, 101  # the group: tokens 96 .. 127
+    c = Case([new], 32, 2, d, [new], seed=d)
+    g = torch.Generator().manual_seed(7)
+    c.cache[3][:] = torch.exp(torch.rand(c.cache[3].shape, generator=g) * 3 - 13.4).half().to(DEV)  # from append's smallest scale up
+    x = _queries(new, 8, d, BF16, 3)
+    want = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    ref, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps)
+    top = float(8 * c.cache[3].max())
+    c.cache[3][int(c.table[0, at // 32]), :, at % 32] = 65504.0
+    got = q.quarot_paged_attn(x, *c.cache, *c.where, max_q=hint)
+    q.quarot_check_error()
+    assert torch.equal(got[:96], want[:96])
+    err = np.abs(_np(got)[:at] - ref[:at])
+    assert (err <= 2.0 ** -22 + 2.0 ** -10 * top + np.abs(ref[:at]) * 2.0 ** -8).all(), err.max()
+    loud, _ = O.attn(_np(x), c.np_cache(), c.table, c.lengths, c.cu, c.ps)
+    assert _row_errors(got, loud)[at:].max() < 2.0 ** -7
